@@ -13,6 +13,11 @@ __all__ = [
     "dora_magnitude_scale",
     "dora_norm_workspace_size",
     "dora_norm_chunk_size",
+    "dora_rms_norm",
+    "dora_rms_norm_quant",
+    "dora_rms_norm_backward",
+    "dora_matmul",
+    "dora_matmul_backward",
 ]
 
 

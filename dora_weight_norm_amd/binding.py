@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -40,6 +41,16 @@ __all__ = [
     "dora_factored_norm_marked",
     "dora_factored_norm_noalloc",
     "NOALLOC_SCRATCH_BYTES",
+    "DORA_E4M3",
+    "ACTS",
+    "dora_rms_norm",
+    "dora_rms_norm_quant",
+    "dora_rms_norm_backward",
+    "dora_rms_norm_backward_workspace_size",
+    "dora_matmul",
+    "dora_matmul_workspace_size",
+    "dora_matmul_backward",
+    "dora_matmul_backward_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdora.so")
@@ -47,6 +58,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdora.so"
 DORA_BF16 = 0
 DORA_F32 = 1
 DORA_F16 = 2
+DORA_E4M3 = 3   # 8-bit operands of dora_matmul only
 DEFAULT_BUDGET = 256 << 20
 NOALLOC_SCRATCH_BYTES = 32 << 20   # DORA_NOALLOC_SCRATCH_BYTES
 
@@ -103,6 +115,16 @@ def load():
         "dora_compose_backward_workspace_size": (_c_i, [_c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
         "dora_compose_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_f, _c_i, _c_i64, _c_i64, _c_p, _c_p, _c_p,
                                          _c_p, _c_f, _c_p, _c_p, _c_sz, _c_p]),
+        "dora_rms_norm": (_c_i, [_c_p, _c_p, _c_p, _c_f, _c_i, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+        "dora_rms_norm_backward_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i, ctypes.POINTER(_c_sz)]),
+        "dora_rms_norm_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_p, _c_p, _c_p,
+                                          _c_sz, _c_p]),
+        "dora_matmul_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i, _c_i, ctypes.POINTER(_c_sz)]),
+        "dora_matmul": (_c_i, [_c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_f, _c_p,
+                               _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+        "dora_matmul_backward_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, ctypes.POINTER(_c_sz)]),
+        "dora_matmul_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i, _c_p,
+                                        _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -414,3 +436,290 @@ def dora_compose_backward(dy, base, lora, g, s: float, need_dg: bool = True, wno
               _ptr(g), s, dt, T, d_out, _ptr(d_base), _ptr(d_lora), _ptr(dg), _ptr(wnorm), eps, _ptr(dm),
               _ptr(workspace), ws_bytes if workspace is not None else 0, _stream(stream))
     return d_base, d_lora, dg, dm
+
+
+# ---------------------------------------------------------------------------
+# The block around the adapted layer: residual RMS norm and matrix product.
+# ---------------------------------------------------------------------------
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_TORCH_DT = {torch.bfloat16: DORA_BF16, torch.float32: DORA_F32, torch.float16: DORA_F16}
+_E4M3 = torch.float8_e4m3fn
+
+
+def _want(t, name: str, shape, dtype, device):
+    """`t` is a contiguous tensor of exactly this shape, dtype and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _first(t, name: str, dims: int = 2):
+    """The tensor a call takes its shapes, dtype and device from."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    if t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and {dims}-D, got {tuple(t.shape)}")
+
+
+def _vec(t, name: str, n: int, device):
+    if t is not None:
+        _want(t, name, (n,), torch.float32, device)
+
+
+def _new(shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=4096)
+def _size_of(name: str, *args) -> int:
+    """A workspace query; a pure function of its arguments."""
+    ws = _c_sz()
+    _call(name, *args, ctypes.byref(ws))
+    return ws.value
+
+
+def dora_rms_norm_backward_workspace_size(T: int, d: int, dtype) -> int:
+    return _size_of("dora_rms_norm_backward_workspace_size", T, d, _dtype_code(dtype))
+
+
+def dora_matmul_workspace_size(M: int, N: int, K: int, r: int, dtype, aligned_operands: int = 15) -> int:
+    code = DORA_E4M3 if dtype in (_E4M3, "e4m3", DORA_E4M3) else _dtype_code(dtype)
+    return _size_of("dora_matmul_workspace_size", M, N, K, r, code, aligned_operands)
+
+
+def dora_matmul_backward_workspace_size(M: int, N: int, K: int, dtype, outputs: int = 15) -> int:
+    """`outputs`: the sum of GRAD_DX, GRAD_DW, GRAD_SUMS and GRAD_DU that apply."""
+    return _size_of("dora_matmul_backward_workspace_size", M, N, K, _dtype_code(dtype), outputs)
+
+
+def _rms_norm(x, weight, eps, residual, h, rstd, want_rstd, stream, y=None, q=None, scale=None, quant=False):
+    _first(x, "x")
+    dt = _TORCH_DT.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {x.dtype}; libdora takes bfloat16, float16 or float32")
+    shape, dev = x.shape, x.device
+    T, d = shape
+    _vec(weight, "weight", d, dev)
+    if residual is not None:
+        _want(residual, "residual", shape, x.dtype, dev)
+        if h is not None:
+            _want(h, "h", shape, x.dtype, dev)
+    elif h is not None:
+        raise ValueError("h needs a residual (without one, h is x)")
+    _vec(rstd, "rstd", T, dev)
+    if quant:
+        if q is not None:
+            _want(q, "q", shape, _E4M3, dev)
+        _vec(scale, "scale", T, dev)
+    elif y is not None:
+        _want(y, "y", shape, x.dtype, dev)
+    with _on(stream):
+        if residual is not None and h is None:
+            h = _new(shape, x.dtype, dev)
+        if rstd is None and want_rstd:
+            rstd = _new((T,), torch.float32, dev)
+        if quant:
+            q = _new(shape, _E4M3, dev) if q is None else q
+            scale = _new((T,), torch.float32, dev) if scale is None else scale
+        else:
+            y = _new(shape, x.dtype, dev) if y is None else y
+        _call("dora_rms_norm", _addr(x), _addr(residual), _addr(weight), eps, dt, T, d, _addr(h), _addr(y), _addr(q),
+              _addr(scale), _addr(rstd), _raw_stream(stream, dev))
+    return y, q, scale, (x if residual is None else h), rstd
+
+
+def dora_rms_norm(x, weight, eps: float, residual=None, y=None, h=None, rstd=None, want_rstd: bool = True,
+                  stream=None):
+    """y = h * rstd * weight with h = x + residual and rstd = 1 / sqrt(mean h^2 + eps) over each row.
+
+    x, residual [T, d] of one dtype (bfloat16, float16 or float32), weight
+    float32 [d] or None. Returns (y, h, rstd): h is x itself without a
+    residual; rstd float32 [T] (None with want_rstd False).
+    """
+    y, _, _, h, rstd = _rms_norm(x, weight, eps, residual, h, rstd, want_rstd, stream, y=y)
+    return y, h, rstd
+
+
+def dora_rms_norm_quant(x, weight, eps: float, residual=None, q=None, scale=None, h=None, rstd=None,
+                        want_rstd: bool = True, stream=None):
+    """dora_rms_norm with its output in 8 bits: q float8_e4m3fn [T, d] and scale
+    float32 [T], the row's largest |value| / 448. Returns (q, scale, h, rstd)."""
+    _, q, scale, h, rstd = _rms_norm(x, weight, eps, residual, h, rstd, want_rstd, stream, q=q, scale=scale,
+                                     quant=True)
+    return q, scale, h, rstd
+
+
+def dora_rms_norm_backward(dy, h, rstd, weight, dh=None, need_dweight: bool = True, dx=None, dweight=None,
+                           workspace=None, stream=None):
+    """Gradients of dora_rms_norm from its h and rstd. Returns (dx, dweight):
+    dx is the gradient of x and of the residual, dh (optional) what reaches h
+    directly is added to it; dweight float32 [d], None if not needed."""
+    _first(dy, "dy")
+    dt = _TORCH_DT.get(dy.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {dy.dtype}; libdora takes bfloat16, float16 or float32")
+    shape, dev = dy.shape, dy.device
+    T, d = shape
+    _want(h, "h", shape, dy.dtype, dev)
+    _want(rstd, "rstd", (T,), torch.float32, dev)
+    _vec(weight, "weight", d, dev)
+    if dh is not None:
+        _want(dh, "dh", shape, dy.dtype, dev)
+    if dx is not None:
+        _want(dx, "dx", shape, dy.dtype, dev)
+    if dweight is not None:
+        if not need_dweight:
+            raise ValueError("dweight given but need_dweight is False")
+        _vec(dweight, "dweight", d, dev)
+    need = dora_rms_norm_backward_workspace_size(T, d, dt) if need_dweight else 0
+    if workspace is not None:
+        _workspace(workspace, "workspace", need, dev)
+    with _on(stream):
+        dx = _new(shape, dy.dtype, dev) if dx is None else dx
+        if need_dweight and dweight is None:
+            dweight = _new((d,), torch.float32, dev)
+        if workspace is None and need > 0:
+            workspace = _new((need,), torch.uint8, dev)
+        _call("dora_rms_norm_backward", _addr(dy), _addr(dh), _addr(h), _addr(rstd), _addr(weight), dt, T, d,
+              _addr(dx), _addr(dweight), _addr(workspace), need, _raw_stream(stream, dev))
+    return dx, dweight
+
+
+def _act(act) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def dora_matmul(x, w, row_scale=None, col_scale=None, t=None, b=None, s: float = 1.0, bias=None, act: str = "none",
+                residual=None, out_dtype=None, save: bool = False, y=None, u=None, workspace=None, stream=None):
+    """y = act(col_scale * u + bias) + residual with u = row_scale * (x w^T) + s * (t b^T).
+
+    x [M, K] and w [N, K] of one dtype (bfloat16, float16, float32 or
+    float8_e4m3fn); t [M, r] and b [N, r] of the same dtype, both or neither
+    (neither with float8); row_scale float32 [M]; col_scale, bias float32 [N];
+    residual [M, N] of the output's dtype. out_dtype is x's, and for float8
+    one of the other three (default bfloat16). act: none, relu, gelu,
+    gelu_tanh or silu. Returns (y, u); u, the product that the backward
+    takes, is None unless `save` (or a buffer for it) is given.
+    """
+    _first(x, "x")
+    e8 = x.dtype == _E4M3
+    dt = DORA_E4M3 if e8 else _TORCH_DT.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {x.dtype}; libdora takes bfloat16, float16, float32 or float8_e4m3fn")
+    dev = x.device
+    M, K = x.shape
+    _first(w, "w")
+    N = w.shape[0]
+    _want(w, "w", (N, K), x.dtype, dev)
+    odt = out_dtype if out_dtype is not None else (torch.bfloat16 if e8 else x.dtype)
+    oc = _TORCH_DT.get(odt)
+    if oc is None or (not e8 and odt != x.dtype):
+        raise TypeError(f"out_dtype {odt} does not go with {x.dtype}")
+    r = 0
+    if t is not None or b is not None:
+        if t is None or b is None:
+            raise ValueError("t and b come together")
+        if e8:
+            raise TypeError("a low-rank pair does not go with float8 operands")
+        _first(t, "t")
+        r = t.shape[1]
+        _want(t, "t", (M, r), x.dtype, dev)
+        _want(b, "b", (N, r), x.dtype, dev)
+    if row_scale is not None:
+        _want(row_scale, "row_scale", (M,), torch.float32, dev)
+    _vec(col_scale, "col_scale", N, dev)
+    _vec(bias, "bias", N, dev)
+    if residual is not None:
+        _want(residual, "residual", (M, N), odt, dev)
+    if y is not None:
+        _want(y, "y", (M, N), odt, dev)
+    if u is not None:
+        _want(u, "u", (M, N), odt, dev)
+    code = _act(act)
+    px, pw, pt, pb = x.data_ptr(), w.data_ptr(), _addr(t), _addr(b)
+    al = ((px & 15) == 0) | ((pw & 15) == 0) << 1
+    if r:
+        al |= ((pt & 15) == 0) << 2 | ((pb & 15) == 0) << 3
+    need = _size_of("dora_matmul_workspace_size", M, N, K, r, dt, al)
+    if workspace is not None:
+        _workspace(workspace, "workspace", need, dev)
+    with _on(stream):
+        y = _new((M, N), odt, dev) if y is None else y
+        if u is None and save:
+            u = _new((M, N), odt, dev)
+        if workspace is None and need > 0:
+            workspace = _new((need,), torch.uint8, dev)
+        _call("dora_matmul", px, pw, dt, M, N, K, _addr(row_scale), _addr(col_scale), pt, pb, r, s, _addr(bias), code,
+              _addr(residual), oc, _addr(y), _addr(u), _addr(workspace), need, _raw_stream(stream, dev))
+    return y, u
+
+
+GRAD_DX, GRAD_DW, GRAD_SUMS, GRAD_DU = 1, 2, 4, 8   # DORA_GRAD_*
+
+
+def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "none", need_dx: bool = True,
+                         need_dw: bool = True, need_dbias: bool = True, need_dcol_scale: bool = True,
+                         workspace=None, stream=None):
+    """Gradients of dora_matmul from its u (bfloat16, float16 or float32).
+
+    Returns (dx, dw, dbias, dcol_scale, du): dx [M, K], dw [N, K], dbias and
+    dcol_scale float32 [N] (each None if not needed), and du [M, N], the
+    gradient of u. x is read for dw and w for dx; either may be None where
+    its product is not needed, but not both. The residual's gradient is dy.
+    """
+    _first(dy, "dy")
+    dt = _TORCH_DT.get(dy.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {dy.dtype}; libdora takes bfloat16, float16 or float32")
+    dev = dy.device
+    M, N = dy.shape
+    _want(u, "u", (M, N), dy.dtype, dev)
+    if need_dx and w is None or need_dw and x is None:
+        raise ValueError("dx needs w, and dw needs x")
+    K = 0
+    if x is not None:
+        _first(x, "x")
+        K = x.shape[1]
+        _want(x, "x", (M, K), dy.dtype, dev)
+    if w is not None:
+        _first(w, "w")
+        K = w.shape[1] if x is None else K
+        _want(w, "w", (N, K), dy.dtype, dev)
+    _vec(col_scale, "col_scale", N, dev)
+    _vec(bias, "bias", N, dev)
+    code = _act(act)
+    with _on(stream):
+        du = _new((M, N), dy.dtype, dev)
+        dx = _new((M, K), dy.dtype, dev) if need_dx else None
+        dw = _new((N, K), dy.dtype, dev) if need_dw else None
+        dbias = _new((N,), torch.float32, dev) if need_dbias else None
+        dcol = _new((N,), torch.float32, dev) if need_dcol_scale else None
+        outputs = (GRAD_DX * need_dx + GRAD_DW * need_dw + GRAD_SUMS * (need_dbias or need_dcol_scale)
+                   + GRAD_DU * (du.data_ptr() % 16 == 0))
+        need = _size_of("dora_matmul_backward_workspace_size", M, N, K, dt, outputs)
+        if workspace is not None:
+            _workspace(workspace, "workspace", need, dev)
+        elif need > 0:
+            workspace = _new((need,), torch.uint8, dev)
+        _call("dora_matmul_backward", _addr(dy), _addr(u), _addr(x) if need_dw else None,
+              _addr(w) if need_dx else None, dt, M, N, K, _addr(col_scale), _addr(bias), code, _addr(du), _addr(dx),
+              _addr(dw), _addr(dbias), _addr(dcol), _addr(workspace), need, _raw_stream(stream, dev))
+    return dx, dw, dbias, dcol, du

@@ -24,7 +24,8 @@ LIB_PATH = os.path.join(HERE, "libdora.so")
 RESOURCE_REPORT = os.path.join(BUILD_DIR, "kernel_resources.txt")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["dora_api.hip", "norm_kernels.hip", "compose_kernels.hip"]
+SOURCES = ["dora_api.hip", "block_api.hip", "norm_kernels.hip", "compose_kernels.hip", "rms_norm_kernels.hip",
+           "matmul_kernels.hip"]
 
 COMMON_FLAGS = [
     "--offload-arch=gfx950",

@@ -24,8 +24,6 @@
 // fp32, and y is rounded once to the storage type. That saves the separate
 // addition's extra pass (read base and delta, write y) and its second
 // rounding.
-#include <type_traits>
-
 #include "dora_device.h"
 #include "dora_launch.h"
 
@@ -34,68 +32,6 @@ namespace dora {
 namespace {
 
 constexpr int kUnroll = 4;
-
-template <typename T, int VEC>
-struct Strip;
-template <typename T>
-struct Strip<T, 1> {
-  using V = T;
-};
-template <>
-struct Strip<bf16_t, 8> {
-  using V = u32x4;
-};
-template <>
-struct Strip<f16_t, 8> {
-  using V = u32x4;
-};
-template <>
-struct Strip<float, 4> {
-  using V = u32x4;
-};
-
-template <typename T, int VEC>
-__device__ __forceinline__ void unpack(const typename Strip<T, VEC>::V& v, float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    f[0] = to_f32(v);
-  } else if constexpr (std::is_same<T, f16_t>::value) {
-    const f16x8 h = __builtin_bit_cast(f16x8, v);   // the whole vector at once
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
-  } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(v[i] << 16);
-      f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
-  }
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ typename Strip<T, VEC>::V pack(const float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    return from_f32<T>(f[0]);
-  } else if constexpr (std::is_same<T, f16_t>::value) {
-    f16x8 h;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (f16_t)f[i];   // round to nearest even
-    return __builtin_bit_cast(u32x4, h);
-  } else if constexpr (sizeof(T) == 2) {
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = (uint32_t)f32_to_bf16_rne(f[2 * i]) | ((uint32_t)f32_to_bf16_rne(f[2 * i + 1]) << 16);
-    return v;
-  } else {
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(f[i]);
-    return v;
-  }
-}
 
 template <typename T, int VEC, bool ADD>
 __global__ __launch_bounds__(256) void compose_kernel(const T* base, const T* lora, const float* __restrict__ g,

@@ -8,34 +8,26 @@
 #include <vector>
 
 #include "../../include/dora.h"
+#include "dora_check.h"
 #include "dora_launch.h"
 #include "dora_plan.h"
 
 using dora::NormPlan;
+using dora::kAlign;
+using dora::align_up;
+using dora::ceil_div;
+using dora::valid_dtype;
+using dora::esize;
+using dora::epc;
+using dora::aligned;
+using dora::overlap;
+using dora::kMaxDim;
+using dora::hip_status;
 
 namespace {
 
 constexpr int kVersion = 10000;  // 1.0.0
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool valid_dtype(int dt) { return dt == DORA_BF16 || dt == DORA_F32 || dt == DORA_F16; }
-int64_t esize(int dt) { return dt == DORA_F32 ? 4 : 2; }
-int64_t epc(int dt) { return dt == DORA_F32 ? 4 : 8; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Byte ranges [a, a+na) and [b, b+nb) intersect (empty ranges never do).
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  if (a == nullptr || b == nullptr || na <= 0 || nb <= 0) return false;
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
-}
-
-// Upper bounds that keep every index and grid dimension in range.
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
+// (kMaxDim and kMaxRank keep every index and grid dimension in range.)
 constexpr int64_t kMaxRank = (int64_t)1 << 16;
 
 // Column tiling over r and the kernel configurations of both passes. Up to
@@ -390,7 +382,6 @@ bool offsets_fit_32(const NormPlan& p) {
   return tile_span < (1ull << 31) && b_span < (1ull << 31) && g_span < (1ull << 31);
 }
 
-dora_status hip_status(hipError_t e) { return e == hipSuccess ? DORA_OK : DORA_ERR_HIP; }
 
 dora_status compose_checked(const void* base, const void* lora, const float* g, float s, int dtype, int64_t T,
                             int64_t d_out, void* out, bool add_base, void* stream) {

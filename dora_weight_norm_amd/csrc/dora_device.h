@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace dora {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -225,6 +227,96 @@ __device__ __forceinline__ float sum32_transpose(const float (&p)[16], int lane)
   const float send = b1 ? q2[0] : q2[1];
   const float q1 = keep + swz_xor<2>(send);
   return q1 + swz_xor<1>(q1);
+}
+
+// s_waitcnt with vmcnt(N) and lgkmcnt(0), expcnt left alone (gfx9 encoding:
+// vmcnt bits [3:0] and [15:14], expcnt [6:4], lgkmcnt [11:8]).
+template <int N>
+__device__ __forceinline__ void wait_vm_lgkm0() {
+  static_assert(N >= 0 && N < 64, "vmcnt is six bits");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// Workgroup barrier that orders memory only through the explicit waits
+// before it: unlike __syncthreads it does not wait for every outstanding
+// load, so direct-to-LDS loads of later stages stay in flight across it.
+// The memory clobber keeps the compiler from moving LDS accesses across.
+__device__ __forceinline__ void barrier_keep_loads() { asm volatile("s_barrier" ::: "memory"); }
+
+// Compile-time flag carried into generic lambdas.
+template <bool V>
+struct Tag {
+  static constexpr bool value = V;
+};
+
+// Out-of-range buffer offset: a buffer load at it returns zeros.
+constexpr uint32_t kOob = 0x80000000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t nbytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)nbytes, 0x00020000);
+}
+
+// One thread's strip of VEC consecutive elements, as it is loaded and stored.
+template <typename T, int VEC>
+struct Strip;
+template <typename T>
+struct Strip<T, 1> {
+  using V = T;
+};
+template <>
+struct Strip<bf16_t, 8> {
+  using V = u32x4;
+};
+template <>
+struct Strip<f16_t, 8> {
+  using V = u32x4;
+};
+template <>
+struct Strip<float, 4> {
+  using V = u32x4;
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const typename Strip<T, VEC>::V& v, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = to_f32(v);
+  } else if constexpr (std::is_same<T, f16_t>::value) {
+    const f16x8 h = __builtin_bit_cast(f16x8, v);   // the whole vector at once
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ typename Strip<T, VEC>::V pack(const float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    return from_f32<T>(f[0]);
+  } else if constexpr (std::is_same<T, f16_t>::value) {
+    f16x8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (f16_t)f[i];   // round to nearest even
+    return __builtin_bit_cast(u32x4, h);
+  } else if constexpr (sizeof(T) == 2) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = (uint32_t)f32_to_bf16_rne(f[2 * i]) | ((uint32_t)f32_to_bf16_rne(f[2 * i + 1]) << 16);
+    return v;
+  } else {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(f[i]);
+    return v;
+  }
 }
 
 }  // namespace dora

@@ -36,6 +36,13 @@ size_t compose_bwd_workspace_bytes(int64_t T, int64_t d_out);
 hipError_t launch_compose_bwd(const void* dy, const void* base, const void* lora, const float* g, float s, int dtype,
                               int64_t T, int64_t d_out, void* d_base, void* d_lora, float* dg, const float* wnorm,
                               float eps, float* dm, void* ws, bool vec, hipStream_t st);
+hipError_t launch_column_sum(const float* part, int n_part, int64_t n, float* out0, int64_t n0, float* out1,
+                             hipStream_t st);
+hipError_t launch_rms_norm(const void* x, const void* residual, const float* weight, float eps, int dtype, int64_t T,
+                           int64_t d, void* h, void* y, void* q, float* scale, float* rstd, hipStream_t st);
+size_t rms_norm_bwd_workspace_bytes(int64_t T, int64_t d, int dtype);
+hipError_t launch_rms_norm_bwd(const void* dy, const void* dh, const void* h, const float* rstd, const float* weight,
+                               int dtype, int64_t T, int64_t d, void* dx, float* dweight, void* ws, hipStream_t st);
 size_t fast_kernel_lds_bytes(int cfg);
 size_t gen_kernel_lds_bytes(int cfg);
 

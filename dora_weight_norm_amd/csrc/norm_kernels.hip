@@ -48,33 +48,6 @@ namespace {
 constexpr int kGramCB = kGramCols;   // columns of G per Gram-term workgroup
 constexpr int kGramRows = 256;  // rows of B per Gram-term workgroup (32 per wave, 8 waves)
 
-// s_waitcnt with vmcnt(N) and lgkmcnt(0), expcnt left alone (gfx9 encoding:
-// vmcnt bits [3:0] and [15:14], expcnt [6:4], lgkmcnt [11:8]).
-template <int N>
-__device__ __forceinline__ void wait_vm_lgkm0() {
-  static_assert(N >= 0 && N < 64, "vmcnt is six bits");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
-
-// Workgroup barrier that orders memory only through the explicit waits
-// before it: unlike __syncthreads it does not wait for every outstanding
-// load, so direct-to-LDS loads of later stages stay in flight across it.
-// The memory clobber keeps the compiler from moving LDS accesses across.
-__device__ __forceinline__ void barrier_keep_loads() { asm volatile("s_barrier" ::: "memory"); }
-
-// Compile-time flag carried into generic lambdas.
-template <bool V>
-struct Tag {
-  static constexpr bool value = V;
-};
-
-// Out-of-range buffer offset: a buffer load at it returns zeros.
-constexpr uint32_t kOob = 0x80000000u;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t nbytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)nbytes, 0x00020000);
-}
-
 // ---------------------------------------------------------------------------
 // Streaming kernel (inputs allow aligned 16-byte loads).
 //

@@ -70,6 +70,10 @@ typedef enum dora_dtype {
                     bf16 hi + lo or in fp32) */
 } dora_dtype;
 
+/* 8-bit operands of dora_matmul and the 8-bit output of dora_rms_norm: OCP
+ * e4m3 (largest value 448, no infinity). No other entry point takes it. */
+#define DORA_E4M3 3
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* dora_status_string(int status);
 
@@ -340,6 +344,145 @@ dora_status dora_compose_backward(const void* dy, const void* base, const void* 
                                   float s, int dtype, int64_t T, int64_t d_out, void* d_base,
                                   void* d_lora, float* dg, const float* wnorm, float eps, float* dm,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------------------------------
+ * The block around the adapted layer: the norm before it, and the product
+ * with what surrounds it. Per-row and per-column vectors are fp32, like
+ * wnorm, m and g above.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *
+ *   h = x + residual
+ *   rstd[t] = 1 / sqrt(mean_j h[t,j]^2 + eps)
+ *   n[t,j]  = h[t,j] * rstd[t] * weight[j]
+ *   y = n in the storage type;  scale[t] = max_j |n[t,j]| / 448 and
+ *   q = n / scale[t] in e4m3 (both round to nearest even)
+ *
+ * x, residual, h, y: [T, d] of `dtype`; q: [T, d] bytes; weight: fp32 [d] or
+ * NULL (ones); scale, rstd: fp32 [T]. residual NULL: h is x, and the h
+ * argument must be NULL. h (with a residual), y, q and rstd may each be NULL
+ * to skip them, but not y and q both; scale comes with q. h may be x or
+ * residual itself. One launch, each input read once from memory (rows of
+ * more than 16384 elements are read again).
+ *
+ * Arithmetic is fp32: the norm is of the unrounded sum x + residual, and h is
+ * that sum rounded. A row of zeros has scale 1; a row whose largest |n| is
+ * below 448 * 2^-100 has scale 2^-100. A NaN in a row makes its rstd, n,
+ * scale and q NaN; an infinity (or a sum of squares past fp32's range) makes
+ * rstd 0, so that n is 0, or NaN at the infinity, and scale and q are then
+ * NaN as well. T == 0 does nothing; d == 0 has no norm and is refused when
+ * scale or rstd is asked for.
+ * Errors: DORA_ERR_INVALID_ARG (sizes, eps not finite or <= 0, missing,
+ * misaligned or overlapping pointers), DORA_ERR_UNSUPPORTED_DTYPE,
+ * DORA_ERR_HIP.
+ */
+dora_status dora_rms_norm(const void* x, const void* residual, const float* weight, float eps, int dtype, int64_t T,
+                          int64_t d, void* h, void* y, void* q, float* scale, float* rstd, void* stream);
+
+/*
+ * Workspace bytes dora_rms_norm_backward needs for dweight. Host only.
+ */
+dora_status dora_rms_norm_backward_workspace_size(int64_t T, int64_t d, int dtype, size_t* ws_bytes);
+
+/*
+ * Backward of the norm, from the h and rstd of the forward (h is x where
+ * there is no residual), with nh = h * rstd and a = dy * weight:
+ *
+ *   dx[t,j]    = rstd[t] * (a[t,j] - nh[t,j] * mean_j(a[t,:] nh[t,:])) + dh[t,j]
+ *   dweight[j] = sum_t dy[t,j] * nh[t,j]
+ *
+ * dx is the gradient of x and of residual alike; dh is the gradient that
+ * reaches h directly (the residual stream), or NULL. dx may be dy or dh
+ * itself. dweight may be NULL (the weight frozen); it is summed in fp32 in a
+ * fixed order, and needs the workspace (256-byte aligned).
+ * Errors: as dora_rms_norm, and DORA_ERR_WORKSPACE.
+ */
+dora_status dora_rms_norm_backward(const void* dy, const void* dh, const void* h, const float* rstd,
+                                   const float* weight, int dtype, int64_t T, int64_t d, void* dx, float* dweight,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum dora_act {
+  DORA_ACT_NONE = 0,
+  DORA_ACT_RELU = 1,
+  DORA_ACT_GELU = 2,      /* z * Phi(z), by the error function              */
+  DORA_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))  */
+  DORA_ACT_SILU = 4       /* z / (1 + exp(-z))                              */
+} dora_act;
+
+/*
+ * Device workspace dora_matmul needs. `aligned_operands` has a bit for each
+ * operand that starts on a 16-byte boundary (1 x, 2 w, 4 t, 8 b): an operand
+ * that does not, or whose row length is no multiple of 16 bytes, is copied
+ * into the workspace at a row stride that is. Host only.
+ */
+dora_status dora_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, int aligned_operands,
+                                       size_t* ws_bytes);
+
+/*
+ * Matrix product with its epilogue:
+ *
+ *   u[m,n] = row_scale[m] * sum_k x[m,k] w[n,k] + s * sum_l t[m,l] b[n,l]
+ *   y[m,n] = act(col_scale[n] * u[m,n] + bias[n]) + residual[m,n]
+ *
+ * x [M, K], w [N, K] of `dtype` (bf16, fp16, fp32 or DORA_E4M3); t [M, r] and
+ * b [N, r] of the same type (the low-rank pair: t = x A^T, b = B; none with
+ * r == 0, and none in e4m3). row_scale fp32 [M], col_scale and bias fp32 [N],
+ * residual [M, N], each or NULL. y, u and residual are of `out_dtype`, which
+ * is `dtype` except for e4m3 (any of the three). u, if not NULL, receives the
+ * product before the column scale, for the backward. y may be residual
+ * itself.
+ *
+ * With w = W, b = B, s the adapter's and col_scale = g of dora_factored_norm,
+ * y is the whole DoRA layer g * (x W^T + s t B^T) + bias in one launch, with
+ * neither projection written to memory. With e4m3 rows and scales of
+ * dora_rms_norm as x and row_scale, col_scale carries the weight rows' scales.
+ *
+ * Products accumulate in fp32 on the matrix cores, the epilogue is fp32, and
+ * y and u are each rounded once. `workspace` (256-byte aligned) holds at
+ * least dora_matmul_workspace_size bytes; its contents on entry are ignored.
+ * K == 0 gives u = s t b^T (0 without a pair); M == 0 or N == 0 does nothing.
+ * Rows of x, w, t, b take less than 2^23 bytes.
+ * Errors: DORA_ERR_INVALID_ARG (sizes, s not finite, unknown act, a pair in
+ * e4m3, missing, misaligned or overlapping pointers),
+ * DORA_ERR_UNSUPPORTED_DTYPE, DORA_ERR_WORKSPACE, DORA_ERR_HIP.
+ */
+dora_status dora_matmul(const void* x, const void* w, int dtype, int64_t M, int64_t N, int64_t K,
+                        const float* row_scale, const float* col_scale, const void* t, const void* b, int64_t r,
+                        float s, const float* bias, int act, const void* residual, int out_dtype, void* y, void* u,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Outputs of dora_matmul_backward, as its workspace query names them. */
+#define DORA_GRAD_DX 1   /* dx                                  */
+#define DORA_GRAD_DW 2   /* dw                                  */
+#define DORA_GRAD_SUMS 4 /* dbias or dcol_scale, or both        */
+#define DORA_GRAD_DU 8   /* du, in an array aligned to 16 bytes */
+
+/* Device workspace dora_matmul_backward needs for a set of outputs. Host only. */
+dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs,
+                                                size_t* ws_bytes);
+
+/*
+ * Backward of the product (bf16, fp16 or fp32), from the u of the forward;
+ * the residual's gradient is dy itself:
+ *
+ *   z = col_scale[n] * u + bias[n]     dz = dy * act'(z)
+ *   dbias[n] = sum_m dz                dcol_scale[n] = sum_m dz * u
+ *   du = col_scale[n] * dz, rounded to the storage type
+ *   dx = du w                          dw = du^T x
+ *
+ * dy, u, du [M, N]; dx [M, K]; dw [N, K]; dbias, dcol_scale fp32 [N]; any
+ * output may be NULL. du may be dy itself. The low-rank pair's gradients are
+ * those of two more products: with du as dy, act none and col_scale NULL,
+ * x = t and w = b give s^-1 dt (dx) and s^-1 db (dw). Sums are fp32 in a
+ * fixed order, without atomics; act' of relu at 0 is 0.
+ * Errors: as dora_matmul; M and N too are limited to rows of 2^23 bytes.
+ */
+dora_status dora_matmul_backward(const void* dy, const void* u, const void* x, const void* w, int dtype, int64_t M,
+                                 int64_t N, int64_t K, const float* col_scale, const float* bias, int act, void* du,
+                                 void* dx, void* dw, float* dbias, float* dcol_scale, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
