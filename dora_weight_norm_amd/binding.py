@@ -609,7 +609,7 @@ def _act(act) -> int:
 
 def dora_matmul(x, w, row_scale=None, col_scale=None, t=None, b=None, s: float = 1.0, bias=None, act: str = "none",
                 residual=None, out_dtype=None, save: bool = False, y=None, u=None, workspace=None, stream=None):
-    """y = act(col_scale * u + bias) + residual with u = row_scale * (x w^T) + s * (t b^T).
+    """y = act(col_scale * u + bias) + residual with u = row_scale * (x w^T + s * t b^T).
 
     x [M, K] and w [N, K] of one dtype (bfloat16, float16, float32 or
     float8_e4m3fn); t [M, r] and b [N, r] of the same dtype, both or neither

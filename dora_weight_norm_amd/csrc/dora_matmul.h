@@ -39,8 +39,8 @@ struct GemmArgs {
   Epilogue ep;
 };
 
-// Tile configurations.
-enum MatmulTile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+// Kernels: tiles of 256, 128 or 64 rows and columns, or the few-rows kernel.
+enum MatmulTile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFewRows = 3 };
 
 struct MatmulPlan {
   int cfg;

@@ -1,6 +1,6 @@
 // Matrix product with a fused epilogue on gfx950, and its backward.
 //
-//   u = row_scale[m] * sum_k x[m,k] w[n,k] + s sum_l t[m,l] b[n,l]
+//   u = row_scale[m] * (sum_k x[m,k] w[n,k] + s sum_l t[m,l] b[n,l])
 //   y = act(col_scale[n] * u + bias[n]) + residual[m,n]
 //
 // bf16, fp16, fp32 or e4m3 operands on the matrix cores with fp32
@@ -73,26 +73,28 @@ constexpr float kTanhC = 0.044715f;
 
 __device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + expf(-v)); }
 
+__device__ __forceinline__ float act1(float z, int act) {
+  switch (act) {
+    case 1: return z < 0.f ? 0.f : z;
+    case 2: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case 3: return z * logistic(2.f * kTanhK * fmaf(kTanhC * z * z, z, z));
+    case 4: return z * logistic(z);
+    default: return z;
+  }
+}
+
 // Eight values at once, so that the (uniform) choice is made once.
 __device__ __forceinline__ void act8(float (&z)[8], int act) {
   switch (act) {
-    case 1:
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = z[e] < 0.f ? 0.f : z[e];
-      break;
-    case 2:
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = 0.5f * z[e] * (1.f + erff(z[e] * 0.70710678118654752f));
-      break;
-    case 3:
-      // z / 2 (1 + tanh(v)) = z / (1 + exp(-2 v))
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] *= logistic(2.f * kTanhK * fmaf(kTanhC * z[e] * z[e], z[e], z[e]));
-      break;
-    case 4:
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] *= logistic(z[e]);
-      break;
+#define DORA_ACT8(A)                                     \
+  case A:                                                \
+    for (int e = 0; e < 8; ++e) z[e] = act1(z[e], A);    \
+    break;
+    DORA_ACT8(1)
+    DORA_ACT8(2)
+    DORA_ACT8(3)
+    DORA_ACT8(4)
+#undef DORA_ACT8
     default: break;
   }
 }
@@ -170,6 +172,16 @@ __device__ __forceinline__ void epilogue8(const Epilogue& ep, float (&v)[8], con
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
   store8<O>(static_cast<O*>(ep.y) + off, n, v);
+}
+
+// The epilogue on one element.
+template <typename O>
+__device__ __forceinline__ void epilogue1(const Epilogue& ep, float v, float cs, float bs, int64_t m, int64_t off) {
+  if (ep.row_scale) v *= ep.row_scale[m];
+  if (ep.u) static_cast<O*>(ep.u)[off] = from_f32<O>(v);
+  v = act1(fmaf(cs, v, bs), ep.act);
+  if (ep.residual) v += to_f32(static_cast<const O*>(ep.residual)[off]);
+  static_cast<O*>(ep.y)[off] = from_f32<O>(v);
 }
 
 __device__ __forceinline__ void column_terms(const Epilogue& ep, int64_t c, int n, float (&cs)[8], float (&bs)[8]) {
@@ -376,6 +388,202 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows (a batch of single tokens): the product is one reading of w. A
+// workgroup owns 16 R columns (rows of w), its eight waves a contiguous
+// eighth of the depth each, and w goes from memory straight into the operand
+// registers of the 16x16 matrix instructions, each row in 64-byte (e4m3:
+// 128-byte) pieces, two batches of kBatch steps in flight. The tokens are the
+// other operand (16 TF of them), read from L2. The waves' sums are added in
+// wave order through LDS, then the epilogue runs on one element a thread.
+// Rows at any element address are read as they are; only the last partial
+// step of the depth is read with bounds.
+// ---------------------------------------------------------------------------
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Op16;
+template <>
+struct Op16<bf16_t> {
+  static __device__ __forceinline__ f32x4 run(const u32x4* a, const u32x4* b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[0]), __builtin_bit_cast(bf16x8, b[0]),
+                                                   c, 0, 0, 0);
+  }
+};
+template <>
+struct Op16<f16_t> {
+  static __device__ __forceinline__ f32x4 run(const u32x4* a, const u32x4* b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a[0]), __builtin_bit_cast(f16x8, b[0]), c,
+                                                  0, 0, 0);
+  }
+};
+template <>
+struct Op16<float> {
+  static __device__ __forceinline__ f32x4 run(const u32x4* a, const u32x4* b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[0][e]), __uint_as_float(b[0][e]), c, 0, 0, 0);
+    return c;
+  }
+};
+template <>
+struct Op16<e4m3_t> {
+  static __device__ __forceinline__ f32x4 run(const u32x4* a, const u32x4* b, f32x4 c) {
+    struct P {
+      u32x4 lo, hi;
+    };
+    const P pa{a[0], a[1]}, pb{b[0], b[1]};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, pa),
+                                                            __builtin_bit_cast(i32x8, pb), c, 0, 0, 0, 0x7f7f7f7f, 0,
+                                                            0x7f7f7f7f);
+  }
+};
+
+constexpr int kFewWaves = 8;   // waves of a workgroup, each with its share of the depth
+
+template <typename T, int R, int TF, int BATCH>
+struct FewFrag {
+  static constexpr int CH = sizeof(T) == 1 ? 2 : 1;   // 16-byte chunks a lane feeds one instruction
+  u32x4 w[BATCH][R][CH], x[BATCH][TF][CH];
+};
+
+// Bytes [at, at + 16) of a row of `len` bytes, zeros past its end.
+__device__ __forceinline__ u32x4 load_bounded(const char* row, int64_t at, int64_t len) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (at + 16 <= len) return *reinterpret_cast<const u32x4_any*>(row + at);
+  if (at < len) {
+    uint8_t tmp[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) tmp[e] = at + e < len ? (uint8_t)row[at + e] : (uint8_t)0;
+    __builtin_memcpy(&v, tmp, 16);
+  }
+  return v;
+}
+
+// acc += this wave's share of the depth of one operand pair.
+template <typename T, int R, int TF, int BATCH>
+__device__ __forceinline__ void few_rows_depth(const char* const (&wp)[R], const char* const (&xp)[TF], int64_t len,
+                                               int part, int parts, int grp, f32x4 (&acc)[R][TF]) {
+  using F = FewFrag<T, R, TF, BATCH>;
+  constexpr int CH = F::CH, SB = 64 * CH;   // bytes of a row that one step takes
+  const int64_t full = len / SB;            // whole steps
+  const int64_t s0 = full * part / parts, s1 = full * (part + 1) / parts;
+  const int64_t base = grp * 16 * CH;
+  auto load = [&](F& f, int64_t s, int n) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (i >= n) continue;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int64_t at = (s + i) * SB + base + c * 16;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          f.w[i][r][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(wp[r] + at));
+#pragma unroll
+        for (int t = 0; t < TF; ++t) f.x[i][t][c] = *reinterpret_cast<const u32x4_any*>(xp[t] + at);
+      }
+    }
+  };
+  auto run = [&](const F& f, int n) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (i >= n) continue;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TF; ++t) acc[r][t] = Op16<T>::run(f.w[i][r], f.x[i][t], acc[r][t]);
+    }
+  };
+  F a, b;
+  int64_t s = s0;
+  if (s + BATCH <= s1) {
+    load(a, s, BATCH);
+    s += BATCH;
+    for (; s + 2 * BATCH <= s1; s += 2 * BATCH) {
+      load(b, s, BATCH);
+      run(a, BATCH);
+      load(a, s + BATCH, BATCH);
+      run(b, BATCH);
+    }
+    run(a, BATCH);
+  }
+  for (; s < s1; ++s) {
+    load(a, s, 1);
+    run(a, 1);
+  }
+  if (part == parts - 1 && full * SB < len) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t at = full * SB + base + c * 16;
+#pragma unroll
+      for (int r = 0; r < R; ++r) a.w[0][r][c] = load_bounded(wp[r], at, len);
+#pragma unroll
+      for (int t = 0; t < TF; ++t) a.x[0][t][c] = load_bounded(xp[t], at, len);
+    }
+    run(a, 1);
+  }
+}
+
+template <typename T, typename O, int R, int TF, int BATCH>
+__global__ __launch_bounds__(kFewWaves * 64, 1) void matmul_few_rows_kernel(GemmArgs g) {
+  constexpr int ESZ = Op<T>::esz;
+  __shared__ float red[kFewWaves * R * TF * 256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i16 = lane & 15, grp = lane >> 4;
+  const int split = blockIdx.x / g.n_nt;
+  const int64_t n0 = (int64_t)(blockIdx.x - split * g.n_nt) * (16 * R);
+  // Columns and tokens past the end read the last one's and are not stored.
+  const char *wp[R], *xp[TF], *bp[R], *tp[TF];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t n = n0 + r * 16 + i16 < g.N ? n0 + r * 16 + i16 : g.N - 1;
+    wp[r] = static_cast<const char*>(g.b) + n * g.ldb * ESZ;
+    bp[r] = static_cast<const char*>(g.b2) + n * g.ldb2 * ESZ;
+  }
+#pragma unroll
+  for (int t = 0; t < TF; ++t) {
+    const int64_t m = t * 16 + i16 < g.M ? t * 16 + i16 : g.M - 1;
+    xp[t] = static_cast<const char*>(g.a) + m * g.lda * ESZ;
+    tp[t] = static_cast<const char*>(g.a2) + m * g.lda2 * ESZ;
+  }
+  f32x4 acc[R][TF];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < TF; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int part = split * kFewWaves + wave, parts = g.splits * kFewWaves;
+  if (g.K2 > 0) {
+    few_rows_depth<T, R, TF, 2>(bp, tp, g.K2 * ESZ, part, parts, grp, acc);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < TF; ++t) acc[r][t] *= g.s;
+  }
+  few_rows_depth<T, R, TF, BATCH>(wp, xp, g.K * ESZ, part, parts, grp, acc);
+  // Lane holds columns 4 grp .. 4 grp + 3 of its 16 and token i16.
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < TF; ++t)
+      *reinterpret_cast<f32x4*>(red + ((wave * R + r) * TF + t) * 256 + lane * 4) = acc[r][t];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256 * R * TF; i += kFewWaves * 64) {
+    const int nl = i % (16 * R), ml = i / (16 * R);
+    const int64_t n = n0 + nl, m = ml;
+    if (m >= g.M || n >= g.N) continue;
+    const int at = ((nl / 16) * TF + ml / 16) * 256 + ((ml % 16) + 16 * ((nl % 16) / 4)) * 4 + nl % 4;
+    float v = red[at];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += red[w * R * TF * 256 + at];
+    if (g.splits > 1) {
+      g.part[((int64_t)split * g.M + m) * g.N + n] = v;
+    } else {
+      const float cs1 = g.ep.col_scale ? g.ep.col_scale[n] : 1.f, bs1 = g.ep.bias ? g.ep.bias[n] : 0.f;
+      epilogue1<O>(g.ep, v, cs1, bs1, m, m * g.N + n);
+    }
+  }
+}
+
 // Adds the parts of the depth in increasing order and runs the epilogue.
 template <typename O>
 __global__ __launch_bounds__(256) void matmul_join_kernel(GemmArgs g) {
@@ -511,6 +719,16 @@ int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 void choose_tile(int64_t M, int64_t N, int64_t stages, int* cfg, int* splits) {
+  if (M <= 16) {
+    // One workgroup per 32 columns; the depth is split over workgroups too
+    // while they do not fill the chip and each wave keeps four steps.
+    *cfg = kFewRows;
+    const int64_t n = up(N, 32) / 32;
+    int64_t s = n >= kCUs || n < 1 ? 1 : kCUs / n;
+    if (s > stages / 16) s = stages / 16;
+    *splits = (int)(s < 1 ? 1 : s);
+    return;
+  }
   auto tiles = [&](int t) { return up(M, t) / t * (up(N, t) / t); };
   *cfg = tiles(256) >= 192 ? kTile256 : (tiles(128) >= 128 ? kTile128 : kTile64);
   const int64_t n = tiles(tile_rows(*cfg));
@@ -534,8 +752,25 @@ hipError_t launch_tile(GemmArgs g, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <typename O>
+hipError_t launch_join(const GemmArgs& g, hipStream_t st) {
+  const int64_t n = g.M * ((g.N + 7) / 8);
+  hipLaunchKernelGGL((matmul_join_kernel<O>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g);
+  return hipGetLastError();
+}
+
+template <typename T, typename O, int R, int TF>
+hipError_t launch_few_rows(GemmArgs g, hipStream_t st) {
+  g.n_nt = (int)((g.N + 16 * R - 1) / (16 * R));
+  hipLaunchKernelGGL((matmul_few_rows_kernel<T, O, R, TF, 4>), dim3((unsigned)(g.n_nt * g.splits)),
+                     dim3(kFewWaves * 64), 0, st, g);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
+}
+
 template <typename T, typename O>
 hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
+  if (cfg == kFewRows) return launch_few_rows<T, O, 2, 1>(g, st);
   constexpr int KT = 128 / Op<T>::esz;
   const int n2 = ((int)((g.K2 + KT - 1) / KT) + 1) & ~1;
   g.stages = n2 + (int)((g.K + KT - 1) / KT);
@@ -551,10 +786,7 @@ hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
     case kTile128: e = launch_tile<T, O, 2, 2, 2, 2>(g, st); break;
     default: e = launch_tile<T, O, 2, 2, 1, 1>(g, st); break;
   }
-  if (e != hipSuccess || g.splits == 1) return e;
-  const int64_t n = g.M * ((g.N + 7) / 8);
-  hipLaunchKernelGGL((matmul_join_kernel<O>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g);
-  return hipGetLastError();
+  return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
 }
 
 hipError_t gemm(const GemmArgs& g, int dtype, int out_dtype, int cfg, hipStream_t st) {
@@ -604,8 +836,10 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   MatmulPlan p{};
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
+  choose_tile(M, N, up(K, KT) / KT, &p.cfg, &p.splits);
   auto operand = [&](int64_t rows, int64_t depth, int bit, bool* pack, int64_t* ld, size_t* at) {
-    *pack = depth > 0 && (depth % epc != 0 || !(al & bit));
+    // (the few-rows kernel reads rows at any element address)
+    *pack = p.cfg != kFewRows && depth > 0 && (depth % epc != 0 || !(al & bit));
     *ld = *pack ? up(depth, epc) : depth;
     *at = off;
     if (*pack) off = up256(off + (size_t)(rows * *ld) * esz);
@@ -614,7 +848,6 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   operand(N, K, 2, &p.pack_w, &p.ldw, &p.off_w);
   operand(M, r, 4, &p.pack_t, &p.ldt, &p.off_t);
   operand(N, r, 8, &p.pack_b, &p.ldb, &p.off_b);
-  choose_tile(M, N, up(K, KT) / KT, &p.cfg, &p.splits);
   p.off_part = off;
   if (p.splits > 1) off = up256(off + (size_t)(p.splits * M * N) * 4);
   p.ws_bytes = off;

@@ -423,7 +423,7 @@ dora_status dora_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int64_t 
 /*
  * Matrix product with its epilogue:
  *
- *   u[m,n] = row_scale[m] * sum_k x[m,k] w[n,k] + s * sum_l t[m,l] b[n,l]
+ *   u[m,n] = row_scale[m] * (sum_k x[m,k] w[n,k] + s * sum_l t[m,l] b[n,l])
  *   y[m,n] = act(col_scale[n] * u[m,n] + bias[n]) + residual[m,n]
  *
  * x [M, K], w [N, K] of `dtype` (bf16, fp16, fp32 or DORA_E4M3); t [M, r] and

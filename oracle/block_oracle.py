@@ -75,12 +75,12 @@ def slope(z, name):
 
 
 def product(x, w, row_scale=None, t=None, b=None, s=1.0):
-    """u = row_scale (x w^T) + s t b^T in fp64."""
+    """u = row_scale (x w^T + s t b^T) in fp64."""
     u = np.asarray(x, np.float64) @ np.asarray(w, np.float64).T
-    if row_scale is not None:
-        u = u * np.asarray(row_scale, np.float64)[:, None]
     if t is not None:
         u = u + s * (np.asarray(t, np.float64) @ np.asarray(b, np.float64).T)
+    if row_scale is not None:
+        u = u * np.asarray(row_scale, np.float64)[:, None]
     return u
 
 

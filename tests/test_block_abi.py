@@ -77,8 +77,8 @@ def test_matmul_refusals():
     assert _mm(y=0x1000000) == 1 and _mm(y=0x2000010) == 1
     assert _mm(residual=0x5000010) == 1                         # partly over y
     assert _mm(u=0x5000000) == 1                                # u over y
-    assert _mm(K=63, ws_bytes=64) == 4 and _mm(K=63, ws=None) == 4 and _mm(K=63, ws=0x8000010) == 4
-    assert _mm(K=63, ws=0x2000000) == 1                         # workspace over w
+    assert _mm(M=40, K=63, ws_bytes=64) == 4 and _mm(M=40, K=63, ws=None) == 4 and _mm(M=40, K=63, ws=0x8000010) == 4
+    assert _mm(M=40, K=63, ws=0x2000000) == 1                         # workspace over w
     assert _mm(M=0) == 0 and _mm(N=0) == 0
 
 

@@ -45,11 +45,11 @@ def product_err(o):
     """Bound of u's fp32 error."""
     x, w = np.abs(host(o["x"])), np.abs(host(o["w"]))
     e = ((x.shape[1] + 4) * EPS32 + (7 * 2.0 ** -13 if o["x"].dtype == TORCH_DT["e4m3"] else 0)) * (x @ w.T)
-    if o.get("row_scale") is not None:
-        e = e * np.abs(host(o["row_scale"]))[:, None]
     if o.get("t") is not None:
         t, b = np.abs(host(o["t"])), np.abs(host(o["b"]))
         e = e + abs(o["s"]) * (t.shape[1] + x.shape[1] + 4) * EPS32 * (t @ b.T)
+    if o.get("row_scale") is not None:
+        e = e * np.abs(host(o["row_scale"]))[:, None]
     return e
 
 
@@ -96,6 +96,21 @@ def test_activations(shape, name):
 def test_e4m3_outputs(shape, out):
     o, rng = operands(*shape, 0, "e4m3", 4)
     check(o, rng, "e4m3", out, "silu", True, True)
+
+
+@pytest.mark.parametrize("shape", [(3, 200, 264, 16), (70, 136, 200, 24)])
+def test_row_scale_covers_the_low_rank_pair(shape):
+    o, rng = operands(*shape, "bf16", 15)
+    o["row_scale"] = vec(rng, shape[0], 0.3)
+    check(o, rng, "bf16", "bf16", "none", False, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32", "e4m3"])
+@pytest.mark.parametrize("M,N,K,r", [(1, 100, 5000, 40), (7, 33, 1023, 5), (16, 8192, 264, 0), (15, 31, 16, 700),
+                                     (2, 64, 20001, 0)])
+def test_few_rows(M, N, K, r, dtype):
+    o, rng = operands(M, N, K, r, dtype, M + N + K)
+    check(o, rng, dtype, "bf16" if dtype == "e4m3" else dtype, ACTS[N % 5], True, True)
 
 
 def test_plain_product_without_any_epilogue():
@@ -292,7 +307,7 @@ def test_refusals_of_the_binding():
         with pytest.raises((ValueError, TypeError)):
             bnd.dora_matmul(**{**dict(x=x, w=w), **kw})
     with pytest.raises(ValueError):   # rows of 252 bytes are copied: the workspace is needed and too small
-        bnd.dora_matmul(x[:, :63].contiguous(), w[:, :63].contiguous(),
+        bnd.dora_matmul(torch.zeros(40, 63, device="cuda"), w[:, :63].contiguous(),
                         workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError):
         bnd.dora_matmul(x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn), t=t, b=b)
