@@ -389,15 +389,24 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (a batch of single tokens): the product is one reading of w. A
-// workgroup owns 16 R columns (rows of w), its eight waves a contiguous
-// eighth of the depth each, and w goes from memory straight into the operand
-// registers of the 16x16 matrix instructions, each row in 64-byte (e4m3:
-// 128-byte) pieces, two batches of kBatch steps in flight. The tokens are the
-// other operand (16 TF of them), read from L2. The waves' sums are added in
-// wave order through LDS, then the epilogue runs on one element a thread.
-// Rows at any element address are read as they are; only the last partial
-// step of the depth is read with bounds.
+// Few rows (a batch of single tokens): the product is one reading of w, and
+// bound by memory. A workgroup owns 8 R columns (rows of w), its eight waves
+// a contiguous eighth of the depth each, and w goes from memory straight into
+// the operand registers of the 16x16 matrix instructions, two batches of
+// BATCH steps in flight. The tokens are the other operand (8 TF of them), read
+// from L2.
+// A load instruction takes 128 bytes of each of eight rows (lane l: row l % 8,
+// chunk l / 8). To the matrix instruction that is 16 rows of four chunks:
+// rows i < 8 are w's rows with the even chunks and rows i >= 8 the same rows
+// with the odd ones, and likewise for the tokens, so that of its 16 x 16 sums
+// the two diagonal 8 x 8 blocks are wanted and are added at the end. It wastes
+// half of the matrix cores, which idle here, for whole 128-byte lines:
+// reading 8192 x 8192 bf16 takes 21 us so, 24 us in 64-byte pieces of 16 rows
+// and 21 us in 1 KiB pieces; with 32 rows a workgroup (one workgroup a compute
+// unit instead of two) each is 10 to 20% slower.
+// The waves' sums are added in wave order through LDS, then the epilogue runs
+// on one element a thread. Rows at any element address are read as they are;
+// only the last partial step of the depth is read with bounds.
 // ---------------------------------------------------------------------------
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -463,19 +472,19 @@ __device__ __forceinline__ u32x4 load_bounded(const char* row, int64_t at, int64
 // acc += this wave's share of the depth of one operand pair.
 template <typename T, int R, int TF, int BATCH>
 __device__ __forceinline__ void few_rows_depth(const char* const (&wp)[R], const char* const (&xp)[TF], int64_t len,
-                                               int part, int parts, int grp, f32x4 (&acc)[R][TF]) {
+                                               int part, int parts, int chunk, f32x4 (&acc)[R][TF]) {
   using F = FewFrag<T, R, TF, BATCH>;
-  constexpr int CH = F::CH, SB = 64 * CH;   // bytes of a row that one step takes
+  constexpr int CH = F::CH, SB = 128 * CH;   // bytes of a row that one step takes
   const int64_t full = len / SB;            // whole steps
   const int64_t s0 = full * part / parts, s1 = full * (part + 1) / parts;
-  const int64_t base = grp * 16 * CH;
+  const int64_t base = chunk * 16;
   auto load = [&](F& f, int64_t s, int n) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       if (i >= n) continue;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int64_t at = (s + i) * SB + base + c * 16;
+        const int64_t at = (s + i) * SB + c * 128 + base;
 #pragma unroll
         for (int r = 0; r < R; ++r)
           f.w[i][r][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(wp[r] + at));
@@ -514,7 +523,7 @@ __device__ __forceinline__ void few_rows_depth(const char* const (&wp)[R], const
   if (part == parts - 1 && full * SB < len) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t at = full * SB + base + c * 16;
+      const int64_t at = full * SB + c * 128 + base;
 #pragma unroll
       for (int r = 0; r < R; ++r) a.w[0][r][c] = load_bounded(wp[r], at, len);
 #pragma unroll
@@ -525,24 +534,24 @@ __device__ __forceinline__ void few_rows_depth(const char* const (&wp)[R], const
 }
 
 template <typename T, typename O, int R, int TF, int BATCH>
-__global__ __launch_bounds__(kFewWaves * 64, 1) void matmul_few_rows_kernel(GemmArgs g) {
+__global__ __launch_bounds__(kFewWaves * 64, TF <= 2 ? 2 : 1) void matmul_few_rows_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz;
   __shared__ float red[kFewWaves * R * TF * 256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, grp = lane >> 4;
+  const int i8 = lane & 7, chunk = lane >> 3;
   const int split = blockIdx.x / g.n_nt;
-  const int64_t n0 = (int64_t)(blockIdx.x - split * g.n_nt) * (16 * R);
+  const int64_t n0 = (int64_t)(blockIdx.x - split * g.n_nt) * (8 * R);
   // Columns and tokens past the end read the last one's and are not stored.
   const char *wp[R], *xp[TF], *bp[R], *tp[TF];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int64_t n = n0 + r * 16 + i16 < g.N ? n0 + r * 16 + i16 : g.N - 1;
+    const int64_t n = n0 + r * 8 + i8 < g.N ? n0 + r * 8 + i8 : g.N - 1;
     wp[r] = static_cast<const char*>(g.b) + n * g.ldb * ESZ;
     bp[r] = static_cast<const char*>(g.b2) + n * g.ldb2 * ESZ;
   }
 #pragma unroll
   for (int t = 0; t < TF; ++t) {
-    const int64_t m = t * 16 + i16 < g.M ? t * 16 + i16 : g.M - 1;
+    const int64_t m = t * 8 + i8 < g.M ? t * 8 + i8 : g.M - 1;
     xp[t] = static_cast<const char*>(g.a) + m * g.lda * ESZ;
     tp[t] = static_cast<const char*>(g.a2) + m * g.lda2 * ESZ;
   }
@@ -553,28 +562,29 @@ __global__ __launch_bounds__(kFewWaves * 64, 1) void matmul_few_rows_kernel(Gemm
     for (int t = 0; t < TF; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int part = split * kFewWaves + wave, parts = g.splits * kFewWaves;
   if (g.K2 > 0) {
-    few_rows_depth<T, R, TF, 2>(bp, tp, g.K2 * ESZ, part, parts, grp, acc);
+    few_rows_depth<T, R, TF, BATCH < 2 ? BATCH : 2>(bp, tp, g.K2 * ESZ, part, parts, chunk, acc);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int t = 0; t < TF; ++t) acc[r][t] *= g.s;
   }
-  few_rows_depth<T, R, TF, BATCH>(wp, xp, g.K * ESZ, part, parts, grp, acc);
-  // Lane holds columns 4 grp .. 4 grp + 3 of its 16 and token i16.
+  few_rows_depth<T, R, TF, BATCH>(wp, xp, g.K * ESZ, part, parts, chunk, acc);
+  // Sum (i, j) of a 16 x 16 block is value i % 4 of lane 16 (i / 4) + j.
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int t = 0; t < TF; ++t)
       *reinterpret_cast<f32x4*>(red + ((wave * R + r) * TF + t) * 256 + lane * 4) = acc[r][t];
   __syncthreads();
-  for (int i = threadIdx.x; i < 256 * R * TF; i += kFewWaves * 64) {
-    const int nl = i % (16 * R), ml = i / (16 * R);
+  for (int i = threadIdx.x; i < 64 * R * TF; i += kFewWaves * 64) {
+    const int nl = i % (8 * R), ml = i / (8 * R);
     const int64_t n = n0 + nl, m = ml;
     if (m >= g.M || n >= g.N) continue;
-    const int at = ((nl / 16) * TF + ml / 16) * 256 + ((ml % 16) + 16 * ((nl % 16) / 4)) * 4 + nl % 4;
-    float v = red[at];
+    const int at = ((nl / 8) * TF + ml / 8) * 256 + (16 * ((nl % 8) / 4) + ml % 8) * 4 + nl % 4;
+    constexpr int kOther = (16 * 2 + 8) * 4;   // from sum (i, j) to sum (i + 8, j + 8)
+    float v = red[at] + red[at + kOther];
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) v += red[w * R * TF * 256 + at];
+    for (int w = 1; w < kFewWaves; ++w) v += red[w * R * TF * 256 + at] + red[w * R * TF * 256 + at + kOther];
     if (g.splits > 1) {
       g.part[((int64_t)split * g.M + m) * g.N + n] = v;
     } else {
@@ -719,11 +729,11 @@ int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 void choose_tile(int64_t M, int64_t N, int64_t stages, int* cfg, int* splits) {
-  if (M <= 16) {
-    // One workgroup per 32 columns; the depth is split over workgroups too
+  if (M <= 32) {
+    // One workgroup per 16 columns; the depth is split over workgroups too
     // while they do not fill the chip and each wave keeps four steps.
     *cfg = kFewRows;
-    const int64_t n = up(N, 32) / 32;
+    const int64_t n = M <= 16 ? up(N, 16) / 16 : up(N, 32) / 32;
     int64_t s = n >= kCUs || n < 1 ? 1 : kCUs / n;
     if (s > stages / 16) s = stages / 16;
     *splits = (int)(s < 1 ? 1 : s);
@@ -761,8 +771,10 @@ hipError_t launch_join(const GemmArgs& g, hipStream_t st) {
 
 template <typename T, typename O, int R, int TF>
 hipError_t launch_few_rows(GemmArgs g, hipStream_t st) {
-  g.n_nt = (int)((g.N + 16 * R - 1) / (16 * R));
-  hipLaunchKernelGGL((matmul_few_rows_kernel<T, O, R, TF, 4>), dim3((unsigned)(g.n_nt * g.splits)),
+  g.n_nt = (int)((g.N + 8 * R - 1) / (8 * R));
+  // (at most 128 registers, two workgroups a compute unit, where TF <= 2)
+  constexpr int BATCH = (TF == 1 ? 4 : 2) / (Op<T>::esz == 1 ? 2 : 1);
+  hipLaunchKernelGGL((matmul_few_rows_kernel<T, O, R, TF, BATCH>), dim3((unsigned)(g.n_nt * g.splits)),
                      dim3(kFewWaves * 64), 0, st, g);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
@@ -770,7 +782,9 @@ hipError_t launch_few_rows(GemmArgs g, hipStream_t st) {
 
 template <typename T, typename O>
 hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
-  if (cfg == kFewRows) return launch_few_rows<T, O, 2, 1>(g, st);
+  if (cfg == kFewRows)
+    return g.M <= 8 ? launch_few_rows<T, O, 2, 1>(g, st)
+                    : (g.M <= 16 ? launch_few_rows<T, O, 2, 2>(g, st) : launch_few_rows<T, O, 4, 4>(g, st));
   constexpr int KT = 128 / Op<T>::esz;
   const int n2 = ((int)((g.K2 + KT - 1) / KT) + 1) & ~1;
   g.stages = n2 + (int)((g.K + KT - 1) / KT);
