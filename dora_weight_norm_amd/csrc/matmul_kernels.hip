@@ -192,9 +192,9 @@ __device__ __forceinline__ void column_terms(const Epilogue& ep, int64_t c, int 
   }
 }
 
-// One operand's share of a stage: R rows of 128 bytes of depth each, staged
-// in LDS by direct loads of 1 KiB (64 lanes x 16 bytes, eight rows). Wave w
-// of NW loads blocks w, w + NW, ...; a lane's offset in block b is off + b *
+// One operand's share of a stage: R rows of 128 bytes of depth each, staged in
+// LDS by direct loads of 1 KiB (64 lanes x 16 bytes, eight rows). Wave w of
+// NW loads blocks w, w + NW, ...; a lane's offset in block b is off + b *
 // step. Rows past the operand lie past the descriptor's end and read zeros.
 struct Stream {
   __amdgpu_buffer_rsrc_t rsrc;
@@ -214,20 +214,31 @@ __device__ __forceinline__ Stream make_stream(const void* p, int64_t ld, int64_t
 
 // ---------------------------------------------------------------------------
 // Tile kernel. Workgroup = WM x WN waves = one tile of (WM MB 32) rows by
-// (WN NB 32) columns over one part of the depth. Each stage is 128 bytes of
-// depth of both operands; two LDS slots alternate, the next stage's direct
-// loads in flight while the matrix cores work on this one.
+// (WN NB 32) columns over one part of the depth. A stage is 128 bytes of depth
+// of both operands. LDS holds a ring of five units of one operand's stage:
+// stage i's rows are in unit 2i mod 5 and its columns in unit 2i + 1. With
+// stage i + 1 and the rows of stage i + 2 already there, the two units that
+// stage i frees take the columns of stage i + 2 first and the rows of stage
+// i + 3 after them: half of the loads have a whole stage to land and half
+// have two. One barrier a stage, where a wave has read all of stage i; a wave
+// holds two sets of fragments and reads the next step's while this step's
+// matrix instructions run.
 // ---------------------------------------------------------------------------
-template <typename T, typename O, int WM, int WN, int MB, int NB>
+constexpr int kUnits = 5;
+
+template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR>
 __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, E = 16 / ESZ, KT = 128 / ESZ;
   constexpr int NW = WM * WN, MT = WM * MB * 32, NT = WN * NB * 32;
-  constexpr int SLOT = (MT + NT) * 128;
+  constexpr int UNIT = (MT > NT ? MT : NT) * 128;           // bytes of a ring unit
   constexpr int ABLK = MT / 8 / NW, BBLK = NT / 8 / NW;   // 1 KiB blocks per wave per stage
+  constexpr int BPW = ABLK + BBLK;
   constexpr int STEPS = 8 / (2 * FC);
   constexpr int EPW = NB * 32 + 8;                         // floats of an epilogue row (padded: no bank conflicts)
   static_assert(MT % (8 * NW) == 0 && NT % (8 * NW) == 0, "a stage splits evenly over the waves");
-  static_assert(NW * 32 * EPW * 4 <= 2 * SLOT, "the epilogue fits the slots");
+  static_assert(NW * 32 * EPW * 4 <= kUnits * UNIT, "the epilogue fits the ring");
+  static_assert(kUnits * UNIT <= 160 * 1024, "gfx950 has 160 KiB of LDS");
+  static_assert(STEPS % 2 == 0, "step s of every stage uses fragment set s & 1");
   extern __shared__ __align__(1024) char lds[];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -250,39 +261,30 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 
   // The lane's chunk of depth in its LDS row is swizzled (by row / 2) so that
   // a fragment read's 16 lanes touch distinct banks.
-  const int lrow = lane >> 3;
-  const int chunk = (lane & 7) ^ (((wave * 8 + lrow) >> 1) & 7);
+  const int chunk = (lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7);
   const Stream sa = make_stream<ESZ, MT, NW>(g.a, g.lda, m0, g.M, lane, wave, chunk);
   const Stream sb = make_stream<ESZ, NT, NW>(g.b, g.ldb, n0, g.N, lane, wave, chunk);
   const Stream sa2 = make_stream<ESZ, MT, NW>(g.a2, g.lda2, m0, g.M, lane, wave, chunk);
   const Stream sb2 = make_stream<ESZ, NT, NW>(g.b2, g.ldb2, n0, g.N, lane, wave, chunk);
-  // Stages: the low-rank pair's first (rounded up to whole pairs of slots,
-  // zeros past its depth), then the main depth's.
-  const int n2 = ((int)((g.K2 + KT - 1) / KT) + 1) & ~1;
+  // Stages: the low-rank pair's first, then the main depth's; this workgroup's
+  // part of them is [st0, st1).
+  const int n2 = PAIR ? (int)((g.K2 + KT - 1) / KT) : 0;
   const int st0 = split * g.stages_per_split;
   const int st1 = st0 + g.stages_per_split < g.stages ? st0 + g.stages_per_split : g.stages;
 
-  auto issue = [&](int i, char* slot) __attribute__((always_inline)) {
-    const bool pr = i < n2;
-    const int64_t k0 = (int64_t)(pr ? i : i - n2) * KT;
-    const int64_t left = (i < st1 ? (pr ? g.K2 : g.K) : 0) - k0;
-    const bool ok = (int64_t)chunk * E < left;
-    const int kb = (int)(k0 * ESZ);
-    const __amdgpu_buffer_rsrc_t ra = pr ? sa2.rsrc : sa.rsrc, rb = pr ? sb2.rsrc : sb.rsrc;
-    const uint32_t oa = pr ? sa2.off : sa.off, ob = pr ? sb2.off : sb.off;
-    const uint32_t pa = pr ? sa2.step : sa.step, pb = pr ? sb2.step : sb.step;
-#pragma unroll
-    for (int b = 0; b < ABLK; ++b) {
-      const uint32_t off = ok ? oa + b * pa : kOob;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          ra, (__attribute__((address_space(3))) void*)(slot + (b * NW + wave) * 1024), 16, off, kb, 0, 0);
-    }
-#pragma unroll
-    for (int b = 0; b < BBLK; ++b) {
-      const uint32_t off = ok ? ob + b * pb : kOob;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (__attribute__((address_space(3))) void*)(slot + MT * 128 + (b * NW + wave) * 1024), 16, off, kb, 0, 0);
-    }
+  // Load b of one operand's stage i into a ring unit. Past the depth every
+  // lane's offset is out of range (zeros), so that every stage issues the same
+  // loads. (Arguments are named before the builtin: a conditional inside its
+  // argument list makes the host pass drop the kernel's stub.)
+  auto issue = [&](const Stream& main, const Stream& pair, int i, int unit, int b) __attribute__((always_inline)) {
+    const bool pr = PAIR && i < n2;
+    const int k0 = (pr ? i : i - n2) * 128;   // bytes of depth before the stage
+    const int left = i < st1 ? (int)((pr ? g.K2 : g.K) * ESZ) - k0 : 0;
+    const uint32_t at = pr ? pair.off + (uint32_t)b * pair.step : main.off + (uint32_t)b * main.step;
+    const uint32_t off = chunk * 16 < left ? at : kOob;
+    const __amdgpu_buffer_rsrc_t rs = pr ? pair.rsrc : main.rsrc;
+    char* dst = lds + unit + (b * NW + wave) * 1024;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, k0, 0, 0);
   };
 
   f32x16 acc[MB][NB];
@@ -294,58 +296,109 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.f;
 
   const int fr = lane & 31, fg = lane >> 5;
-  auto stage = [&](char* slot) __attribute__((always_inline)) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      u32x4 fa[MB][FC], fb[NB][FC];
-#pragma unroll
-      for (int f = 0; f < FC; ++f) {
-        const int c = (((s * 2 + fg) * FC + f) ^ ((fr >> 1) & 7)) * 16;
-#pragma unroll
-        for (int a = 0; a < MB; ++a)
-          fa[a][f] = *reinterpret_cast<const u32x4*>(slot + ((wm * MB + a) * 32 + fr) * 128 + c);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          fb[b][f] = *reinterpret_cast<const u32x4*>(slot + MT * 128 + ((wn * NB + b) * 32 + fr) * 128 + c);
-      }
-#pragma unroll
-      for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[a][b] = Op<T>::run(fa[a], fb[b], acc[a][b]);
-    }
+  struct Frag {
+    u32x4 a[MB][FC], b[NB][FC];
   };
-
-  if (st0 < st1) issue(st0, lds);
-  for (int i = st0; i < st1; i += 2) {
-    if (i == n2 && n2 > 0) {
-#pragma unroll
-      for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[a][b][v] *= g.s;
-    }
-    wait_vm_lgkm0<0>();
-    barrier_keep_loads();   // slot 0 is whole, slot 1 read by every wave
-    issue(i + 1, lds + SLOT);
-    stage(lds);
-    wait_vm_lgkm0<0>();
-    barrier_keep_loads();
-    issue(i + 2, lds);
-    stage(lds + SLOT);
-  }
-  wait_vm_lgkm0<0>();
-  barrier_keep_loads();
-  // (the pair alone: nothing of the main depth came after it)
-  if (n2 > 0 && st0 < n2 && st1 <= n2) {
+  // Read q of a step's (MB + NB) FC fragment pieces, in the order in which the
+  // step's matrix instructions (row blocks outermost) come to need them: the
+  // first row block, the column blocks, the other row blocks.
+  constexpr int ND = (MB + NB) * FC, NM = MB * NB;
+  auto read = [&](int ua, int ub, int s, Frag& F, int q) __attribute__((always_inline)) {
+    const int f = q % FC, w = q / FC;
+    const bool isb = w >= 1 && w <= NB;
+    const int blk = w == 0 ? 0 : (isb ? w - 1 : w - NB);
+    const int c = (((s * 2 + fg) * FC + f) ^ ((fr >> 1) & 7)) * 16;
+    const char* at = isb ? lds + ub + ((wn * NB + blk) * 32 + fr) * 128 + c
+                         : lds + ua + ((wm * MB + blk) * 32 + fr) * 128 + c;
+    if (isb)
+      F.b[blk < NB ? blk : 0][f] = *reinterpret_cast<const u32x4*>(at);
+    else
+      F.a[blk < MB ? blk : 0][f] = *reinterpret_cast<const u32x4*>(at);
+  };
+  auto scale = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[a][b][v] *= g.s;
-  }
+  };
 
+  // One step: its matrix instructions, and between them the next step's
+  // fragment reads (in its first half) and loads [l0, l1) of the period's BPW,
+  // the columns' first. Four waves that issue a stage's loads at once wait for
+  // the address unit for half of the stage. The order is pinned: the compiler
+  // keeps LDS reads and direct loads (which write LDS) in the order of the
+  // source but not the matrix instructions between them.
+  constexpr int RPM = (2 * ND + NM - 1) / NM;
+  Frag F[2];
+  auto step = [&](Frag& cur, Frag& nxt, int ua, int ub, int s, int i, int ul, int um, int l0, int l1)
+      __attribute__((always_inline)) {
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+#pragma unroll
+      for (int q = m * RPM; q < (m + 1) * RPM && q < ND; ++q)
+        read(ua, ub, s, nxt, q);
+#pragma unroll
+      for (int l = l0; l < l1; ++l)
+        if ((l - l0) * NM / (l1 - l0) == m) {
+          if (l < BBLK)
+            issue(sb, sb2, i + 2, ul, l);
+          else
+            issue(sa, sa2, i + 3, um, l - BBLK);
+        }
+      acc[m / NB][m % NB] = Op<T>::run(cur.a[m / NB], cur.b[m % NB], acc[m / NB][m % NB]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Ring units (bytes) of stage i's rows and columns, and of stage i + 1's.
+  int u0 = 0, u1 = UNIT, u2 = 2 * UNIT, u3 = 3 * UNIT, u4 = 4 * UNIT;
+#pragma unroll
+  for (int b = 0; b < ABLK; ++b) issue(sa, sa2, st0, u0, b);
+#pragma unroll
+  for (int b = 0; b < BBLK; ++b) issue(sb, sb2, st0, u1, b);
+#pragma unroll
+  for (int b = 0; b < ABLK; ++b) issue(sa, sa2, st0 + 1, u2, b);
+  // (the columns of the second stage and the rows of the third: one period's
+  // loads, of which the first step's part goes out here)
+  constexpr int L1 = BPW / STEPS;
+#pragma unroll
+  for (int l = 0; l < L1; ++l) {
+    if (l < BBLK)
+      issue(sb, sb2, st0 + 1, u3, l);
+    else
+      issue(sa, sa2, st0 + 2, u4, l - BBLK);
+  }
+  wait_vm_lgkm0<ABLK + L1>();
+  barrier_keep_loads();
+#pragma unroll
+  for (int q = 0; q < ND; ++q) read(u0, u1, 0, F[0], q);
+  // Every matrix instruction stands in this one loop body: with the last
+  // step's outside of it the compiler moved all accumulators between register
+  // files around the loop.
+  auto stage = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s + 1 < STEPS; ++s)
+      step(F[s & 1], F[(s + 1) & 1], u0, u1, s + 1, i - 1, u3, u4, BPW * (s + 1) / STEPS, BPW * (s + 2) / STEPS);
+    // This wave has read all of stage i, and its loads of stage i + 1 have
+    // landed; the rows of stage i + 2 stay in flight. Past the barrier the
+    // units of stage i take the next period's loads.
+    wait_vm_lgkm0<ABLK>();
+    barrier_keep_loads();
+    step(F[1], F[0], u2, u3, 0, i, u0, u1, 0, L1);
+    const int t0 = u0, t1 = u1;
+    u0 = u2, u1 = u3, u2 = u4, u3 = t0, u4 = t1;
+  };
+  int i = st0;
+  if constexpr (PAIR) {
+    if (st0 < n2) {
+      for (; i < n2; ++i) stage(i);
+      scale();
+    }
+  }
+  for (; i < st1; ++i) stage(i);
+  wait_vm_lgkm0<0>();   // (the loads past the depth too: the ring is reused)
+  barrier_keep_loads();
   // Epilogue: each wave turns its accumulators, 32 rows at a time, into rows
   // of eight columns a lane through its own part of LDS, so that loads and
   // stores of the outputs are 16 bytes a lane along a row.
@@ -723,12 +776,13 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
 constexpr int kCUs = 256;
 
 int tile_rows(int cfg) { return cfg == kTile256 ? 256 : (cfg == kTile128 ? 128 : 64); }
+// Elements of a stage's 128 bytes of depth.
 int stage_depth(int dtype) { return dtype == 1 ? 32 : (dtype == 3 ? 128 : 64); }
 int elem_size(int dtype) { return dtype == 1 ? 4 : (dtype == 3 ? 1 : 2); }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-void choose_tile(int64_t M, int64_t N, int64_t stages, int* cfg, int* splits) {
+void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int* cfg, int* splits) {
   if (M <= 32) {
     // One workgroup per 16 columns; the depth is split over workgroups too
     // while they do not fill the chip and each wave keeps four steps.
@@ -740,7 +794,8 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int* cfg, int* splits) {
     return;
   }
   auto tiles = [&](int t) { return up(M, t) / t * (up(N, t) / t); };
-  *cfg = tiles(256) >= 192 ? kTile256 : (tiles(128) >= 128 ? kTile128 : kTile64);
+  // (fp32's matrix instructions are slow enough for the smaller tile's loads)
+  *cfg = tiles(256) >= 192 && dtype != 1 ? kTile256 : (tiles(128) >= 128 ? kTile128 : kTile64);
   const int64_t n = tiles(tile_rows(*cfg));
   // Fewer tiles than compute units: split the depth, at least 8 stages each.
   int64_t s = n >= kCUs || n < 1 ? 1 : kCUs / n;
@@ -749,13 +804,13 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int* cfg, int* splits) {
   *splits = (int)(s < 1 ? 1 : s);
 }
 
-template <typename T, typename O, int WM, int WN, int MB, int NB>
+template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR>
 hipError_t launch_tile(GemmArgs g, hipStream_t st) {
   constexpr int MT = WM * MB * 32, NT = WN * NB * 32;
   g.n_mt = (int)((g.M + MT - 1) / MT);
   g.n_nt = (int)((g.N + NT - 1) / NT);
-  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB>;
-  constexpr int lds = 2 * (MT + NT) * 128;
+  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB, PAIR>;
+  constexpr int lds = kUnits * (MT > NT ? MT : NT) * 128;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k, dim3((unsigned)((int64_t)g.n_mt * g.n_nt * g.splits)), dim3(WM * WN * 64), lds, st, g);
@@ -786,19 +841,31 @@ hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
     return g.M <= 8 ? launch_few_rows<T, O, 2, 1>(g, st)
                     : (g.M <= 16 ? launch_few_rows<T, O, 2, 2>(g, st) : launch_few_rows<T, O, 4, 4>(g, st));
   constexpr int KT = 128 / Op<T>::esz;
-  const int n2 = ((int)((g.K2 + KT - 1) / KT) + 1) & ~1;
+  const int n2 = (int)((g.K2 + KT - 1) / KT);
   g.stages = n2 + (int)((g.K + KT - 1) / KT);
-  const int per = ((g.stages + g.splits - 1) / g.splits + 1) & ~1;   // whole pairs of slots
+  if (g.stages < 1) g.stages = 1;   // (no depth at all: one stage of zeros)
   // The low-rank stages and their scaling belong to the first part alone.
+  const int per = (g.stages + g.splits - 1) / g.splits;
   g.stages_per_split = per > n2 ? per : n2;
-  if (g.stages_per_split < 2) g.stages_per_split = 2;
   g.splits = (g.stages + g.stages_per_split - 1) / g.stages_per_split;
-  if (g.splits < 1) g.splits = 1;
-  hipError_t e;
-  switch (cfg) {
-    case kTile256: e = launch_tile<T, O, 2, 4, 4, 2>(g, st); break;
-    case kTile128: e = launch_tile<T, O, 2, 2, 2, 2>(g, st); break;
-    default: e = launch_tile<T, O, 2, 2, 1, 1>(g, st); break;
+  hipError_t e = hipErrorInvalidValue;
+  if (g.K2 > 0) {
+    if constexpr (Op<T>::esz > 1) {   // (no pair in e4m3)
+      if constexpr (Op<T>::esz == 2) {
+        if (cfg == kTile256) e = launch_tile<T, O, 2, 4, 4, 2, true>(g, st);
+      }
+      if (cfg == kTile128) e = launch_tile<T, O, 2, 2, 2, 2, true>(g, st);
+      if (cfg == kTile64) e = launch_tile<T, O, 2, 2, 1, 1, true>(g, st);
+    }
+  } else {
+    if constexpr (Op<T>::esz == 2) {
+      if (cfg == kTile256) e = launch_tile<T, O, 2, 4, 4, 2, false>(g, st);
+    }
+    if constexpr (Op<T>::esz == 1) {
+      if (cfg == kTile256) e = launch_tile<T, O, 2, 2, 4, 4, false>(g, st);
+    }
+    if (cfg == kTile128) e = launch_tile<T, O, 2, 2, 2, 2, false>(g, st);
+    if (cfg == kTile64) e = launch_tile<T, O, 2, 2, 1, 1, false>(g, st);
   }
   return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
 }
@@ -850,7 +917,7 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   MatmulPlan p{};
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
-  choose_tile(M, N, up(K, KT) / KT, &p.cfg, &p.splits);
+  choose_tile(M, N, up(K, KT) / KT, dtype, &p.cfg, &p.splits);
   auto operand = [&](int64_t rows, int64_t depth, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
     *pack = p.cfg != kFewRows && depth > 0 && (depth % epc != 0 || !(al & bit));
@@ -919,11 +986,11 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.off_xt = take(need_dw ? (size_t)(K * p.ldm) * esz : 0);
   size_t part = 0;
   if (need_dx) {
-    choose_tile(M, K, up(N, KT) / KT, &p.cfg_dx, &p.splits_dx);
+    choose_tile(M, K, up(N, KT) / KT, dtype, &p.cfg_dx, &p.splits_dx);
     if (p.splits_dx > 1) part = (size_t)(p.splits_dx * M * K) * 4;
   }
   if (need_dw) {
-    choose_tile(N, K, up(M, KT) / KT, &p.cfg_dw, &p.splits_dw);
+    choose_tile(N, K, up(M, KT) / KT, dtype, &p.cfg_dw, &p.splits_dw);
     const size_t q = p.splits_dw > 1 ? (size_t)(p.splits_dw * N * K) * 4 : 0;
     part = q > part ? q : part;
   }
