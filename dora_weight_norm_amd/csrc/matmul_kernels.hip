@@ -71,7 +71,13 @@ struct Op<e4m3_t> {
 constexpr float kTanhK = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kTanhC = 0.044715f;
 
-__device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + expf(-v)); }
+// 1 / (1 + e^-v) by the hardware's exponential of base two and reciprocal (one
+// unit in the last place each; the product with log2(e) adds |v| 2^-24
+// relative): a correctly rounded division and expf cost the epilogue of the
+// 8192 x 28672 product about as much again as its stores.
+__device__ __forceinline__ float logistic(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896f * v));
+}
 
 __device__ __forceinline__ float act1(float z, int act) {
   switch (act) {
@@ -83,18 +89,19 @@ __device__ __forceinline__ float act1(float z, int act) {
   }
 }
 
-// Eight values at once, so that the (uniform) choice is made once.
-__device__ __forceinline__ void act8(float (&z)[8], int act) {
+// N values at once, so that the (uniform) choice is made once.
+template <int N>
+__device__ __forceinline__ void act_all(float (&z)[N], int act) {
   switch (act) {
-#define DORA_ACT8(A)                                     \
+#define DORA_ACT(A)                                      \
   case A:                                                \
-    for (int e = 0; e < 8; ++e) z[e] = act1(z[e], A);    \
+    for (int e = 0; e < N; ++e) z[e] = act1(z[e], A);    \
     break;
-    DORA_ACT8(1)
-    DORA_ACT8(2)
-    DORA_ACT8(3)
-    DORA_ACT8(4)
-#undef DORA_ACT8
+    DORA_ACT(1)
+    DORA_ACT(2)
+    DORA_ACT(3)
+    DORA_ACT(4)
+#undef DORA_ACT
     default: break;
   }
 }
@@ -115,22 +122,43 @@ __device__ __forceinline__ float slope_of(float z, int act) {
   }
 }
 
-// Eight consecutive elements of an output row, in the output type.
+// Eight consecutive elements of an output row in the output type, as loaded.
 template <typename O>
-__device__ __forceinline__ void load8(const O* p, int n, float (&f)[8]) {
+struct Raw8 {
+  u32x4 v[8 / Elem<O>::epc];
+};
+
+template <typename O>
+__device__ __forceinline__ Raw8<O> load_raw8(const O* p, int n) {
   constexpr int E = Elem<O>::epc;
+  Raw8<O> r;
   if (n >= 8) {
 #pragma unroll
-    for (int i = 0; i < 8 / E; ++i) {
-      float g[E];
-      unpack<O, E>(*reinterpret_cast<const u32x4_any*>(p + i * E), g);
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[i * E + e] = g[e];
-    }
+    for (int i = 0; i < 8 / E; ++i) r.v[i] = *reinterpret_cast<const u32x4_any*>(p + i * E);
   } else {
+    O tmp[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = e < n ? to_f32(p[e]) : 0.f;
+    for (int e = 0; e < 8; ++e) tmp[e] = e < n ? p[e] : O(0);
+    __builtin_memcpy(&r, tmp, sizeof(r));
   }
+  return r;
+}
+
+template <typename O>
+__device__ __forceinline__ void unpack8(const Raw8<O>& r, float (&f)[8]) {
+  constexpr int E = Elem<O>::epc;
+#pragma unroll
+  for (int i = 0; i < 8 / E; ++i) {
+    float g[E];
+    unpack<O, E>(r.v[i], g);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[i * E + e] = g[e];
+  }
+}
+
+template <typename O>
+__device__ __forceinline__ void load8(const O* p, int n, float (&f)[8]) {
+  unpack8<O>(load_raw8<O>(p, n), f);
 }
 
 template <typename O>
@@ -151,27 +179,44 @@ __device__ __forceinline__ void store8(O* p, int n, const float (&f)[8]) {
   }
 }
 
-// The epilogue on eight consecutive columns of one row; cs and bs are their
-// column scales and biases, n how many of them exist.
-template <typename O>
-__device__ __forceinline__ void epilogue8(const Epilogue& ep, float (&v)[8], const float (&cs)[8],
-                                          const float (&bs)[8], int64_t m, int64_t off, int n) {
+// The epilogue on eight consecutive columns of R rows: row m[i] at offset
+// off[i] if ok[i]; cs and bs are the columns' scales and biases, n how many of
+// them exist, res the rows' residual (already loaded).
+template <typename O, int R>
+__device__ __forceinline__ void epilogue_rows(const Epilogue& ep, float (&v)[8 * R], const float (&cs)[8],
+                                              const float (&bs)[8], const int64_t (&m)[R], const int64_t (&off)[R],
+                                              const bool (&ok)[R], int n, const Raw8<O> (&res)[R]) {
   if (ep.row_scale) {
-    const float rs = ep.row_scale[m];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= rs;
+    for (int i = 0; i < R; ++i) {
+      const float rs = ok[i] ? ep.row_scale[m[i]] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * i + e] *= rs;
+    }
   }
-  if (ep.u) store8<O>(static_cast<O*>(ep.u) + off, n, v);
+  auto put = [&](void* to) __attribute__((always_inline)) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = fmaf(cs[e], v[e], bs[e]);
-  act8(v, ep.act);
+    for (int i = 0; i < R; ++i) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = v[8 * i + e];
+      if (ok[i]) store8<O>(static_cast<O*>(to) + off[i], n, o);
+    }
+  };
+  if (ep.u) put(ep.u);
+#pragma unroll
+  for (int e = 0; e < 8 * R; ++e) v[e] = fmaf(cs[e % 8], v[e], bs[e % 8]);
+  act_all<8 * R>(v, ep.act);
   if (ep.residual) {
-    float r[8];
-    load8<O>(static_cast<const O*>(ep.residual) + off, n, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += r[e];
+    for (int i = 0; i < R; ++i) {
+      float r[8];
+      unpack8<O>(res[i], r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * i + e] += r[e];
+    }
   }
-  store8<O>(static_cast<O*>(ep.y) + off, n, v);
+  put(ep.y);
 }
 
 // The epilogue on one element.
@@ -184,12 +229,13 @@ __device__ __forceinline__ void epilogue1(const Epilogue& ep, float v, float cs,
   static_cast<O*>(ep.y)[off] = from_f32<O>(v);
 }
 
+// Eight column scales and biases from column c on, n of them there.
 __device__ __forceinline__ void column_terms(const Epilogue& ep, int64_t c, int n, float (&cs)[8], float (&bs)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = (ep.col_scale && e < n) ? ep.col_scale[c + e] : 1.f;
-    bs[e] = (ep.bias && e < n) ? ep.bias[c + e] : 0.f;
-  }
+  for (int e = 0; e < 8; ++e) cs[e] = 1.f, bs[e] = 0.f;
+  if (n <= 0) return;
+  if (ep.col_scale) load8<float>(ep.col_scale + c, n, cs);
+  if (ep.bias) load8<float>(ep.bias + c, n, bs);
 }
 
 // One operand's share of a stage: R rows of 128 bytes of depth each, staged in
@@ -286,6 +332,15 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
     char* dst = lds + unit + (b * NW + wave) * 1024;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, k0, 0, 0);
   };
+
+  // The epilogue's columns of this lane: their scales and biases are asked for
+  // here, a whole depth before they are needed.
+  constexpr int LPR = NB * 4, RPP = 64 / LPR, PB = 32 / RPP;   // lanes a row, rows a pass, passes a block
+  const int col = (lane % LPR) * 8;
+  const int64_t n = n0 + wn * NB * 32 + col;
+  const int nv = (int)(g.N - n < 8 ? g.N - n : 8);
+  float cs[8], bs[8];
+  column_terms(g.ep, n, nv, cs, bs);
 
   f32x16 acc[MB][NB];
 #pragma unroll
@@ -403,41 +458,64 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // of eight columns a lane through its own part of LDS, so that loads and
   // stores of the outputs are 16 bytes a lane along a row.
   float* ew = reinterpret_cast<float*>(lds) + wave * 32 * EPW;
-  constexpr int LPR = NB * 4, RPP = 64 / LPR;
-  const int col = (lane % LPR) * 8;
-  const int64_t n = n0 + wn * NB * 32 + col;
-  const int nv = (int)(g.N - n < 8 ? g.N - n : 8);
-  float cs[8], bs[8];
-  column_terms(g.ep, n, nv, cs, bs);
-  // (One copy of the epilogue's code: the blocks of 32 rows are taken in a
-  // real loop, and the accumulators are named by constants in a chain of
-  // uniform branches, since registers cannot be indexed.)
-#pragma unroll 1
-  for (int a = 0; a < MB; ++a) {
+  // The epilogue's code is one real loop over pairs of passes: unrolled, its
+  // instructions were fetched anew by every tile, which cost more than the
+  // loop. The accumulators are named by constants in a chain of uniform
+  // branches, since registers cannot be indexed. The residual's rows are
+  // loaded one pass ahead.
+  constexpr int IT = MB * PB / 2;
+  const bool has_res = g.ep.residual != nullptr && g.splits == 1;
+  auto row_of = [&](int it, int i) __attribute__((always_inline)) {
+    return m0 + (wm * MB + it / (PB / 2)) * 32 + ((it % (PB / 2)) * 2 + i) * RPP + lane / LPR;
+  };
+  Raw8<O> next[2] = {};
+  auto load_res = [&](int it) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < MB; ++c) {
-      if (c != a) continue;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) ew[acc_row(v, fg) * EPW + b * 32 + fr] = acc[c][b][v];
+    for (int i = 0; i < 2; ++i) {
+      const int64_t m = row_of(it, i);
+      if (m < g.M && nv > 0) next[i] = load_raw8<O>(static_cast<const O*>(g.ep.residual) + m * g.N + n, nv);
     }
-    __builtin_amdgcn_wave_barrier();
+  };
+  if (has_res) load_res(0);
 #pragma unroll 1
-    for (int p = 0; p < 32 / RPP; ++p) {
-      const int row = p * RPP + lane / LPR;
-      const int64_t m = m0 + (wm * MB + a) * 32 + row;
-      float v[8];
+  for (int it = 0; it < IT; ++it) {
+    const Raw8<O> res[2] = {next[0], next[1]};
+    if (has_res && it + 1 < IT) load_res(it + 1);
+    if (it % (PB / 2) == 0) {
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = ew[row * EPW + col + e];
-      if (m < g.M && nv > 0) {
-        if (g.splits > 1)
-          store8<float>(g.part + ((int64_t)split * g.M + m) * g.N + n, nv, v);
-        else
-          epilogue8<O>(g.ep, v, cs, bs, m, m * g.N + n, nv);
+      for (int c = 0; c < MB; ++c) {
+        if (c != it / (PB / 2)) continue;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) ew[acc_row(v, fg) * EPW + b * 32 + fr] = acc[c][b][v];
       }
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
+    float v[16];
+    int64_t m[2], off[2];
+    bool ok[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = ((it % (PB / 2)) * 2 + i) * RPP + lane / LPR;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * i + e] = ew[row * EPW + col + e];
+      m[i] = row_of(it, i);
+      off[i] = m[i] * g.N + n;
+      ok[i] = m[i] < g.M && nv > 0;
+    }
+    if (g.splits > 1) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v[8 * i + e];
+        if (ok[i]) store8<float>(g.part + (int64_t)split * g.M * g.N + off[i], nv, o);
+      }
+    } else {
+      epilogue_rows<O, 2>(g.ep, v, cs, bs, m, off, ok, nv, res);
+    }
   }
 }
 
@@ -665,7 +743,12 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(GemmArgs g) {
   }
   float cs[8], bs[8];
   column_terms(g.ep, n, nv, cs, bs);
-  epilogue8<O>(g.ep, v, cs, bs, m, m * g.N + n, nv);
+  const int64_t off = m * g.N + n;
+  Raw8<O> res[1] = {};
+  if (g.ep.residual) res[0] = load_raw8<O>(static_cast<const O*>(g.ep.residual) + off, nv);
+  const int64_t ms[1] = {m}, offs[1] = {off};
+  const bool ok[1] = {true};
+  epilogue_rows<O, 1>(g.ep, v, cs, bs, ms, offs, ok, nv, res);
 }
 
 // Copy of [rows][K] (row stride K, any alignment) to row stride ld (a
