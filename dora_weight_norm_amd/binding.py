@@ -446,44 +446,72 @@ _TORCH_DT = {torch.bfloat16: DORA_BF16, torch.float32: DORA_F32, torch.float16: 
 _E4M3 = torch.float8_e4m3fn
 
 
-def _want(t, name: str, shape, dtype, device):
-    """`t` is a contiguous tensor of exactly this shape, dtype and device."""
+# A call of a single token takes the GPU a few microseconds, so the checks below
+# cost as little as they can: one pass of plain comparisons a tensor, the
+# device as its index, and messages only where a check fails.
+def _refuse(t, name: str, shape, dtype, dev: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _first(t, name: str, dims: int = 2):
-    """The tensor a call takes its shapes, dtype and device from."""
+def _want(t, name: str, shape, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of exactly this shape, dtype and GPU."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_cuda
+            or t.get_device() != dev or not t.is_contiguous()):
+        _refuse(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _maybe(t, name: str, shape, dtype, dev: int):
+    return None if t is None else _want(t, name, shape, dtype, dev)
+
+
+def _first(t, name: str) -> int:
+    """The GPU of the 2-D tensor that a call takes its shapes and dtype from."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device, got {t.device}")
-    if t.dim() != dims or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and {dims}-D, got {tuple(t.shape)}")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and 2-D, got {tuple(t.shape)}")
+    return t.get_device()
 
 
-def _vec(t, name: str, n: int, device):
-    if t is not None:
-        _want(t, name, (n,), torch.float32, device)
+def _type_code(dtype) -> int:
+    code = _TORCH_DT.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; libdora takes bfloat16, float16 or float32")
+    return code
 
 
-def _new(shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device)
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _new(stream, shape, dtype, dev: int):
+    """A tensor that belongs to `stream` (see _on)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _space(workspace, need: int, stream, dev: int):
+    """The caller's workspace, checked, or a new one; None where none is needed."""
+    if workspace is not None:
+        _workspace(workspace, "workspace", need, torch.device("cuda", dev))
+        return workspace
+    return _new(stream, (need,), torch.uint8, dev) if need > 0 else None
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream, device):
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=4096)
@@ -509,38 +537,31 @@ def dora_matmul_backward_workspace_size(M: int, N: int, K: int, dtype, outputs: 
 
 
 def _rms_norm(x, weight, eps, residual, h, rstd, want_rstd, stream, y=None, q=None, scale=None, quant=False):
-    _first(x, "x")
-    dt = _TORCH_DT.get(x.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {x.dtype}; libdora takes bfloat16, float16 or float32")
-    shape, dev = x.shape, x.device
+    dev, dtype, shape = _first(x, "x"), x.dtype, x.shape
+    code = _type_code(dtype)
     T, d = shape
-    _vec(weight, "weight", d, dev)
-    if residual is not None:
-        _want(residual, "residual", shape, x.dtype, dev)
-        if h is not None:
-            _want(h, "h", shape, x.dtype, dev)
-    elif h is not None:
+    f32 = torch.float32
+    pw = _maybe(weight, "weight", (d,), f32, dev)
+    pres = _maybe(residual, "residual", shape, dtype, dev)
+    if h is not None and residual is None:
         raise ValueError("h needs a residual (without one, h is x)")
-    _vec(rstd, "rstd", T, dev)
+    ph = _maybe(h, "h", shape, dtype, dev)
+    prs = _maybe(rstd, "rstd", (T,), f32, dev)
+    if residual is not None and h is None:
+        h = _new(stream, shape, dtype, dev)
+        ph = h.data_ptr()
+    if rstd is None and want_rstd:
+        rstd = _new(stream, (T,), f32, dev)
+        prs = rstd.data_ptr()
+    py = pq = ps = None
     if quant:
-        if q is not None:
-            _want(q, "q", shape, _E4M3, dev)
-        _vec(scale, "scale", T, dev)
-    elif y is not None:
-        _want(y, "y", shape, x.dtype, dev)
-    with _on(stream):
-        if residual is not None and h is None:
-            h = _new(shape, x.dtype, dev)
-        if rstd is None and want_rstd:
-            rstd = _new((T,), torch.float32, dev)
-        if quant:
-            q = _new(shape, _E4M3, dev) if q is None else q
-            scale = _new((T,), torch.float32, dev) if scale is None else scale
-        else:
-            y = _new(shape, x.dtype, dev) if y is None else y
-        _call("dora_rms_norm", _addr(x), _addr(residual), _addr(weight), eps, dt, T, d, _addr(h), _addr(y), _addr(q),
-              _addr(scale), _addr(rstd), _raw_stream(stream, dev))
+        q = _new(stream, shape, _E4M3, dev) if q is None else q
+        scale = _new(stream, (T,), f32, dev) if scale is None else scale
+        pq, ps = _want(q, "q", shape, _E4M3, dev), _want(scale, "scale", (T,), f32, dev)
+    else:
+        y = _new(stream, shape, dtype, dev) if y is None else y
+        py = _want(y, "y", shape, dtype, dev)
+    _call("dora_rms_norm", x.data_ptr(), pres, pw, eps, code, T, d, ph, py, pq, ps, prs, _raw_stream(stream, dev))
     return y, q, scale, (x if residual is None else h), rstd
 
 
@@ -570,34 +591,22 @@ def dora_rms_norm_backward(dy, h, rstd, weight, dh=None, need_dweight: bool = Tr
     """Gradients of dora_rms_norm from its h and rstd. Returns (dx, dweight):
     dx is the gradient of x and of the residual, dh (optional) what reaches h
     directly is added to it; dweight float32 [d], None if not needed."""
-    _first(dy, "dy")
-    dt = _TORCH_DT.get(dy.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {dy.dtype}; libdora takes bfloat16, float16 or float32")
-    shape, dev = dy.shape, dy.device
+    dev, dtype, shape = _first(dy, "dy"), dy.dtype, dy.shape
+    code = _type_code(dtype)
     T, d = shape
-    _want(h, "h", shape, dy.dtype, dev)
-    _want(rstd, "rstd", (T,), torch.float32, dev)
-    _vec(weight, "weight", d, dev)
-    if dh is not None:
-        _want(dh, "dh", shape, dy.dtype, dev)
-    if dx is not None:
-        _want(dx, "dx", shape, dy.dtype, dev)
-    if dweight is not None:
-        if not need_dweight:
-            raise ValueError("dweight given but need_dweight is False")
-        _vec(dweight, "dweight", d, dev)
-    need = dora_rms_norm_backward_workspace_size(T, d, dt) if need_dweight else 0
-    if workspace is not None:
-        _workspace(workspace, "workspace", need, dev)
-    with _on(stream):
-        dx = _new(shape, dy.dtype, dev) if dx is None else dx
-        if need_dweight and dweight is None:
-            dweight = _new((d,), torch.float32, dev)
-        if workspace is None and need > 0:
-            workspace = _new((need,), torch.uint8, dev)
-        _call("dora_rms_norm_backward", _addr(dy), _addr(dh), _addr(h), _addr(rstd), _addr(weight), dt, T, d,
-              _addr(dx), _addr(dweight), _addr(workspace), need, _raw_stream(stream, dev))
+    f32 = torch.float32
+    ph, prs = _want(h, "h", shape, dtype, dev), _want(rstd, "rstd", (T,), f32, dev)
+    pw, pdh = _maybe(weight, "weight", (d,), f32, dev), _maybe(dh, "dh", shape, dtype, dev)
+    if dweight is not None and not need_dweight:
+        raise ValueError("dweight given but need_dweight is False")
+    need = dora_rms_norm_backward_workspace_size(T, d, code) if need_dweight else 0
+    dx = _new(stream, shape, dtype, dev) if dx is None else dx
+    if need_dweight and dweight is None:
+        dweight = _new(stream, (d,), f32, dev)
+    pdx, pdw = _want(dx, "dx", shape, dtype, dev), _maybe(dweight, "dweight", (d,), f32, dev)
+    workspace = _space(workspace, need, stream, dev)
+    _call("dora_rms_norm_backward", dy.data_ptr(), pdh, ph, prs, pw, code, T, d, pdx, pdw, _addr(workspace), need,
+          _raw_stream(stream, dev))
     return dx, dweight
 
 
@@ -619,21 +628,21 @@ def dora_matmul(x, w, row_scale=None, col_scale=None, t=None, b=None, s: float =
     gelu_tanh or silu. Returns (y, u); u, the product that the backward
     takes, is None unless `save` (or a buffer for it) is given.
     """
-    _first(x, "x")
-    e8 = x.dtype == _E4M3
-    dt = DORA_E4M3 if e8 else _TORCH_DT.get(x.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {x.dtype}; libdora takes bfloat16, float16, float32 or float8_e4m3fn")
-    dev = x.device
+    dev, dtype = _first(x, "x"), x.dtype
+    e8 = dtype is _E4M3
+    code = DORA_E4M3 if e8 else _TORCH_DT.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; libdora takes bfloat16, float16, float32 or float8_e4m3fn")
     M, K = x.shape
     _first(w, "w")
     N = w.shape[0]
-    _want(w, "w", (N, K), x.dtype, dev)
-    odt = out_dtype if out_dtype is not None else (torch.bfloat16 if e8 else x.dtype)
-    oc = _TORCH_DT.get(odt)
-    if oc is None or (not e8 and odt != x.dtype):
-        raise TypeError(f"out_dtype {odt} does not go with {x.dtype}")
-    r = 0
+    px, pw = x.data_ptr(), _want(w, "w", (N, K), dtype, dev)
+    odt = out_dtype if out_dtype is not None else (torch.bfloat16 if e8 else dtype)
+    out_code = _TORCH_DT.get(odt)
+    if out_code is None or (not e8 and odt is not dtype):
+        raise TypeError(f"out_dtype {odt} does not go with {dtype}")
+    r, pt, pb = 0, None, None
+    al = ((px & 15) == 0) | ((pw & 15) == 0) << 1
     if t is not None or b is not None:
         if t is None or b is None:
             raise ValueError("t and b come together")
@@ -641,34 +650,21 @@ def dora_matmul(x, w, row_scale=None, col_scale=None, t=None, b=None, s: float =
             raise TypeError("a low-rank pair does not go with float8 operands")
         _first(t, "t")
         r = t.shape[1]
-        _want(t, "t", (M, r), x.dtype, dev)
-        _want(b, "b", (N, r), x.dtype, dev)
-    if row_scale is not None:
-        _want(row_scale, "row_scale", (M,), torch.float32, dev)
-    _vec(col_scale, "col_scale", N, dev)
-    _vec(bias, "bias", N, dev)
-    if residual is not None:
-        _want(residual, "residual", (M, N), odt, dev)
-    if y is not None:
-        _want(y, "y", (M, N), odt, dev)
-    if u is not None:
-        _want(u, "u", (M, N), odt, dev)
-    code = _act(act)
-    px, pw, pt, pb = x.data_ptr(), w.data_ptr(), _addr(t), _addr(b)
-    al = ((px & 15) == 0) | ((pw & 15) == 0) << 1
-    if r:
+        pt, pb = _want(t, "t", (M, r), dtype, dev), _want(b, "b", (N, r), dtype, dev)
         al |= ((pt & 15) == 0) << 2 | ((pb & 15) == 0) << 3
-    need = _size_of("dora_matmul_workspace_size", M, N, K, r, dt, al)
-    if workspace is not None:
-        _workspace(workspace, "workspace", need, dev)
-    with _on(stream):
-        y = _new((M, N), odt, dev) if y is None else y
-        if u is None and save:
-            u = _new((M, N), odt, dev)
-        if workspace is None and need > 0:
-            workspace = _new((need,), torch.uint8, dev)
-        _call("dora_matmul", px, pw, dt, M, N, K, _addr(row_scale), _addr(col_scale), pt, pb, r, s, _addr(bias), code,
-              _addr(residual), oc, _addr(y), _addr(u), _addr(workspace), need, _raw_stream(stream, dev))
+    f32, out = torch.float32, (M, N)
+    prow = _maybe(row_scale, "row_scale", (M,), f32, dev)
+    pcol, pbias = _maybe(col_scale, "col_scale", (N,), f32, dev), _maybe(bias, "bias", (N,), f32, dev)
+    pres = _maybe(residual, "residual", out, odt, dev)
+    act_code = _act(act)
+    need = _size_of("dora_matmul_workspace_size", M, N, K, r, code, al)
+    y = _new(stream, out, odt, dev) if y is None else y
+    if u is None and save:
+        u = _new(stream, out, odt, dev)
+    py, pu = _want(y, "y", out, odt, dev), _maybe(u, "u", out, odt, dev)
+    workspace = _space(workspace, need, stream, dev)
+    _call("dora_matmul", px, pw, code, M, N, K, prow, pcol, pt, pb, r, s, pbias, act_code, pres, out_code, py, pu,
+          _addr(workspace), need, _raw_stream(stream, dev))
     return y, u
 
 
@@ -685,41 +681,34 @@ def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "non
     gradient of u. x is read for dw and w for dx; either may be None where
     its product is not needed, but not both. The residual's gradient is dy.
     """
-    _first(dy, "dy")
-    dt = _TORCH_DT.get(dy.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {dy.dtype}; libdora takes bfloat16, float16 or float32")
-    dev = dy.device
-    M, N = dy.shape
-    _want(u, "u", (M, N), dy.dtype, dev)
+    dev, dtype = _first(dy, "dy"), dy.dtype
+    code = _type_code(dtype)
+    M, N = out = dy.shape
+    pu = _want(u, "u", out, dtype, dev)
     if need_dx and w is None or need_dw and x is None:
         raise ValueError("dx needs w, and dw needs x")
     K = 0
     if x is not None:
         _first(x, "x")
         K = x.shape[1]
-        _want(x, "x", (M, K), dy.dtype, dev)
+        _want(x, "x", (M, K), dtype, dev)
     if w is not None:
         _first(w, "w")
         K = w.shape[1] if x is None else K
-        _want(w, "w", (N, K), dy.dtype, dev)
-    _vec(col_scale, "col_scale", N, dev)
-    _vec(bias, "bias", N, dev)
-    code = _act(act)
-    with _on(stream):
-        du = _new((M, N), dy.dtype, dev)
-        dx = _new((M, K), dy.dtype, dev) if need_dx else None
-        dw = _new((N, K), dy.dtype, dev) if need_dw else None
-        dbias = _new((N,), torch.float32, dev) if need_dbias else None
-        dcol = _new((N,), torch.float32, dev) if need_dcol_scale else None
-        outputs = (GRAD_DX * need_dx + GRAD_DW * need_dw + GRAD_SUMS * (need_dbias or need_dcol_scale)
-                   + GRAD_DU * (du.data_ptr() % 16 == 0))
-        need = _size_of("dora_matmul_backward_workspace_size", M, N, K, dt, outputs)
-        if workspace is not None:
-            _workspace(workspace, "workspace", need, dev)
-        elif need > 0:
-            workspace = _new((need,), torch.uint8, dev)
-        _call("dora_matmul_backward", _addr(dy), _addr(u), _addr(x) if need_dw else None,
-              _addr(w) if need_dx else None, dt, M, N, K, _addr(col_scale), _addr(bias), code, _addr(du), _addr(dx),
-              _addr(dw), _addr(dbias), _addr(dcol), _addr(workspace), need, _raw_stream(stream, dev))
+        _want(w, "w", (N, K), dtype, dev)
+    f32 = torch.float32
+    pcol, pbias = _maybe(col_scale, "col_scale", (N,), f32, dev), _maybe(bias, "bias", (N,), f32, dev)
+    act_code = _act(act)
+    du = _new(stream, out, dtype, dev)
+    dx = _new(stream, (M, K), dtype, dev) if need_dx else None
+    dw = _new(stream, (N, K), dtype, dev) if need_dw else None
+    dbias = _new(stream, (N,), f32, dev) if need_dbias else None
+    dcol = _new(stream, (N,), f32, dev) if need_dcol_scale else None
+    outputs = (GRAD_DX * need_dx + GRAD_DW * need_dw + GRAD_SUMS * (need_dbias or need_dcol_scale)
+               + GRAD_DU * (du.data_ptr() % 16 == 0))
+    need = _size_of("dora_matmul_backward_workspace_size", M, N, K, code, outputs)
+    workspace = _space(workspace, need, stream, dev)
+    _call("dora_matmul_backward", dy.data_ptr(), pu, _addr(x) if need_dw else None, _addr(w) if need_dx else None,
+          code, M, N, K, pcol, pbias, act_code, _addr(du), _addr(dx), _addr(dw), _addr(dbias), _addr(dcol),
+          _addr(workspace), need, _raw_stream(stream, dev))
     return dx, dw, dbias, dcol, du

@@ -876,15 +876,33 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int* cfg, int*
     *splits = (int)(s < 1 ? 1 : s);
     return;
   }
-  auto tiles = [&](int t) { return up(M, t) / t * (up(N, t) / t); };
-  // (fp32's matrix instructions are slow enough for the smaller tile's loads)
-  *cfg = tiles(256) >= 192 && dtype != 1 ? kTile256 : (tiles(128) >= 128 ? kTile128 : kTile64);
-  const int64_t n = tiles(tile_rows(*cfg));
-  // Fewer tiles than compute units: split the depth, at least 8 stages each.
-  int64_t s = n >= kCUs || n < 1 ? 1 : kCUs / n;
-  if (s > stages / 8) s = stages / 8;
-  if (s > 32) s = 32;
-  *splits = (int)(s < 1 ? 1 : s);
+  // The tile and the split that a model of the time puts first, in cycles. A
+  // compute unit holds 1, 2 or 4 workgroups of 256-, 128- or 64-row tiles; a
+  // stage of each costs it t^2 / 32 of matrix instructions (fp32: 16 times
+  // that) or 4 t of loads, and a workgroup waits about kStageWait for a stage
+  // from memory (measured: 1500 to 1900 cycles a stage where 256 workgroups of
+  // either small tile run, whatever the tile). The parts of a split are added
+  // by a second launch that reads them all.
+  constexpr double kStageWait = 1600, kTileFixed = 8000, kJoinFixed = 12000, kBytesPerCycle = 2000;
+  double best = 0;
+  *cfg = kTile64, *splits = 1;
+  for (int c = kTile256; c <= kTile64; ++c) {
+    if (c == kTile256 && dtype == 1) continue;   // (fp32 has no such kernel: its matrix instructions are slow)
+    const int t = tile_rows(c), fit = c == kTile256 ? 1 : (c == kTile128 ? 2 : 4);
+    const int64_t n = up(M, t) / t * (up(N, t) / t);
+    const double work = (dtype == 1 ? 16.0 : 1.0) * t * t / 32, load = 4.0 * t, busy = work > load ? work : load;
+    for (int s = 1; s <= 32 && (s == 1 || s <= stages / 4); ++s) {
+      const int64_t groups = n * s, rounds = (groups + kCUs * fit - 1) / (kCUs * fit);
+      const int64_t last = groups - (rounds - 1) * kCUs * fit;   // workgroups of the last round
+      auto round = [&](int64_t g) {
+        const double here = (double)((g + kCUs - 1) / kCUs) * busy;
+        return (double)((stages + s - 1) / s) * (here > kStageWait ? here : kStageWait) + kTileFixed;
+      };
+      double time = (double)(rounds - 1) * round((int64_t)kCUs * fit) + round(last);
+      if (s > 1) time += kJoinFixed + 8.0 * s * (double)M * (double)N / kBytesPerCycle;
+      if (best == 0 || time < best) best = time, *cfg = c, *splits = s;
+    }
+  }
 }
 
 template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR>
