@@ -531,8 +531,8 @@ def dora_matmul_workspace_size(M: int, N: int, K: int, r: int, dtype, aligned_op
     return _size_of("dora_matmul_workspace_size", M, N, K, r, code, aligned_operands)
 
 
-def dora_matmul_backward_workspace_size(M: int, N: int, K: int, dtype, outputs: int = 15) -> int:
-    """`outputs`: the sum of GRAD_DX, GRAD_DW, GRAD_SUMS and GRAD_DU that apply."""
+def dora_matmul_backward_workspace_size(M: int, N: int, K: int, dtype, outputs: int = 31) -> int:
+    """`outputs`: the sum of the GRAD_ constants that apply."""
     return _size_of("dora_matmul_backward_workspace_size", M, N, K, _dtype_code(dtype), outputs)
 
 
@@ -668,7 +668,7 @@ def dora_matmul(x, w, row_scale=None, col_scale=None, t=None, b=None, s: float =
     return y, u
 
 
-GRAD_DX, GRAD_DW, GRAD_SUMS, GRAD_DU = 1, 2, 4, 8   # DORA_GRAD_*
+GRAD_DX, GRAD_DW, GRAD_SUMS, GRAD_DU, GRAD_ALIGNED = 1, 2, 4, 8, 16   # DORA_GRAD_*
 
 
 def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "none", need_dx: bool = True,
@@ -705,7 +705,8 @@ def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "non
     dbias = _new(stream, (N,), f32, dev) if need_dbias else None
     dcol = _new(stream, (N,), f32, dev) if need_dcol_scale else None
     outputs = (GRAD_DX * need_dx + GRAD_DW * need_dw + GRAD_SUMS * (need_dbias or need_dcol_scale)
-               + GRAD_DU * (du.data_ptr() % 16 == 0))
+               + GRAD_DU * (du.data_ptr() % 16 == 0)
+               + GRAD_ALIGNED * ((not need_dw or x.data_ptr() % 16 == 0) and (not need_dx or w.data_ptr() % 16 == 0)))
     need = _size_of("dora_matmul_backward_workspace_size", M, N, K, code, outputs)
     workspace = _space(workspace, need, stream, dev)
     _call("dora_matmul_backward", dy.data_ptr(), pu, _addr(x) if need_dw else None, _addr(w) if need_dx else None,

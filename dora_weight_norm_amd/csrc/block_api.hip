@@ -160,11 +160,11 @@ dora_status dora_matmul(const void* x, const void* w, int dtype, int64_t M, int6
 dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs,
                                                 size_t* ws_bytes) {
   if (!valid_dtype(dtype)) return DORA_ERR_UNSUPPORTED_DTYPE;
-  if (ws_bytes == nullptr || outputs < 0 || outputs >= 2 * DORA_GRAD_DU ||
+  if (ws_bytes == nullptr || outputs < 0 || outputs >= 2 * DORA_GRAD_ALIGNED ||
       !matmul_sizes_ok(M, N, K, 0, esize(dtype)) || !matmul_sizes_ok(K, K, M, N, esize(dtype)))
     return DORA_ERR_INVALID_ARG;
   *ws_bytes = dora::plan_matmul_backward(M, N, K, dtype, outputs & DORA_GRAD_DX, outputs & DORA_GRAD_DW,
-                                         outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU)
+                                         outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU, outputs & DORA_GRAD_ALIGNED)
                   .ws_bytes;
   return DORA_OK;
 }
@@ -190,7 +190,8 @@ dora_status dora_matmul_backward(const void* dy, const void* u, const void* x, c
   if (!buffers_ok(in, 6, out, 5, same)) return DORA_ERR_INVALID_ARG;
   const dora::MatmulBackwardPlan p =
       dora::plan_matmul_backward(M, N, K, dtype, dx != nullptr, dw != nullptr, dbias != nullptr || dcol_scale != nullptr,
-                                 du != nullptr && aligned(du, 16));
+                                 du != nullptr && aligned(du, 16),
+                                 (dw == nullptr || aligned(x, 16)) && (dx == nullptr || aligned(w, 16)));
   const dora_status st = workspace_ok(workspace, workspace_bytes, p.ws_bytes, in, 6, out, 5);
   if (st != DORA_OK) return st;
   return hip_status(dora::launch_matmul_backward(p, dy, u, x, w, dtype, M, N, K, col_scale, bias, act, du, dx, dw,

@@ -57,6 +57,7 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
 
 struct MatmulBackwardPlan {
   bool du_direct;                               // du is written into the caller's array alone
+  bool direct;                                  // the products read x, w and du as they lie
   int64_t rows;                                 // row blocks of the element-wise pass
   int64_t ldn, ldm;                             // padded N and M
   int cfg_dx, cfg_dw, splits_dx, splits_dw;
@@ -64,7 +65,7 @@ struct MatmulBackwardPlan {
   size_t ws_bytes;
 };
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
-                                        bool need_sums, bool du_direct);
+                                        bool need_sums, bool du_direct, bool aligned_xw);
 
 hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int dtype, int64_t M, int64_t N,
                          int64_t K, const void* t, const void* b, int64_t r, float s, const Epilogue& ep,

@@ -238,24 +238,80 @@ __device__ __forceinline__ void column_terms(const Epilogue& ep, int64_t c, int 
   if (ep.bias) load8<float>(ep.bias + c, n, bs);
 }
 
-// One operand's share of a stage: R rows of 128 bytes of depth each, staged in
-// LDS by direct loads of 1 KiB (64 lanes x 16 bytes, eight rows). Wave w of
-// NW loads blocks w, w + NW, ...; a lane's offset in block b is off + b *
-// step. Rows past the operand lie past the descriptor's end and read zeros.
+// One operand's share of a stage, R rows by 128 bytes of depth, staged in LDS
+// by direct loads of 1 KiB (64 lanes x 16 bytes). Wave w of NW makes loads w,
+// w + NW, ...; a lane's offset in its load b is off + b * step.
+//   Rows along the depth ([row][k] in memory): an LDS row is one row's 128
+// bytes, a load eight of them; chunk c of row r lies at chunk c ^ (r / 2 mod
+// 8). Rows past the operand lie past the descriptor's end and read zeros.
+//   TR, rows across it ([k][row] in memory, 16-bit types): an LDS row is one
+// k's R elements, 64 of them a stage; chunk c of k lies at c ^ trswz(k), under
+// which the four k that a transposing read touches at once lie in distinct
+// banks. Columns past the operand are out of range per lane, and k past the
+// depth lie past the descriptor's end.
+template <int R>
+__device__ __forceinline__ int trswz(int k) {
+  return R >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
+}
+
 struct Stream {
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t off, step;
+  const char* p;      // TR: the operand, and bytes of one k
+  int64_t kbytes;
 };
 
-template <int ESZ, int R, int NW>
-__device__ __forceinline__ Stream make_stream(const void* p, int64_t ld, int64_t row0, int64_t rows, int lane, int wave,
-                                              int chunk) {
-  const int64_t left = rows - row0 < R ? rows - row0 : R;
+template <int ESZ, int R, int NW, bool TR>
+__device__ __forceinline__ Stream make_stream(const void* p, int64_t ld, int64_t row0, int64_t rows, int lane,
+                                              int wave) {
   Stream s;
-  s.rsrc = make_rsrc(static_cast<const char*>(p) + row0 * ld * ESZ, p ? (uint32_t)(left * ld * ESZ) : 0u);
-  s.off = (uint32_t)((wave * 8 + (lane >> 3)) * ld * ESZ) + (uint32_t)(chunk * 16);
-  s.step = (uint32_t)(NW * 8 * ld * ESZ);
+  s.p = static_cast<const char*>(p);
+  s.kbytes = ld * ESZ;
+  if constexpr (TR) {
+    constexpr int CPR = R / 8, KPB = 64 / CPR;   // chunks of an LDS row, k a load
+    const int k = wave * KPB + lane / CPR;
+    const int64_t col = row0 + ((lane % CPR) ^ trswz<R>(k)) * 8;
+    s.rsrc = make_rsrc(p, 0u);
+    s.off = col < rows ? (uint32_t)(k * s.kbytes + col * ESZ) : kOob;
+    s.step = (uint32_t)(NW * KPB * s.kbytes);
+  } else {
+    const int64_t left = rows - row0 < R ? rows - row0 : R;
+    const int chunk = (lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7);
+    s.rsrc = make_rsrc(s.p + row0 * s.kbytes, p ? (uint32_t)(left * s.kbytes) : 0u);
+    s.off = (uint32_t)((wave * 8 + (lane >> 3)) * s.kbytes) + (uint32_t)(chunk * 16);
+    s.step = (uint32_t)(NW * 8 * s.kbytes);
+  }
   return s;
+}
+
+// A lane's fragment (row r0 + lane % 32, eight k of step s from 8 (lane / 32))
+// of an operand staged as [k][R rows]: two transposing reads, each of which
+// gives lane i of 16 four k of row i from the rows of four k that its group's
+// lanes point at.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// (A function of its own with a restricted pointer: inlining it gives the read
+// alias information. Without any, the compiler takes it to depend on every
+// direct load in flight and waits for them all.)
+__device__ __forceinline__ s16x4 tr_load(lds_s16x4* __restrict p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
+
+template <int R>
+__device__ __forceinline__ u32x4 read_tr(const char* unit, int r0, int s, int lane) {
+  const int g = lane >> 4, m = lane & 15;
+  const int col = r0 + 16 * (g & 1) + 4 * (m & 3);
+  s16x4 h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = s * 16 + 8 * (g >> 1) + 4 * i + (m >> 2);
+    const char* at = unit + k * (R * 2) + (((col >> 3) ^ trswz<R>(k)) * 16 + (col & 7) * 2);
+    h[i] = tr_load((lds_s16x4*)at);
+  }
+  struct P {
+    s16x4 lo, hi;
+  };
+  const P p{h[0], h[1]};
+  return __builtin_bit_cast(u32x4, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -272,7 +328,7 @@ __device__ __forceinline__ Stream make_stream(const void* p, int64_t ld, int64_t
 // ---------------------------------------------------------------------------
 constexpr int kUnits = 5;
 
-template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR>
+template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR, bool AT, bool BT>
 __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, E = 16 / ESZ, KT = 128 / ESZ;
   constexpr int NW = WM * WN, MT = WM * MB * 32, NT = WN * NB * 32;
@@ -305,13 +361,11 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   const int mt = first + (id - grp * gsz) % gm, nt = (id - grp * gsz) / gm;
   const int64_t m0 = (int64_t)mt * MT, n0 = (int64_t)nt * NT;
 
-  // The lane's chunk of depth in its LDS row is swizzled (by row / 2) so that
-  // a fragment read's 16 lanes touch distinct banks.
-  const int chunk = (lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7);
-  const Stream sa = make_stream<ESZ, MT, NW>(g.a, g.lda, m0, g.M, lane, wave, chunk);
-  const Stream sb = make_stream<ESZ, NT, NW>(g.b, g.ldb, n0, g.N, lane, wave, chunk);
-  const Stream sa2 = make_stream<ESZ, MT, NW>(g.a2, g.lda2, m0, g.M, lane, wave, chunk);
-  const Stream sb2 = make_stream<ESZ, NT, NW>(g.b2, g.ldb2, n0, g.N, lane, wave, chunk);
+  const int chunk = (lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7);   // of depth, in rows along it
+  const Stream sa = make_stream<ESZ, MT, NW, AT>(g.a, g.lda, m0, g.M, lane, wave);
+  const Stream sb = make_stream<ESZ, NT, NW, BT>(g.b, g.ldb, n0, g.N, lane, wave);
+  const Stream sa2 = make_stream<ESZ, MT, NW, false>(g.a2, g.lda2, m0, g.M, lane, wave);
+  const Stream sb2 = make_stream<ESZ, NT, NW, false>(g.b2, g.ldb2, n0, g.N, lane, wave);
   // Stages: the low-rank pair's first, then the main depth's; this workgroup's
   // part of them is [st0, st1).
   const int n2 = PAIR ? (int)((g.K2 + KT - 1) / KT) : 0;
@@ -322,16 +376,27 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // lane's offset is out of range (zeros), so that every stage issues the same
   // loads. (Arguments are named before the builtin: a conditional inside its
   // argument list makes the host pass drop the kernel's stub.)
-  auto issue = [&](const Stream& main, const Stream& pair, int i, int unit, int b) __attribute__((always_inline)) {
-    const bool pr = PAIR && i < n2;
-    const int k0 = (pr ? i : i - n2) * 128;   // bytes of depth before the stage
-    const int left = i < st1 ? (int)((pr ? g.K2 : g.K) * ESZ) - k0 : 0;
-    const uint32_t at = pr ? pair.off + (uint32_t)b * pair.step : main.off + (uint32_t)b * main.step;
-    const uint32_t off = chunk * 16 < left ? at : kOob;
-    const __amdgpu_buffer_rsrc_t rs = pr ? pair.rsrc : main.rsrc;
+  auto issue = [&](const Stream& main, const Stream& pair, int i, int unit, int b, auto tr)
+      __attribute__((always_inline)) {
     char* dst = lds + unit + (b * NW + wave) * 1024;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, k0, 0, 0);
+    if constexpr (decltype(tr)::value) {
+      const int64_t left = (i < st1 ? g.K - (int64_t)i * KT : 0) * main.kbytes;
+      const uint32_t bytes = (uint32_t)(left < 0 ? 0 : (left < 0x7fffffff ? left : 0x7fffffff));
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(main.p + (int64_t)i * KT * main.kbytes, bytes);
+      const uint32_t off = main.off + (uint32_t)b * main.step;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
+    } else {
+      const bool pr = PAIR && i < n2;
+      const int k0 = (pr ? i : i - n2) * 128;   // bytes of depth before the stage
+      const int left = i < st1 ? (int)((pr ? g.K2 : g.K) * ESZ) - k0 : 0;
+      const uint32_t at = pr ? pair.off + (uint32_t)b * pair.step : main.off + (uint32_t)b * main.step;
+      const uint32_t off = chunk * 16 < left ? at : kOob;
+      const __amdgpu_buffer_rsrc_t rs = pr ? pair.rsrc : main.rsrc;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, k0, 0, 0);
+    }
   };
+  auto issue_a = [&](int i, int unit, int b) __attribute__((always_inline)) { issue(sa, sa2, i, unit, b, Tag<AT>{}); };
+  auto issue_b = [&](int i, int unit, int b) __attribute__((always_inline)) { issue(sb, sb2, i, unit, b, Tag<BT>{}); };
 
   // The epilogue's columns of this lane: their scales and biases are asked for
   // here, a whole depth before they are needed.
@@ -362,13 +427,21 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
     const int f = q % FC, w = q / FC;
     const bool isb = w >= 1 && w <= NB;
     const int blk = w == 0 ? 0 : (isb ? w - 1 : w - NB);
-    const int c = (((s * 2 + fg) * FC + f) ^ ((fr >> 1) & 7)) * 16;
-    const char* at = isb ? lds + ub + ((wn * NB + blk) * 32 + fr) * 128 + c
-                         : lds + ua + ((wm * MB + blk) * 32 + fr) * 128 + c;
+    const int r0 = (isb ? wn * NB : wm * MB) * 32 + blk * 32;   // first row of the block
+    const char* unit = lds + (isb ? ub : ua);
+    u32x4 v;
+    if constexpr (AT || BT) {
+      if (isb ? BT : AT)
+        v = isb ? read_tr<NT>(unit, r0, s, lane) : read_tr<MT>(unit, r0, s, lane);
+      else
+        v = *reinterpret_cast<const u32x4*>(unit + (r0 + fr) * 128 + (((s * 2 + fg) * FC + f) ^ ((fr >> 1) & 7)) * 16);
+    } else {
+      v = *reinterpret_cast<const u32x4*>(unit + (r0 + fr) * 128 + (((s * 2 + fg) * FC + f) ^ ((fr >> 1) & 7)) * 16);
+    }
     if (isb)
-      F.b[blk < NB ? blk : 0][f] = *reinterpret_cast<const u32x4*>(at);
+      F.b[blk < NB ? blk : 0][f] = v;
     else
-      F.a[blk < MB ? blk : 0][f] = *reinterpret_cast<const u32x4*>(at);
+      F.a[blk < MB ? blk : 0][f] = v;
   };
   auto scale = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -398,9 +471,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       for (int l = l0; l < l1; ++l)
         if ((l - l0) * NM / (l1 - l0) == m) {
           if (l < BBLK)
-            issue(sb, sb2, i + 2, ul, l);
+            issue_b(i + 2, ul, l);
           else
-            issue(sa, sa2, i + 3, um, l - BBLK);
+            issue_a(i + 3, um, l - BBLK);
         }
       acc[m / NB][m % NB] = Op<T>::run(cur.a[m / NB], cur.b[m % NB], acc[m / NB][m % NB]);
       __builtin_amdgcn_sched_barrier(0);
@@ -409,20 +482,20 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // Ring units (bytes) of stage i's rows and columns, and of stage i + 1's.
   int u0 = 0, u1 = UNIT, u2 = 2 * UNIT, u3 = 3 * UNIT, u4 = 4 * UNIT;
 #pragma unroll
-  for (int b = 0; b < ABLK; ++b) issue(sa, sa2, st0, u0, b);
+  for (int b = 0; b < ABLK; ++b) issue_a(st0, u0, b);
 #pragma unroll
-  for (int b = 0; b < BBLK; ++b) issue(sb, sb2, st0, u1, b);
+  for (int b = 0; b < BBLK; ++b) issue_b(st0, u1, b);
 #pragma unroll
-  for (int b = 0; b < ABLK; ++b) issue(sa, sa2, st0 + 1, u2, b);
+  for (int b = 0; b < ABLK; ++b) issue_a(st0 + 1, u2, b);
   // (the columns of the second stage and the rows of the third: one period's
   // loads, of which the first step's part goes out here)
   constexpr int L1 = BPW / STEPS;
 #pragma unroll
   for (int l = 0; l < L1; ++l) {
     if (l < BBLK)
-      issue(sb, sb2, st0 + 1, u3, l);
+      issue_b(st0 + 1, u3, l);
     else
-      issue(sa, sa2, st0 + 2, u4, l - BBLK);
+      issue_a(st0 + 2, u4, l - BBLK);
   }
   wait_vm_lgkm0<ABLK + L1>();
   barrier_keep_loads();
@@ -865,8 +938,8 @@ int elem_size(int dtype) { return dtype == 1 ? 4 : (dtype == 3 ? 1 : 2); }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int* cfg, int* splits) {
-  if (M <= 32) {
+void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, bool few, int* cfg, int* splits) {
+  if (few && M <= 32) {
     // One workgroup per 16 columns; the depth is split over workgroups too
     // while they do not fill the chip and each wave keeps four steps.
     *cfg = kFewRows;
@@ -905,12 +978,12 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int* cfg, int*
   }
 }
 
-template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR>
+template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR, bool AT = false, bool BT = false>
 hipError_t launch_tile(GemmArgs g, hipStream_t st) {
   constexpr int MT = WM * MB * 32, NT = WN * NB * 32;
   g.n_mt = (int)((g.M + MT - 1) / MT);
   g.n_nt = (int)((g.N + NT - 1) / NT);
-  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB, PAIR>;
+  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB, PAIR, AT, BT>;
   constexpr int lds = kUnits * (MT > NT ? MT : NT) * 128;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
@@ -936,12 +1009,8 @@ hipError_t launch_few_rows(GemmArgs g, hipStream_t st) {
   return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
 }
 
-template <typename T, typename O>
-hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
-  if (cfg == kFewRows)
-    return g.M <= 8 ? launch_few_rows<T, O, 2, 1>(g, st)
-                    : (g.M <= 16 ? launch_few_rows<T, O, 2, 2>(g, st) : launch_few_rows<T, O, 4, 4>(g, st));
-  constexpr int KT = 128 / Op<T>::esz;
+// Stages of KT elements of the whole depth and of each of g.splits parts.
+void split_stages(GemmArgs& g, int KT) {
   const int n2 = (int)((g.K2 + KT - 1) / KT);
   g.stages = n2 + (int)((g.K + KT - 1) / KT);
   if (g.stages < 1) g.stages = 1;   // (no depth at all: one stage of zeros)
@@ -949,6 +1018,26 @@ hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
   const int per = (g.stages + g.splits - 1) / g.splits;
   g.stages_per_split = per > n2 ? per : n2;
   g.splits = (g.stages + g.stages_per_split - 1) / g.stages_per_split;
+}
+
+// The backward's products on operands as they lie (16-bit types): `b` stored
+// [k][row], and with AT `a` too.
+template <typename T, bool AT>
+hipError_t launch_gemm_tr(GemmArgs g, int cfg, hipStream_t st) {
+  split_stages(g, 64);
+  hipError_t e = hipErrorInvalidValue;
+  if (cfg == kTile256) e = launch_tile<T, T, 2, 4, 4, 2, false, AT, true>(g, st);
+  if (cfg == kTile128) e = launch_tile<T, T, 2, 2, 2, 2, false, AT, true>(g, st);
+  if (cfg == kTile64) e = launch_tile<T, T, 2, 2, 1, 1, false, AT, true>(g, st);
+  return e != hipSuccess || g.splits == 1 ? e : launch_join<T>(g, st);
+}
+
+template <typename T, typename O>
+hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
+  if (cfg == kFewRows)
+    return g.M <= 8 ? launch_few_rows<T, O, 2, 1>(g, st)
+                    : (g.M <= 16 ? launch_few_rows<T, O, 2, 2>(g, st) : launch_few_rows<T, O, 4, 4>(g, st));
+  split_stages(g, 128 / Op<T>::esz);
   hipError_t e = hipErrorInvalidValue;
   if (g.K2 > 0) {
     if constexpr (Op<T>::esz > 1) {   // (no pair in e4m3)
@@ -1018,7 +1107,7 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   MatmulPlan p{};
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
-  choose_tile(M, N, up(K, KT) / KT, dtype, &p.cfg, &p.splits);
+  choose_tile(M, N, up(K, KT) / KT, dtype, true, &p.cfg, &p.splits);
   auto operand = [&](int64_t rows, int64_t depth, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
     *pack = p.cfg != kFewRows && depth > 0 && (depth % epc != 0 || !(al & bit));
@@ -1065,7 +1154,7 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
 }
 
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
-                                        bool need_sums, bool du_direct) {
+                                        bool need_sums, bool du_direct, bool aligned_xw) {
   MatmulBackwardPlan p{};
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   p.ldn = up(N, epc), p.ldm = up(M, epc);
@@ -1082,16 +1171,17 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.du_direct = du_direct && N % epc == 0;
   p.off_du = take(p.du_direct ? 0 : (size_t)(M * p.ldn) * esz);
   p.off_sum = take(need_sums ? (size_t)(p.rows * 2 * N) * 4 : 0);
-  p.off_wt = take(need_dx ? (size_t)(K * p.ldn) * esz : 0);
-  p.off_dut = take(need_dw ? (size_t)(N * p.ldm) * esz : 0);
-  p.off_xt = take(need_dw ? (size_t)(K * p.ldm) * esz : 0);
+  p.direct = dtype != 1 && aligned_xw && N % epc == 0 && K % epc == 0;
+  p.off_wt = take(need_dx && !p.direct ? (size_t)(K * p.ldn) * esz : 0);
+  p.off_dut = take(need_dw && !p.direct ? (size_t)(N * p.ldm) * esz : 0);
+  p.off_xt = take(need_dw && !p.direct ? (size_t)(K * p.ldm) * esz : 0);
   size_t part = 0;
   if (need_dx) {
-    choose_tile(M, K, up(N, KT) / KT, dtype, &p.cfg_dx, &p.splits_dx);
+    choose_tile(M, K, up(N, KT) / KT, dtype, !p.direct, &p.cfg_dx, &p.splits_dx);
     if (p.splits_dx > 1) part = (size_t)(p.splits_dx * M * K) * 4;
   }
   if (need_dw) {
-    choose_tile(N, K, up(M, KT) / KT, dtype, &p.cfg_dw, &p.splits_dw);
+    choose_tile(N, K, up(M, KT) / KT, dtype, !p.direct, &p.cfg_dw, &p.splits_dw);
     const size_t q = p.splits_dw > 1 ? (size_t)(p.splits_dw * N * K) * 4 : 0;
     part = q > part ? q : part;
   }
@@ -1137,6 +1227,21 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   }
   GemmArgs g{};
   g.part = reinterpret_cast<float*>(ws + p.off_part);
+  if (p.direct) {
+    // dx: du along the depth, w across it; dw: both across it.
+    if (dx && M > 0 && K > 0) {
+      g.a = d, g.b = w, g.lda = N, g.ldb = K, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
+      g.ep.y = dx;
+      e = dtype == 0 ? launch_gemm_tr<bf16_t, false>(g, p.cfg_dx, st) : launch_gemm_tr<f16_t, false>(g, p.cfg_dx, st);
+      if (e != hipSuccess) return e;
+    }
+    if (dw && N > 0 && K > 0) {
+      g.a = d, g.b = x, g.lda = N, g.ldb = K, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
+      g.ep.y = dw;
+      e = dtype == 0 ? launch_gemm_tr<bf16_t, true>(g, p.cfg_dw, st) : launch_gemm_tr<f16_t, true>(g, p.cfg_dw, st);
+    }
+    return e;
+  }
   if (dx && M > 0 && K > 0) {
     if (N > 0) e = transpose(w, N, K, K, p.ldn, esz, ws + p.off_wt, st);
     if (e != hipSuccess) return e;

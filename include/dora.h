@@ -458,6 +458,7 @@ dora_status dora_matmul(const void* x, const void* w, int dtype, int64_t M, int6
 #define DORA_GRAD_DW 2   /* dw                                  */
 #define DORA_GRAD_SUMS 4 /* dbias or dcol_scale, or both        */
 #define DORA_GRAD_DU 8   /* du, in an array aligned to 16 bytes */
+#define DORA_GRAD_ALIGNED 16 /* x (for dw) and w (for dx) start on 16-byte boundaries */
 
 /* Device workspace dora_matmul_backward needs for a set of outputs. Host only. */
 dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs,

@@ -118,7 +118,7 @@ def test_matmul_backward_refusals():
     assert _mm_bwd(ws_bytes=16) == 4 and _mm_bwd(ws=None) == 4
     sz = ctypes.c_size_t()
     f = bnd.load().dora_matmul_backward_workspace_size
-    assert f(4, 32, 64, 0, 16, ctypes.byref(sz)) == 1 and f(4, 32, 64, 3, 1, ctypes.byref(sz)) == 2
+    assert f(4, 32, 64, 0, 32, ctypes.byref(sz)) == 1 and f(4, 32, 64, 3, 1, ctypes.byref(sz)) == 2
     assert f(4, 32, 64, 0, 15, None) == 1
 
 
