@@ -122,6 +122,24 @@ __device__ __forceinline__ float slope_of(float z, int act) {
   }
 }
 
+// z to the activation's slope there, N values at once.
+template <int N>
+__device__ __forceinline__ void slope_all(float (&z)[N], int act) {
+  switch (act) {
+#define DORA_SLOPE(A)                                    \
+  case A:                                                \
+    for (int e = 0; e < N; ++e) z[e] = slope_of(z[e], A); \
+    break;
+    DORA_SLOPE(0)
+    DORA_SLOPE(1)
+    DORA_SLOPE(2)
+    DORA_SLOPE(3)
+    DORA_SLOPE(4)
+#undef DORA_SLOPE
+    default: break;
+  }
+}
+
 // Eight consecutive elements of an output row in the output type, as loaded.
 template <typename O>
 struct Raw8 {
@@ -886,26 +904,46 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
     bs[e] = (bias && e < nv) ? bias[n + e] : 0.f;
     sb[e] = sc[e] = 0.f;
   }
-  for (int64_t m = (int64_t)blockIdx.y * nl + ly; nv > 0 && m < M; m += (int64_t)gridDim.y * nl) {
-    float y[8], v[8], o[8];
-    load8<T>(dy + m * N + n, nv, y);
-    load8<T>(u + m * N + n, nv, v);
+  // Four rows' loads are in flight at a time.
+  constexpr int U = 4;
+  const int64_t step = (int64_t)gridDim.y * nl;
+  for (int64_t m0 = (int64_t)blockIdx.y * nl + ly; nv > 0 && m0 < M; m0 += U * step) {
+    Raw8<T> ry[U], ru[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float dz = y[e] * slope_of(fmaf(cs[e], v[e], bs[e]), act);
-      sb[e] += dz;
-      sc[e] = fmaf(dz, v[e], sc[e]);
-      o[e] = cs[e] * dz;
+    for (int i = 0; i < U; ++i) {
+      const int64_t m = m0 + i * step;
+      if (m < M) {
+        ry[i] = load_raw8<T>(dy + m * N + n, nv);
+        ru[i] = load_raw8<T>(u + m * N + n, nv);
+      }
     }
-    if (du2) store8<T>(du2 + m * N + n, nv, o);
-    // (a padded row's tail, up to the next strip of eight, is written as zeros)
-    if (nv < 8 && ldu > N) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e >= nv) o[e] = 0.f;
-      store8<T>(du + m * ldu + n, (int)(ldu - n < 8 ? ldu - n : 8), o);
-    } else {
-      store8<T>(du + m * ldu + n, nv, o);
+    for (int i = 0; i < U; ++i) {
+      const int64_t m = m0 + i * step;
+      if (m >= M) continue;
+      float y[8], v[8], o[8];
+      unpack8<T>(ry[i], y);
+      unpack8<T>(ru[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(cs[e], v[e], bs[e]);
+      slope_all<8>(o, act);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float dz = y[e] * o[e];
+        sb[e] += dz;
+        sc[e] = fmaf(dz, v[e], sc[e]);
+        o[e] = cs[e] * dz;
+      }
+      if (du2) store8<T>(du2 + m * N + n, nv, o);
+      // (a padded row's tail, up to the next strip of eight, is written as zeros)
+      if (nv < 8 && ldu > N) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e >= nv) o[e] = 0.f;
+        store8<T>(du + m * ldu + n, (int)(ldu - n < 8 ? ldu - n : 8), o);
+      } else {
+        store8<T>(du + m * ldu + n, nv, o);
+      }
     }
   }
   if (sums == nullptr) return;   // uniform
@@ -930,6 +968,8 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
 }
 
 constexpr int kCUs = 256;
+
+constexpr int kRowBlocks = 512;   // workgroups of the element-wise backward
 
 int tile_rows(int cfg) { return cfg == kTile256 ? 256 : (cfg == kTile128 ? 128 : 64); }
 // Elements of a stage's 128 bytes of depth.
@@ -1159,7 +1199,7 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   p.ldn = up(N, epc), p.ldm = up(M, epc);
   const int64_t strips = (N + 7) / 8, bx = (strips + 255) / 256;
-  p.rows = bx > 0 ? 512 / bx : 1;
+  p.rows = bx > 0 ? kRowBlocks / bx : 1;
   if (p.rows < 1) p.rows = 1;
   if (p.rows > (M + 7) / 8) p.rows = (M + 7) / 8;
   size_t off = 0;

@@ -22,6 +22,7 @@ namespace dora {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
+constexpr int64_t kFwdGrid = 1024;   // workgroups of 256 threads, four a compute unit
 // Smallest scale: rows whose largest |n| is below 448 times it (about 2^-91)
 // keep it, so that the reciprocal stays finite.
 constexpr float kMinScale = 0x1p-100f;
@@ -162,7 +163,9 @@ struct NormArgs {
 };
 
 // NT threads and C chunks a thread to a row; workgroups of 256 threads hold
-// 256 / NT rows where NT is 64.
+// 256 / NT rows where NT is 64. A workgroup walks rows gridDim.x apart: its
+// weights are read once, and a row's loads go out before the row ahead of it
+// is reduced.
 template <typename T, int NT, int C>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs a) {
   constexpr int E = Elem<T>::epc;
@@ -171,22 +174,29 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
   const int lane = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
   constexpr int RPW = NT == 64 ? 4 : 1;   // rows a workgroup holds at a time
   int par = 0;
-  for (int64_t t = (int64_t)blockIdx.x * RPW + (NT == 64 ? threadIdx.x >> 6 : 0); t < a.T;
-       t += (int64_t)gridDim.x * RPW, par ^= 1) {
+  const int64_t t0 = (int64_t)blockIdx.x * RPW + (NT == 64 ? threadIdx.x >> 6 : 0);
+  const bool has_res = a.residual != nullptr;
+  u32x4 xv[C], rv[C];
+  auto load = [&](int64_t t) __attribute__((always_inline)) {
     const T* x = static_cast<const T*>(a.x) + t * a.d;
-    const T* res = a.residual ? static_cast<const T*>(a.residual) + t * a.d : nullptr;
-    u32x4 xv[C], rv[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) xv[c] = load_row_chunk(x, (int64_t)(c * NT + lane) * E, a.d);
-    if (res) {
+    if (has_res) {
+      const T* res = static_cast<const T*>(a.residual) + t * a.d;
 #pragma unroll
       for (int c = 0; c < C; ++c) rv[c] = load_row_chunk(res, (int64_t)(c * NT + lane) * E, a.d);
     }
+  };
+  if (t0 < a.T) load(t0);
+  float w[C][E];
+#pragma unroll
+  for (int c = 0; c < C; ++c) load_weight<E>(a.weight, (int64_t)(c * NT + lane) * E, a.d, w[c]);
+  for (int64_t t = t0; t < a.T; t += (int64_t)gridDim.x * RPW, par ^= 1) {
     float f[C][E], q = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       unpack<T, E>(xv[c], f[c]);
-      if (res) {
+      if (has_res) {
         float r[E];
         unpack<T, E>(rv[c], r);
 #pragma unroll
@@ -195,23 +205,23 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
 #pragma unroll
       for (int e = 0; e < E; ++e) q = fmaf(f[c][e], f[c][e], q);
     }
-    q = row_sum<NT>(q, red[par]);
-    const float rs = 1.f / sqrtf(q / (float)a.d + a.eps);
-    if (lane == 0 && a.rstd) a.rstd[t] = rs;
+    // (h may be x or residual itself: other rows' loads are of other rows)
+    if (t + (int64_t)gridDim.x * RPW < a.T) load(t + (int64_t)gridDim.x * RPW);
     if (a.h) {
       T* h = static_cast<T*>(a.h) + t * a.d;
 #pragma unroll
       for (int c = 0; c < C; ++c) store_row_chunk<T>(h, (int64_t)(c * NT + lane) * E, a.d, f[c]);
     }
+    q = row_sum<NT>(q, red[par]);
+    const float rs = 1.f / sqrtf(q / (float)a.d + a.eps);
+    if (lane == 0 && a.rstd) a.rstd[t] = rs;
     uint32_t top = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float w[E];
       const int64_t k = (int64_t)(c * NT + lane) * E;
-      load_weight<E>(a.weight, k, a.d, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        f[c][e] = f[c][e] * rs * w[e];
+        f[c][e] = f[c][e] * rs * w[c][e];
         // (past d the row is 0 * rs * w: it counts only where it exists)
         const uint32_t b = k + e < a.d ? abs_bits(f[c][e]) : 0u;
         top = b > top ? b : top;
@@ -335,27 +345,32 @@ __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(NormBwdArgs a) {
     for (int e = 0; e < E; ++e) dw[c][e] = 0.f;
   }
   int par = 0;   // which words the row's sum goes through: a wave a row ahead uses the other ones
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
+  u32x4 yv[2][C], hv[2][C], gv[2][C];
+  float rs2[2];
+  // (a row's loads go out before the row ahead of it is reduced)
+  auto load = [&](int64_t t, u32x4 (&y)[C], u32x4 (&h)[C], u32x4 (&g)[C], float& rs) __attribute__((always_inline)) {
     const T* dyr = static_cast<const T*>(a.dy) + t * a.d;
     const T* hr = static_cast<const T*>(a.h) + t * a.d;
-    u32x4 yv[C], hv[C], gv[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      yv[c] = load_row_chunk(dyr, (int64_t)(c * NT + lane) * E, a.d);
-      hv[c] = load_row_chunk(hr, (int64_t)(c * NT + lane) * E, a.d);
+      y[c] = load_row_chunk(dyr, (int64_t)(c * NT + lane) * E, a.d);
+      h[c] = load_row_chunk(hr, (int64_t)(c * NT + lane) * E, a.d);
     }
     if (a.dh) {
       const T* gr = static_cast<const T*>(a.dh) + t * a.d;
 #pragma unroll
-      for (int c = 0; c < C; ++c) gv[c] = load_row_chunk(gr, (int64_t)(c * NT + lane) * E, a.d);
+      for (int c = 0; c < C; ++c) g[c] = load_row_chunk(gr, (int64_t)(c * NT + lane) * E, a.d);
     }
-    const float rs = a.rstd[t];
+    rs = a.rstd[t];
+  };
+  auto row = [&](int64_t t, const u32x4 (&yr)[C], const u32x4 (&hr)[C], const u32x4 (&gr)[C], float rs)
+      __attribute__((always_inline)) {
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float y[E], n[E];
-      unpack<T, E>(yv[c], y);
-      unpack<T, E>(hv[c], n);
+      unpack<T, E>(yr[c], y);
+      unpack<T, E>(hr[c], n);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         n[e] *= rs;
@@ -364,21 +379,39 @@ __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(NormBwdArgs a) {
       }
     }
     const float mean = row_sum<NT>(sum, red[par]) / (float)a.d;
+    par ^= 1;
     T* dxr = static_cast<T*>(a.dx) + t * a.d;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float y[E], n[E], o[E];
-      unpack<T, E>(yv[c], y);
-      unpack<T, E>(hv[c], n);
+      unpack<T, E>(yr[c], y);
+      unpack<T, E>(hr[c], n);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = rs * fmaf(-(n[e] * rs), mean, y[e] * w[c][e]);
       if (a.dh) {
         float g[E];
-        unpack<T, E>(gv[c], g);
+        unpack<T, E>(gr[c], g);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += g[e];
       }
       store_row_chunk<T>(dxr, (int64_t)(c * NT + lane) * E, a.d, o);
+    }
+  };
+  const int64_t step = gridDim.x;
+  int64_t t = blockIdx.x;
+  if constexpr (C > 2) {   // (no registers for a second row)
+    for (; t < a.T; t += step) {
+      load(t, yv[0], hv[0], gv[0], rs2[0]);
+      row(t, yv[0], hv[0], gv[0], rs2[0]);
+    }
+  } else {
+    if (t < a.T) load(t, yv[0], hv[0], gv[0], rs2[0]);
+    for (; t < a.T; t += 2 * step) {
+      if (t + step < a.T) load(t + step, yv[1], hv[1], gv[1], rs2[1]);
+      row(t, yv[0], hv[0], gv[0], rs2[0]);
+      if (t + step >= a.T) break;
+      if (t + 2 * step < a.T) load(t + 2 * step, yv[0], hv[0], gv[0], rs2[0]);
+      row(t + step, yv[1], hv[1], gv[1], rs2[1]);
     }
   }
   if (a.part) {
@@ -441,9 +474,9 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_long_kernel(NormBwdArgs a) 
 
 // out0[j] (j < n0) or out1[j - n0] = sum of column j over the n_part rows of
 // part [n_part][n]; either output may be null. One workgroup owns 64 columns;
-// its four waves each add a contiguous quarter of the rows in increasing
-// order (loads kSumBatch at a time), then wave 0 adds the quarters in order.
-constexpr int kSumCols = 64, kSumSplit = 4, kSumBatch = 16;
+// its sixteen waves each add a contiguous sixteenth of the rows in increasing
+// order (loads kSumBatch at a time), then wave 0 adds those sums in order.
+constexpr int kSumCols = 64, kSumSplit = 16, kSumBatch = 16;
 
 __global__ __launch_bounds__(kSumCols* kSumSplit) void column_sum_kernel(const float* part, int n_part, int64_t n,
                                                                           float* out0, int64_t n0, float* out1) {
@@ -511,20 +544,23 @@ RowShape backward_shape(int64_t d, int epc) {
 // units), few enough that the dweight partials stay small beside the rows.
 int64_t backward_grid(int64_t T, int64_t d, int epc) {
   const RowShape r = backward_shape(d, epc);
-  const int64_t g = r.nt == 64 ? 2048 : (r.nt == 256 ? 1024 : 512);
+  const int64_t g = r.nt == 64 ? 2048 : 512;
   return T < g ? T : g;
 }
 
-// Workgroups of the forward: one a row (or four rows), up to a grid limit
-// past which each takes several.
-unsigned grid_of(int64_t n) { return (unsigned)(n < ((int64_t)1 << 20) ? n : ((int64_t)1 << 20)); }
+// Workgroups of the forward: one a row (or four rows), up to what the chip
+// holds at once; past that each takes several rows.
+unsigned grid_of(int64_t n, int nt) {
+  const int64_t most = nt == 1024 ? 512 : kFwdGrid;
+  return (unsigned)(n < most ? n : most);
+}
 
 template <typename T>
 hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
   const RowShape r = forward_shape(a.T, a.d, Elem<T>::epc);
 #define DORA_NORM(NT, C)                                                                                   \
   if (r.nt == NT && r.c == C) {                                                                            \
-    hipLaunchKernelGGL((rms_norm_kernel<T, NT, C>), dim3(grid_of(NT == 64 ? (a.T + 3) / 4 : a.T)),         \
+    hipLaunchKernelGGL((rms_norm_kernel<T, NT, C>), dim3(grid_of(NT == 64 ? (a.T + 3) / 4 : a.T, NT)),     \
                        dim3(NT == 64 ? 256 : NT), 0, st, a);                                               \
     return hipGetLastError();                                                                              \
   }
@@ -541,7 +577,7 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
     DORA_NORM(1024, 4)
   }
 #undef DORA_NORM
-  hipLaunchKernelGGL((rms_norm_long_kernel<T>), dim3(grid_of(a.T)), dim3(1024), 0, st, a);
+  hipLaunchKernelGGL((rms_norm_long_kernel<T>), dim3(grid_of(a.T, 1024)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
