@@ -22,6 +22,11 @@ namespace dora {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
+// Inputs of more than this stream past the caches, which they would only
+// empty: measured at 8192 x 8192 bf16 to 8 bits 84 us with ordinary loads and
+// stores, 77.5 us with non-temporal ones; at 777 x 3583, which the caches
+// hold, 8.1 and 8.6 us.
+constexpr int64_t kStreamBytes = (int64_t)16 << 20;
 constexpr int64_t kFwdGrid = 1024;   // workgroups of 256 threads, four a compute unit
 // Smallest scale: rows whose largest |n| is below 448 times it (about 2^-91)
 // keep it, so that the reciprocal stays finite.
@@ -32,12 +37,17 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
-// One 16-byte chunk of a row: elements [k, k + E), zeros past d.
-template <typename T>
+// One 16-byte chunk of a row: elements [k, k + E), zeros past d. STREAM: the
+// rows pass the caches by (see kStreamBytes).
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ u32x4 load_row_chunk(const T* row, int64_t k, int64_t d) {
   constexpr int E = Elem<T>::epc;
   u32x4 v = {0u, 0u, 0u, 0u};
-  if (k + E <= d) return *reinterpret_cast<const u32x4_any*>(row + k);
+  if (k + E <= d) {
+    const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + k);
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    return *p;
+  }
   if (k < d) {
     T tmp[E];
 #pragma unroll
@@ -47,11 +57,14 @@ __device__ __forceinline__ u32x4 load_row_chunk(const T* row, int64_t k, int64_t
   return v;
 }
 
-template <typename T>
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ void store_row_chunk(T* row, int64_t k, int64_t d, const float (&f)[Elem<T>::epc]) {
   constexpr int E = Elem<T>::epc;
   if (k + E <= d) {
-    *reinterpret_cast<u32x4_any*>(row + k) = pack<T, E>(f);
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(pack<T, E>(f), reinterpret_cast<u32x4_any*>(row + k));
+    else
+      *reinterpret_cast<u32x4_any*>(row + k) = pack<T, E>(f);
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -60,7 +73,7 @@ __device__ __forceinline__ void store_row_chunk(T* row, int64_t k, int64_t d, co
 }
 
 // E fp32 values to e4m3 (OCP, round to nearest even), four to a word.
-template <int E>
+template <int E, bool STREAM = false>
 __device__ __forceinline__ void store_row_q(uint8_t* row, int64_t k, int64_t d, const float (&f)[E]) {
   uint32_t w[E / 4];
 #pragma unroll
@@ -72,7 +85,10 @@ __device__ __forceinline__ void store_row_q(uint8_t* row, int64_t k, int64_t d, 
   if (k + E <= d) {
     if constexpr (E == 8) {
       const u32x2 p = {w[0], w[1]};
-      *reinterpret_cast<u32x2_any*>(row + k) = p;
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(p, reinterpret_cast<u32x2_any*>(row + k));
+      else
+        *reinterpret_cast<u32x2_any*>(row + k) = p;
     } else {
       *reinterpret_cast<u32_any*>(row + k) = w[0];
     }
@@ -166,7 +182,7 @@ struct NormArgs {
 // 256 / NT rows where NT is 64. A workgroup walks rows gridDim.x apart: its
 // weights are read once, and a row's loads go out before the row ahead of it
 // is reduced.
-template <typename T, int NT, int C>
+template <typename T, int NT, int C, bool STREAM>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs a) {
   constexpr int E = Elem<T>::epc;
   // (two sets of words: a wave one row ahead uses the other one)
@@ -180,11 +196,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
   auto load = [&](int64_t t) __attribute__((always_inline)) {
     const T* x = static_cast<const T*>(a.x) + t * a.d;
 #pragma unroll
-    for (int c = 0; c < C; ++c) xv[c] = load_row_chunk(x, (int64_t)(c * NT + lane) * E, a.d);
+    for (int c = 0; c < C; ++c) xv[c] = load_row_chunk<T, STREAM>(x, (int64_t)(c * NT + lane) * E, a.d);
     if (has_res) {
       const T* res = static_cast<const T*>(a.residual) + t * a.d;
 #pragma unroll
-      for (int c = 0; c < C; ++c) rv[c] = load_row_chunk(res, (int64_t)(c * NT + lane) * E, a.d);
+      for (int c = 0; c < C; ++c) rv[c] = load_row_chunk<T, STREAM>(res, (int64_t)(c * NT + lane) * E, a.d);
     }
   };
   if (t0 < a.T) load(t0);
@@ -210,7 +226,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
     if (a.h) {
       T* h = static_cast<T*>(a.h) + t * a.d;
 #pragma unroll
-      for (int c = 0; c < C; ++c) store_row_chunk<T>(h, (int64_t)(c * NT + lane) * E, a.d, f[c]);
+      for (int c = 0; c < C; ++c) store_row_chunk<T, STREAM>(h, (int64_t)(c * NT + lane) * E, a.d, f[c]);
     }
     q = row_sum<NT>(q, red[par]);
     const float rs = 1.f / sqrtf(q / (float)a.d + a.eps);
@@ -230,7 +246,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
     if (a.y) {
       T* y = static_cast<T*>(a.y) + t * a.d;
 #pragma unroll
-      for (int c = 0; c < C; ++c) store_row_chunk<T>(y, (int64_t)(c * NT + lane) * E, a.d, f[c]);
+      for (int c = 0; c < C; ++c) store_row_chunk<T, STREAM>(y, (int64_t)(c * NT + lane) * E, a.d, f[c]);
     }
     if (a.q) {   // uniform over the grid
       top = row_max_bits<NT>(top, reinterpret_cast<uint32_t*>(red[par]) + (NT > 64 ? NT / 64 : 0));
@@ -241,7 +257,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
       for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int e = 0; e < E; ++e) f[c][e] *= inv;
-        store_row_q<E>(qr, (int64_t)(c * NT + lane) * E, a.d, f[c]);
+        store_row_q<E, STREAM>(qr, (int64_t)(c * NT + lane) * E, a.d, f[c]);
       }
     }
   }
@@ -332,7 +348,7 @@ struct NormBwdArgs {
   float* part;   // [gridDim.x][d], or null
 };
 
-template <typename T, int NT, int C>
+template <typename T, int NT, int C, bool STREAM>
 __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(NormBwdArgs a) {
   constexpr int E = Elem<T>::epc;
   __shared__ float red[2][NT > 64 ? NT / 64 : 1];
@@ -353,13 +369,13 @@ __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(NormBwdArgs a) {
     const T* hr = static_cast<const T*>(a.h) + t * a.d;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      y[c] = load_row_chunk(dyr, (int64_t)(c * NT + lane) * E, a.d);
-      h[c] = load_row_chunk(hr, (int64_t)(c * NT + lane) * E, a.d);
+      y[c] = load_row_chunk<T, STREAM>(dyr, (int64_t)(c * NT + lane) * E, a.d);
+      h[c] = load_row_chunk<T, STREAM>(hr, (int64_t)(c * NT + lane) * E, a.d);
     }
     if (a.dh) {
       const T* gr = static_cast<const T*>(a.dh) + t * a.d;
 #pragma unroll
-      for (int c = 0; c < C; ++c) g[c] = load_row_chunk(gr, (int64_t)(c * NT + lane) * E, a.d);
+      for (int c = 0; c < C; ++c) g[c] = load_row_chunk<T, STREAM>(gr, (int64_t)(c * NT + lane) * E, a.d);
     }
     rs = a.rstd[t];
   };
@@ -515,8 +531,9 @@ struct RowShape {
 };
 
 // Forward. Many short rows take a wave each (no barrier); other rows take
-// 256 threads, or 1024 where there are too few rows to fill the chip or the
-// row is too long for 256. Rows of up to 16384 elements stay in registers
+// 256 threads, 512 past two chunks a thread (four of 8192 bf16 elements ran
+// two workgroups a compute unit for their registers: 80 against 77.5 us), or
+// 1024 where there are too few rows to fill the chip. Rows of up to 16384 elements stay in registers
 // (1024 threads have 128 registers each: two 16-bit chunks or four fp32).
 RowShape forward_shape(int64_t T, int64_t d, int epc) {
   const int64_t ch = (d + epc - 1) / epc;
@@ -525,7 +542,8 @@ RowShape forward_shape(int64_t T, int64_t d, int epc) {
     return (int)(c <= 1 ? 1 : (c <= 2 ? 2 : (c <= 4 ? 4 : (c <= 8 ? 8 : 0))));
   };
   if (ch <= 256 && (T >= 512 || ch <= 64)) return RowShape{64, fit(64)};
-  if (ch <= 2048 && (T >= 512 || ch <= 256)) return RowShape{256, fit(256)};
+  if (ch <= 512 && (T >= 512 || ch <= 256)) return RowShape{256, fit(256)};
+  if (ch <= 2048 && T >= 512) return RowShape{512, fit(512)};
   return ch <= (epc == 8 ? 2048 : 4096) ? RowShape{1024, fit(1024)} : RowShape{0, 0};
 }
 
@@ -544,7 +562,7 @@ RowShape backward_shape(int64_t d, int epc) {
 // units), few enough that the dweight partials stay small beside the rows.
 int64_t backward_grid(int64_t T, int64_t d, int epc) {
   const RowShape r = backward_shape(d, epc);
-  const int64_t g = r.nt == 64 ? 2048 : 512;
+  const int64_t g = r.nt == 64 ? 2048 : (r.nt == 256 ? 512 : 256);
   return T < g ? T : g;
 }
 
@@ -560,8 +578,11 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
   const RowShape r = forward_shape(a.T, a.d, Elem<T>::epc);
 #define DORA_NORM(NT, C)                                                                                   \
   if (r.nt == NT && r.c == C) {                                                                            \
-    hipLaunchKernelGGL((rms_norm_kernel<T, NT, C>), dim3(grid_of(NT == 64 ? (a.T + 3) / 4 : a.T, NT)),     \
-                       dim3(NT == 64 ? 256 : NT), 0, st, a);                                               \
+    const dim3 grid(grid_of(NT == 64 ? (a.T + 3) / 4 : a.T, NT)), block(NT == 64 ? 256 : NT);              \
+    if (a.T * a.d * (int64_t)sizeof(T) > kStreamBytes)                                                     \
+      hipLaunchKernelGGL((rms_norm_kernel<T, NT, C, true>), grid, block, 0, st, a);                        \
+    else                                                                                                   \
+      hipLaunchKernelGGL((rms_norm_kernel<T, NT, C, false>), grid, block, 0, st, a);                       \
     return hipGetLastError();                                                                              \
   }
   DORA_NORM(64, 1)
@@ -569,8 +590,8 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
   DORA_NORM(64, 4)
   DORA_NORM(256, 1)
   DORA_NORM(256, 2)
-  DORA_NORM(256, 4)
-  DORA_NORM(256, 8)
+  DORA_NORM(512, 2)
+  DORA_NORM(512, 4)
   DORA_NORM(1024, 1)
   DORA_NORM(1024, 2)
   if constexpr (Elem<T>::epc == 4) {
@@ -589,7 +610,10 @@ hipError_t launch_bwd(NormBwdArgs a, float* dweight, hipStream_t st) {
     hipError_t e = hipErrorInvalidValue;
 #define DORA_NORM_BWD(NT, C)                                                                            \
   if (r.nt == NT && r.c == C) {                                                                         \
-    hipLaunchKernelGGL((rms_norm_bwd_kernel<T, NT, C>), dim3((unsigned)grid), dim3(NT), 0, st, a);      \
+    if (a.T * a.d * (int64_t)sizeof(T) > kStreamBytes)                                                  \
+      hipLaunchKernelGGL((rms_norm_bwd_kernel<T, NT, C, true>), dim3((unsigned)grid), dim3(NT), 0, st, a);  \
+    else                                                                                                \
+      hipLaunchKernelGGL((rms_norm_bwd_kernel<T, NT, C, false>), dim3((unsigned)grid), dim3(NT), 0, st, a); \
     e = hipGetLastError();                                                                              \
   }
     DORA_NORM_BWD(64, 1)
