@@ -146,13 +146,19 @@ struct Raw8 {
   u32x4 v[8 / Elem<O>::epc];
 };
 
-template <typename O>
+template <typename O, bool STREAM = false>
 __device__ __forceinline__ Raw8<O> load_raw8(const O* p, int n) {
   constexpr int E = Elem<O>::epc;
   Raw8<O> r;
   if (n >= 8) {
 #pragma unroll
-    for (int i = 0; i < 8 / E; ++i) r.v[i] = *reinterpret_cast<const u32x4_any*>(p + i * E);
+    for (int i = 0; i < 8 / E; ++i) {
+      const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p + i * E);
+      if constexpr (STREAM)
+        r.v[i] = __builtin_nontemporal_load(q);
+      else
+        r.v[i] = *q;
+    }
   } else {
     O tmp[8];
 #pragma unroll
@@ -913,8 +919,9 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
     for (int i = 0; i < U; ++i) {
       const int64_t m = m0 + i * step;
       if (m < M) {
-        ry[i] = load_raw8<T>(dy + m * N + n, nv);
-        ru[i] = load_raw8<T>(u + m * N + n, nv);
+        // (du, which the products read next, is to stay in the caches)
+        ry[i] = load_raw8<T, true>(dy + m * N + n, nv);
+        ru[i] = load_raw8<T, true>(u + m * N + n, nv);
       }
     }
 #pragma unroll
