@@ -79,11 +79,26 @@ __device__ __forceinline__ float logistic(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896f * v));
 }
 
+// Phi(z) = (1 + erf(z / sqrt 2)) / 2 by Abramowitz and Stegun 7.1.26: with t =
+// 1 / (1 + p x), erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2) within 1.5e-7, an
+// absolute error below fp32's own at 1; a third of erff's instructions.
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  const float h = 0.5f * (q * t) * __builtin_amdgcn_exp2f(-1.44269504088896f * (x * x));   // erfc(x) / 2
+  return z < 0.f ? h : 1.f - h;
+}
+
 __device__ __forceinline__ float act1(float z, int act) {
   switch (act) {
     case 1: return z < 0.f ? 0.f : z;
-    case 2: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case 3: return z * logistic(2.f * kTanhK * fmaf(kTanhC * z * z, z, z));
+    case 2: return z * normal_cdf(z);
+    // z / 2 (1 + tanh(v)) = z / (1 + exp(-2 v))
+    case 3: return z * logistic(z * fmaf(2.f * kTanhK * kTanhC, z * z, 2.f * kTanhK));
     case 4: return z * logistic(z);
     default: return z;
   }
@@ -109,9 +124,9 @@ __device__ __forceinline__ void act_all(float (&z)[N], int act) {
 __device__ __forceinline__ float slope_of(float z, int act) {
   switch (act) {
     case 1: return z > 0.f ? 1.f : (z != z ? z : 0.f);
-    case 2: return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+    case 2: return normal_cdf(z) + z * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.72134752044448f * (z * z));
     case 3: {
-      const float p = logistic(2.f * kTanhK * fmaf(kTanhC * z * z, z, z));
+      const float p = logistic(z * fmaf(2.f * kTanhK * kTanhC, z * z, 2.f * kTanhK));
       return p + z * p * (1.f - p) * 2.f * kTanhK * fmaf(3.f * kTanhC * z, z, 1.f);
     }
     case 4: {
@@ -341,18 +356,19 @@ __device__ __forceinline__ u32x4 read_tr(const char* unit, int r0, int s, int la
 // ---------------------------------------------------------------------------
 // Tile kernel. Workgroup = WM x WN waves = one tile of (WM MB 32) rows by
 // (WN NB 32) columns over one part of the depth. A stage is 128 bytes of depth
-// of both operands. LDS holds a ring of five units of one operand's stage:
-// stage i's rows are in unit 2i mod 5 and its columns in unit 2i + 1. With
-// stage i + 1 and the rows of stage i + 2 already there, the two units that
-// stage i frees take the columns of stage i + 2 first and the rows of stage
-// i + 3 after them: half of the loads have a whole stage to land and half
-// have two. One barrier a stage, where a wave has read all of stage i; a wave
-// holds two sets of fragments and reads the next step's while this step's
-// matrix instructions run.
+// of both operands. LDS holds a ring of 2P + 1 units of one operand's stage:
+// stage i's rows are in unit 2i and its columns in unit 2i + 1 (mod 2P + 1).
+// With the stages up to i + P - 1 and the rows of stage i + P already there,
+// the two units that stage i frees take the columns of stage i + P first and
+// the rows of stage i + P + 1 after them. At P = 2, which fills LDS for the
+// 256-row tile, half of the loads so have a whole stage to land and half have
+// two (8192^3 bf16: 806 us, against 860 us with two slots of whole stages and
+// the next lines asked into L2 ahead); the 64-row tile takes P = 4. One
+// barrier a stage, where a wave has read all of stage i; a wave holds two sets
+// of fragments and reads the next step's while this step's matrix instructions
+// run.
 // ---------------------------------------------------------------------------
-constexpr int kUnits = 5;
-
-template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR, bool AT, bool BT>
+template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT, bool BT>
 __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, E = 16 / ESZ, KT = 128 / ESZ;
   constexpr int NW = WM * WN, MT = WM * MB * 32, NT = WN * NB * 32;
@@ -360,10 +376,11 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   constexpr int ABLK = MT / 8 / NW, BBLK = NT / 8 / NW;   // 1 KiB blocks per wave per stage
   constexpr int BPW = ABLK + BBLK;
   constexpr int STEPS = 8 / (2 * FC);
-  constexpr int EPW = NB * 32 + 8;                         // floats of an epilogue row (padded: no bank conflicts)
+  constexpr int EPW = NB * 32 + 4;                         // floats of an epilogue row (padded: no bank conflicts)
   static_assert(MT % (8 * NW) == 0 && NT % (8 * NW) == 0, "a stage splits evenly over the waves");
-  static_assert(NW * 32 * EPW * 4 <= kUnits * UNIT, "the epilogue fits the ring");
-  static_assert(kUnits * UNIT <= 160 * 1024, "gfx950 has 160 KiB of LDS");
+  constexpr int RING = (2 * P + 1) * UNIT;
+  static_assert(NW * 32 * EPW * 4 <= RING, "the epilogue fits the ring");
+  static_assert(RING <= 160 * 1024, "gfx950 has 160 KiB of LDS");
   static_assert(STEPS % 2 == 0, "step s of every stage uses fragment set s & 1");
   extern __shared__ __align__(1024) char lds[];
 
@@ -495,51 +512,59 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       for (int l = l0; l < l1; ++l)
         if ((l - l0) * NM / (l1 - l0) == m) {
           if (l < BBLK)
-            issue_b(i + 2, ul, l);
+            issue_b(i + P, ul, l);
           else
-            issue_a(i + 3, um, l - BBLK);
+            issue_a(i + P + 1, um, l - BBLK);
         }
-      acc[m / NB][m % NB] = Op<T>::run(cur.a[m / NB], cur.b[m % NB], acc[m / NB][m % NB]);
+      acc[m / NB][m % NB] = Op<T>::run(cur.b[m % NB], cur.a[m / NB], acc[m / NB][m % NB]);   // (turned)
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Ring units (bytes) of stage i's rows and columns, and of stage i + 1's.
-  int u0 = 0, u1 = UNIT, u2 = 2 * UNIT, u3 = 3 * UNIT, u4 = 4 * UNIT;
+  // Byte offset of the k-th unit after the current stage's rows.
+  int u0 = 0;
+  auto unit = [&](int k) __attribute__((always_inline)) {
+    const int at = u0 + k * UNIT;
+    return at >= RING ? at - RING : at;
+  };
 #pragma unroll
-  for (int b = 0; b < ABLK; ++b) issue_a(st0, u0, b);
+  for (int j = 0; j < P; ++j) {
 #pragma unroll
-  for (int b = 0; b < BBLK; ++b) issue_b(st0, u1, b);
+    for (int b = 0; b < ABLK; ++b) issue_a(st0 + j, 2 * j * UNIT, b);
+    if (j + 1 < P) {
 #pragma unroll
-  for (int b = 0; b < ABLK; ++b) issue_a(st0 + 1, u2, b);
-  // (the columns of the second stage and the rows of the third: one period's
-  // loads, of which the first step's part goes out here)
+      for (int b = 0; b < BBLK; ++b) issue_b(st0 + j, (2 * j + 1) * UNIT, b);
+    }
+  }
+  // (the columns of stage P - 1 and the rows of stage P: one period's loads, of
+  // which the first step's part goes out here)
   constexpr int L1 = BPW / STEPS;
+  constexpr int LATER = (P - 1) * ABLK + (P - 2) * BBLK;   // loads younger than the next stage's
 #pragma unroll
   for (int l = 0; l < L1; ++l) {
     if (l < BBLK)
-      issue_b(st0 + 1, u3, l);
+      issue_b(st0 + P - 1, (2 * P - 1) * UNIT, l);
     else
-      issue_a(st0 + 2, u4, l - BBLK);
+      issue_a(st0 + P, 2 * P * UNIT, l - BBLK);
   }
-  wait_vm_lgkm0<ABLK + L1>();
+  wait_vm_lgkm0<LATER + L1>();
   barrier_keep_loads();
 #pragma unroll
-  for (int q = 0; q < ND; ++q) read(u0, u1, 0, F[0], q);
+  for (int q = 0; q < ND; ++q) read(0, UNIT, 0, F[0], q);
   // Every matrix instruction stands in this one loop body: with the last
   // step's outside of it the compiler moved all accumulators between register
   // files around the loop.
   auto stage = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s + 1 < STEPS; ++s)
-      step(F[s & 1], F[(s + 1) & 1], u0, u1, s + 1, i - 1, u3, u4, BPW * (s + 1) / STEPS, BPW * (s + 2) / STEPS);
+      step(F[s & 1], F[(s + 1) & 1], unit(0), unit(1), s + 1, i - 1, unit(2 * P - 1), unit(2 * P),
+           BPW * (s + 1) / STEPS, BPW * (s + 2) / STEPS);
     // This wave has read all of stage i, and its loads of stage i + 1 have
-    // landed; the rows of stage i + 2 stay in flight. Past the barrier the
-    // units of stage i take the next period's loads.
-    wait_vm_lgkm0<ABLK>();
+    // landed; younger ones stay in flight. Past the barrier the units of stage
+    // i take the next period's loads.
+    wait_vm_lgkm0<LATER>();
     barrier_keep_loads();
-    step(F[1], F[0], u2, u3, 0, i, u0, u1, 0, L1);
-    const int t0 = u0, t1 = u1;
-    u0 = u2, u1 = u3, u2 = u4, u3 = t0, u4 = t1;
+    step(F[1], F[0], unit(2), unit(3), 0, i, unit(0), unit(1), 0, L1);
+    u0 = unit(2);
   };
   int i = st0;
   if constexpr (PAIR) {
@@ -553,31 +578,34 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   barrier_keep_loads();
   // Epilogue: each wave turns its accumulators, 32 rows at a time, into rows
   // of eight columns a lane through its own part of LDS, so that loads and
-  // stores of the outputs are 16 bytes a lane along a row.
+  // stores of the outputs are 16 bytes a lane along a row. (The operands were
+  // given to the matrix instructions in turned order: a lane holds row lane %
+  // 32 of a block and four consecutive columns in each four accumulators, so
+  // that it writes 16 bytes at a time here too.)
+  // The code is one real loop over pairs of passes: unrolled, its instructions
+  // were fetched anew by every tile, which cost more than the loop. The
+  // accumulators are named by constants in a chain of uniform branches, since
+  // registers cannot be indexed. The residual's rows are loaded one pass ahead.
   float* ew = reinterpret_cast<float*>(lds) + wave * 32 * EPW;
-  // The epilogue's code is one real loop over pairs of passes: unrolled, its
-  // instructions were fetched anew by every tile, which cost more than the
-  // loop. The accumulators are named by constants in a chain of uniform
-  // branches, since registers cannot be indexed. The residual's rows are
-  // loaded one pass ahead.
   constexpr int IT = MB * PB / 2;
   const bool has_res = g.ep.residual != nullptr && g.splits == 1;
-  auto row_of = [&](int it, int i) __attribute__((always_inline)) {
-    return m0 + (wm * MB + it / (PB / 2)) * 32 + ((it % (PB / 2)) * 2 + i) * RPP + lane / LPR;
-  };
+  const int64_t m_first = m0 + wm * MB * 32 + lane / LPR;   // this lane's first row; the others RPP apart
+  const int64_t rows_left = g.M - m_first;
+  const int rl = nv <= 0 || rows_left <= 0 ? 0 : (int)(rows_left < MB * 32 ? rows_left : MB * 32);
+  const int64_t pass = (int64_t)RPP * g.N;                  // elements from one pass to the next
+  int64_t at = m_first * g.N + n;
   Raw8<O> next[2] = {};
-  auto load_res = [&](int it) __attribute__((always_inline)) {
+  auto load_res = [&](int it, int64_t from) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t m = row_of(it, i);
-      if (m < g.M && nv > 0) next[i] = load_raw8<O>(static_cast<const O*>(g.ep.residual) + m * g.N + n, nv);
-    }
+    for (int i = 0; i < 2; ++i)
+      if ((2 * it + i) * RPP < rl)
+        next[i] = load_raw8<O>(static_cast<const O*>(g.ep.residual) + from + i * pass, nv);
   };
-  if (has_res) load_res(0);
+  if (has_res) load_res(0, at);
 #pragma unroll 1
-  for (int it = 0; it < IT; ++it) {
+  for (int it = 0; it < IT; ++it, at += 2 * pass) {
     const Raw8<O> res[2] = {next[0], next[1]};
-    if (has_res && it + 1 < IT) load_res(it + 1);
+    if (has_res && it + 1 < IT) load_res(it + 1, at + 2 * pass);
     if (it % (PB / 2) == 0) {
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -586,7 +614,11 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) ew[acc_row(v, fg) * EPW + b * 32 + fr] = acc[c][b][v];
+          for (int q = 0; q < 4; ++q) {
+            typedef float f32x4v __attribute__((ext_vector_type(4)));
+            const f32x4v v = {acc[c][b][4 * q], acc[c][b][4 * q + 1], acc[c][b][4 * q + 2], acc[c][b][4 * q + 3]};
+            *reinterpret_cast<f32x4v*>(ew + fr * EPW + b * 32 + 8 * q + 4 * fg) = v;
+          }
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -598,9 +630,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       const int row = ((it % (PB / 2)) * 2 + i) * RPP + lane / LPR;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[8 * i + e] = ew[row * EPW + col + e];
-      m[i] = row_of(it, i);
-      off[i] = m[i] * g.N + n;
-      ok[i] = m[i] < g.M && nv > 0;
+      m[i] = m_first + (2 * it + i) * RPP;
+      off[i] = at + i * pass;
+      ok[i] = (2 * it + i) * RPP < rl;
     }
     if (g.splits > 1) {
 #pragma unroll
@@ -848,26 +880,28 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(GemmArgs g) {
   epilogue_rows<O, 1>(g.ep, v, cs, bs, ms, offs, ok, nv, res);
 }
 
-// Copy of [rows][K] (row stride K, any alignment) to row stride ld (a
-// multiple of 16 bytes), zeros from K on; bytes of ESZ-byte elements.
-template <int ESZ>
-__global__ __launch_bounds__(256) void pack_rows_kernel(const char* src, int64_t rows, int64_t K, int64_t ld,
-                                                        char* dst) {
-  const int64_t cpr = ld * ESZ / 16, kb = K * ESZ;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * cpr) return;
-  const int64_t r = i / cpr, c = (i - r * cpr) * 16;
-  const char* p = src + r * kb + c;
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (c + 16 <= kb) {
-    v = *reinterpret_cast<const u32x4_any*>(p);
-  } else if (c < kb) {
-    uint8_t tmp[16];
+// Copies of up to four operands [rows][kb bytes] (rows one after the other, at
+// any alignment) to rows of lb bytes (a multiple of 16), zeros from kb on, in
+// one launch. Job j's 16-byte chunks are numbers [first[j], first[j + 1]).
+struct PackJobs {
+  const char* src[4];
+  char* dst[4];
+  int64_t kb[4], lb[4], first[5];
+  int n;
+};
+
+__global__ __launch_bounds__(256) void pack_rows_kernel(PackJobs p) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.first[p.n]) return;
+  const char* src = p.src[0];
+  char* dst = p.dst[0];
+  int64_t kb = p.kb[0], lb = p.lb[0], base = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) tmp[e] = c + e < kb ? (uint8_t)p[e] : (uint8_t)0;
-    __builtin_memcpy(&v, tmp, 16);
-  }
-  *reinterpret_cast<u32x4*>(dst + r * ld * ESZ + c) = v;
+  for (int j = 1; j < 4; ++j)
+    if (j < p.n && i >= p.first[j]) src = p.src[j], dst = p.dst[j], kb = p.kb[j], lb = p.lb[j], base = p.first[j];
+  i -= base;
+  const int64_t cpr = lb / 16, r = i / cpr, c = (i - r * cpr) * 16;
+  *reinterpret_cast<u32x4*>(dst + r * lb + c) = load_bounded(src + r * kb, c, kb);
 }
 
 // dst[c][r] = src[r][c] for src [rows][cols] at row stride lds_; dst rows of
@@ -997,26 +1031,28 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, bool few, int*
     return;
   }
   // The tile and the split that a model of the time puts first, in cycles. A
-  // compute unit holds 1, 2 or 4 workgroups of 256-, 128- or 64-row tiles; a
+  // compute unit holds one workgroup of a 256-row tile or two of the others; a
   // stage of each costs it t^2 / 32 of matrix instructions (fp32: 16 times
   // that) or 4 t of loads, and a workgroup waits about kStageWait for a stage
-  // from memory (measured: 1500 to 1900 cycles a stage where 256 workgroups of
-  // either small tile run, whatever the tile). The parts of a split are added
-  // by a second launch that reads them all.
-  constexpr double kStageWait = 1600, kTileFixed = 8000, kJoinFixed = 12000, kBytesPerCycle = 2000;
+  // from memory with a ring of two stages ahead (measured: 1500 to 1900 cycles
+  // a stage where 256 workgroups of either small tile run), half of that with
+  // four. The parts of a split are added by a second launch that reads them
+  // all.
+  constexpr double kStageWait = 1600, kJoinFixed = 12000, kBytesPerCycle = 2000;
   double best = 0;
   *cfg = kTile64, *splits = 1;
   for (int c = kTile256; c <= kTile64; ++c) {
     if (c == kTile256 && dtype == 1) continue;   // (fp32 has no such kernel: its matrix instructions are slow)
-    const int t = tile_rows(c), fit = c == kTile256 ? 1 : (c == kTile128 ? 2 : 4);
+    const int t = tile_rows(c), fit = c == kTile256 ? 1 : 2;
     const int64_t n = up(M, t) / t * (up(N, t) / t);
     const double work = (dtype == 1 ? 16.0 : 1.0) * t * t / 32, load = 4.0 * t, busy = work > load ? work : load;
+    const double wait = c == kTile64 ? kStageWait / 2 : kStageWait;
     for (int s = 1; s <= 32 && (s == 1 || s <= stages / 4); ++s) {
       const int64_t groups = n * s, rounds = (groups + kCUs * fit - 1) / (kCUs * fit);
       const int64_t last = groups - (rounds - 1) * kCUs * fit;   // workgroups of the last round
       auto round = [&](int64_t g) {
         const double here = (double)((g + kCUs - 1) / kCUs) * busy;
-        return (double)((stages + s - 1) / s) * (here > kStageWait ? here : kStageWait) + kTileFixed;
+        return (double)((stages + s - 1) / s) * (here > wait ? here : wait) + 4000 + 16 * t;
       };
       double time = (double)(rounds - 1) * round((int64_t)kCUs * fit) + round(last);
       if (s > 1) time += kJoinFixed + 8.0 * s * (double)M * (double)N / kBytesPerCycle;
@@ -1025,13 +1061,13 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, bool few, int*
   }
 }
 
-template <typename T, typename O, int WM, int WN, int MB, int NB, bool PAIR, bool AT = false, bool BT = false>
+template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT = false, bool BT = false>
 hipError_t launch_tile(GemmArgs g, hipStream_t st) {
   constexpr int MT = WM * MB * 32, NT = WN * NB * 32;
   g.n_mt = (int)((g.M + MT - 1) / MT);
   g.n_nt = (int)((g.N + NT - 1) / NT);
-  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB, PAIR, AT, BT>;
-  constexpr int lds = kUnits * (MT > NT ? MT : NT) * 128;
+  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB, P, PAIR, AT, BT>;
+  constexpr int lds = (2 * P + 1) * (MT > NT ? MT : NT) * 128;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k, dim3((unsigned)((int64_t)g.n_mt * g.n_nt * g.splits)), dim3(WM * WN * 64), lds, st, g);
@@ -1073,9 +1109,9 @@ template <typename T, bool AT>
 hipError_t launch_gemm_tr(GemmArgs g, int cfg, hipStream_t st) {
   split_stages(g, 64);
   hipError_t e = hipErrorInvalidValue;
-  if (cfg == kTile256) e = launch_tile<T, T, 2, 4, 4, 2, false, AT, true>(g, st);
-  if (cfg == kTile128) e = launch_tile<T, T, 2, 2, 2, 2, false, AT, true>(g, st);
-  if (cfg == kTile64) e = launch_tile<T, T, 2, 2, 1, 1, false, AT, true>(g, st);
+  if (cfg == kTile256) e = launch_tile<T, T, 2, 4, 4, 2, 2, false, AT, true>(g, st);
+  if (cfg == kTile128) e = launch_tile<T, T, 2, 2, 2, 2, 2, false, AT, true>(g, st);
+  if (cfg == kTile64) e = launch_tile<T, T, 2, 2, 1, 1, 4, false, AT, true>(g, st);
   return e != hipSuccess || g.splits == 1 ? e : launch_join<T>(g, st);
 }
 
@@ -1089,20 +1125,20 @@ hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
   if (g.K2 > 0) {
     if constexpr (Op<T>::esz > 1) {   // (no pair in e4m3)
       if constexpr (Op<T>::esz == 2) {
-        if (cfg == kTile256) e = launch_tile<T, O, 2, 4, 4, 2, true>(g, st);
+        if (cfg == kTile256) e = launch_tile<T, O, 2, 4, 4, 2, 2, true>(g, st);
       }
-      if (cfg == kTile128) e = launch_tile<T, O, 2, 2, 2, 2, true>(g, st);
-      if (cfg == kTile64) e = launch_tile<T, O, 2, 2, 1, 1, true>(g, st);
+      if (cfg == kTile128) e = launch_tile<T, O, 2, 2, 2, 2, 2, true>(g, st);
+      if (cfg == kTile64) e = launch_tile<T, O, 2, 2, 1, 1, 4, true>(g, st);
     }
   } else {
     if constexpr (Op<T>::esz == 2) {
-      if (cfg == kTile256) e = launch_tile<T, O, 2, 4, 4, 2, false>(g, st);
+      if (cfg == kTile256) e = launch_tile<T, O, 2, 4, 4, 2, 2, false>(g, st);
     }
     if constexpr (Op<T>::esz == 1) {
-      if (cfg == kTile256) e = launch_tile<T, O, 2, 2, 4, 4, false>(g, st);
+      if (cfg == kTile256) e = launch_tile<T, O, 2, 2, 4, 4, 2, false>(g, st);
     }
-    if (cfg == kTile128) e = launch_tile<T, O, 2, 2, 2, 2, false>(g, st);
-    if (cfg == kTile64) e = launch_tile<T, O, 2, 2, 1, 1, false>(g, st);
+    if (cfg == kTile128) e = launch_tile<T, O, 2, 2, 2, 2, 2, false>(g, st);
+    if (cfg == kTile64) e = launch_tile<T, O, 2, 2, 1, 1, 4, false>(g, st);
   }
   return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
 }
@@ -1119,20 +1155,6 @@ hipError_t gemm(const GemmArgs& g, int dtype, int out_dtype, int cfg, hipStream_
         default: return launch_gemm<e4m3_t, float>(g, cfg, st);
       }
   }
-}
-
-hipError_t pack_rows(const void* src, int64_t rows, int64_t K, int64_t ld, int esz, void* dst, hipStream_t st) {
-  const int64_t n = rows * (ld * esz / 16);
-  if (n == 0) return hipSuccess;
-  const dim3 grid((unsigned)((n + 255) / 256));
-  const char* s = static_cast<const char*>(src);
-  char* d = static_cast<char*>(dst);
-  switch (esz) {
-    case 1: hipLaunchKernelGGL((pack_rows_kernel<1>), grid, dim3(256), 0, st, s, rows, K, ld, d); break;
-    case 2: hipLaunchKernelGGL((pack_rows_kernel<2>), grid, dim3(256), 0, st, s, rows, K, ld, d); break;
-    default: hipLaunchKernelGGL((pack_rows_kernel<4>), grid, dim3(256), 0, st, s, rows, K, ld, d); break;
-  }
-  return hipGetLastError();
 }
 
 hipError_t transpose(const void* src, int64_t rows, int64_t cols, int64_t lsrc, int64_t ld, int esz, void* dst,
@@ -1176,20 +1198,23 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
                          int64_t K, const void* t, const void* b, int64_t r, float s, const Epilogue& ep,
                          int out_dtype, char* ws, hipStream_t st) {
   const int esz = elem_size(dtype);
-  struct Job {
-    bool pack;
-    const void** p;
-    int64_t rows, depth, ld;
-    size_t off;
-  } jobs[] = {{p.pack_x, &x, M, K, p.ldx, p.off_x},
-              {p.pack_w, &w, N, K, p.ldw, p.off_w},
-              {p.pack_t, &t, M, r, p.ldt, p.off_t},
-              {p.pack_b, &b, N, r, p.ldb, p.off_b}};
-  for (Job& j : jobs) {
-    if (!j.pack) continue;
-    const hipError_t e = pack_rows(*j.p, j.rows, j.depth, j.ld, esz, ws + j.off, st);
+  PackJobs jobs{};
+  auto pack = [&](bool yes, const void** src, int64_t rows, int64_t depth, int64_t ld, size_t off) {
+    if (!yes) return;
+    const int j = jobs.n++;
+    jobs.src[j] = static_cast<const char*>(*src), jobs.dst[j] = ws + off;
+    jobs.kb[j] = depth * esz, jobs.lb[j] = ld * esz;
+    jobs.first[j + 1] = jobs.first[j] + rows * (ld * esz / 16);
+    *src = ws + off;
+  };
+  pack(p.pack_x, &x, M, K, p.ldx, p.off_x);
+  pack(p.pack_w, &w, N, K, p.ldw, p.off_w);
+  pack(p.pack_t, &t, M, r, p.ldt, p.off_t);
+  pack(p.pack_b, &b, N, r, p.ldb, p.off_b);
+  if (jobs.n > 0) {
+    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)((jobs.first[jobs.n] + 255) / 256)), dim3(256), 0, st, jobs);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    *j.p = ws + j.off;
   }
   GemmArgs g{};
   g.a = x, g.b = w, g.lda = p.ldx, g.ldb = p.ldw, g.K = K;
