@@ -49,6 +49,7 @@ __all__ = [
     "dora_rms_norm_backward_workspace_size",
     "dora_matmul",
     "dora_matmul_workspace_size",
+    "dora_matmul_plan_info",
     "dora_matmul_backward",
     "dora_matmul_backward_workspace_size",
 ]
@@ -120,6 +121,7 @@ def load():
         "dora_rms_norm_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_p, _c_p, _c_p,
                                           _c_sz, _c_p]),
         "dora_matmul_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i, _c_i, ctypes.POINTER(_c_sz)]),
+        "dora_matmul_plan_info": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i, _c_i, ctypes.POINTER(_c_i64), _c_i]),
         "dora_matmul": (_c_i, [_c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_f, _c_p,
                                _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
         "dora_matmul_backward_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, ctypes.POINTER(_c_sz)]),
@@ -526,9 +528,18 @@ def dora_rms_norm_backward_workspace_size(T: int, d: int, dtype) -> int:
     return _size_of("dora_rms_norm_backward_workspace_size", T, d, _dtype_code(dtype))
 
 
+def _operand_code(dtype) -> int:
+    return DORA_E4M3 if dtype in (_E4M3, "e4m3", DORA_E4M3) else _dtype_code(dtype)
+
+
 def dora_matmul_workspace_size(M: int, N: int, K: int, r: int, dtype, aligned_operands: int = 15) -> int:
-    code = DORA_E4M3 if dtype in (_E4M3, "e4m3", DORA_E4M3) else _dtype_code(dtype)
-    return _size_of("dora_matmul_workspace_size", M, N, K, r, code, aligned_operands)
+    return _size_of("dora_matmul_workspace_size", M, N, K, r, _operand_code(dtype), aligned_operands)
+
+
+def dora_matmul_plan_info(M: int, N: int, K: int, r: int, dtype, aligned_operands: int = 15) -> dict:
+    buf = (_c_i64 * 4)()
+    _call("dora_matmul_plan_info", M, N, K, r, _operand_code(dtype), aligned_operands, buf, 4)
+    return dict(zip(("tile_rows", "splits", "copies", "workspace_bytes"), list(buf)))
 
 
 def dora_matmul_backward_workspace_size(M: int, N: int, K: int, dtype, outputs: int = 31) -> int:

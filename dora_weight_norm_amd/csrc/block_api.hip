@@ -27,7 +27,7 @@ struct Span {
 
 // Every element of a tensor is reached with 64-bit arithmetic far from its
 // limits, and every launch stays within its grid.
-constexpr int64_t kMaxElems = (int64_t)1 << 34;
+constexpr int64_t kMaxElems = (int64_t)1 << 33;
 // Bytes of one row of a product's operand (the tile kernel's 32-bit offsets
 // span 256 rows).
 constexpr int64_t kMaxRowBytes = (int64_t)1 << 23;
@@ -126,6 +126,19 @@ dora_status dora_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int64_t 
   if (!valid_dtype(dtype) && dtype != DORA_E4M3) return DORA_ERR_UNSUPPORTED_DTYPE;
   if (ws_bytes == nullptr || !matmul_sizes_ok(M, N, K, r, operand_size(dtype))) return DORA_ERR_INVALID_ARG;
   *ws_bytes = M > 0 && N > 0 ? dora::plan_matmul(M, N, K, r, dtype, aligned_operands).ws_bytes : 0;
+  return DORA_OK;
+}
+
+dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, int aligned_operands,
+                                  int64_t* info, int n_info) {
+  if (!valid_dtype(dtype) && dtype != DORA_E4M3) return DORA_ERR_UNSUPPORTED_DTYPE;
+  if (info == nullptr || n_info < 0 || !matmul_sizes_ok(M, N, K, r, operand_size(dtype))) return DORA_ERR_INVALID_ARG;
+  const dora::MatmulPlan p = M > 0 && N > 0 ? dora::plan_matmul(M, N, K, r, dtype, aligned_operands)
+                                            : dora::MatmulPlan{};
+  const int rows = p.cfg == dora::kTile256 ? 256 : (p.cfg == dora::kTile128 ? 128 : (p.cfg == dora::kTile64 ? 64 : 0));
+  const int copies = (p.pack_x ? 1 : 0) | (p.pack_w ? 2 : 0) | (p.pack_t ? 4 : 0) | (p.pack_b ? 8 : 0);
+  const int64_t vals[] = {M > 0 && N > 0 ? rows : -1, p.splits, copies, (int64_t)p.ws_bytes};
+  for (int i = 0; i < n_info; ++i) info[i] = i < 4 ? vals[i] : -1;
   return DORA_OK;
 }
 

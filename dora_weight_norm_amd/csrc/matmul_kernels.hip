@@ -910,7 +910,8 @@ template <typename U>
 __global__ __launch_bounds__(256) void transpose_kernel(const U* src, int64_t rows, int64_t cols, int64_t lsrc,
                                                         int64_t ld, U* dst) {
   __shared__ U tile[64][65];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+  const int64_t nr = (ld + 63) / 64;   // row tiles (of the destination's stride, so that its padding is written)
+  const int64_t r0 = blockIdx.x % nr * 64, c0 = blockIdx.x / nr * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -1159,8 +1160,7 @@ hipError_t gemm(const GemmArgs& g, int dtype, int out_dtype, int cfg, hipStream_
 
 hipError_t transpose(const void* src, int64_t rows, int64_t cols, int64_t lsrc, int64_t ld, int esz, void* dst,
                      hipStream_t st) {
-  // (x covers ld, so that the padding is written too)
-  const dim3 grid((unsigned)((ld + 63) / 64), (unsigned)((cols + 63) / 64));
+  const dim3 grid((unsigned)((ld + 63) / 64 * ((cols + 63) / 64)));
   if (esz == 2)
     hipLaunchKernelGGL((transpose_kernel<uint16_t>), grid, dim3(256), 0, st, static_cast<const uint16_t*>(src), rows,
                        cols, lsrc, ld, static_cast<uint16_t*>(dst));

@@ -421,6 +421,17 @@ dora_status dora_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int64_t 
                                        size_t* ws_bytes);
 
 /*
+ * The plan dora_matmul would use, for diagnostics and tests: info[0 ..
+ * n_info-1] are, in order, the rows of its tile (256, 128 or 64; 0: the
+ * kernel for few rows; -1: nothing to do), the parts the depth is split into
+ * (more than one are added by a second launch), a bit for each operand that
+ * is copied first (as in dora_matmul_workspace_size), and the workspace
+ * bytes; further entries are -1. Host only.
+ */
+dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, int aligned_operands,
+                                  int64_t* info, int n_info);
+
+/*
  * Matrix product with its epilogue:
  *
  *   u[m,n] = row_scale[m] * (sum_k x[m,k] w[n,k] + s * sum_l t[m,l] b[n,l])

@@ -100,6 +100,24 @@ def test_matmul_workspace():
     assert f(4, 4, 4, 0, 0, 15, None) == 1 and f(-4, 4, 4, 0, 0, 15, ctypes.byref(sz)) == 1
 
 
+def test_matmul_plans_cover_every_kernel():
+    # (the shapes of the GPU tests' coverage list; see test_gpu_matmul.py)
+    def plan(*a, **k):
+        p = bnd.dora_matmul_plan_info(*a, **k)
+        return p["tile_rows"], p["splits"] > 1, p["copies"]
+
+    assert plan(8192, 8192, 8192, 384, "bf16") == (256, False, 0)
+    assert plan(16, 28672, 8192, 0, "e4m3")[0] == 0 and plan(32, 64, 64, 0, "bf16")[0] == 0
+    assert plan(33, 64, 64, 0, "bf16")[0] == 64
+    assert plan(64, 8192, 8192, 0, "bf16")[1]
+    assert plan(333, 1001, 777, 24, "f16") == (64, False, 3)
+    assert plan(333, 1001, 777, 20, "f16")[2] == 15 and plan(333, 1001, 776, 24, "f16", aligned_operands=11)[2] == 4
+    assert bnd.dora_matmul_plan_info(0, 8, 8, 0, "bf16")["tile_rows"] == -1
+    f, info = bnd.load().dora_matmul_plan_info, (ctypes.c_int64 * 6)()
+    assert f(64, 64, 64, 0, 0, 15, info, 6) == 0 and info[4] == info[5] == -1
+    assert f(64, 64, 64, 0, 0, 15, None, 4) == 1 and f(64, 64, 64, 0, 9, 15, info, 4) == 2
+
+
 def _mm_bwd(dy=0x1000000, u=0x2000000, x=0x3000000, w=0x4000000, dtype=0, M=4, N=32, K=64, col_scale=None, bias=None,
             act=0, du=None, dx=0x5000000, dw=0x6000000, dbias=0x7000000, dcol=0x7100000, ws=0x8000000,
             ws_bytes=1 << 24):

@@ -113,6 +113,22 @@ def test_few_rows(M, N, K, r, dtype):
     check(o, rng, dtype, "bf16" if dtype == "e4m3" else dtype, ACTS[N % 5], True, True)
 
 
+# One shape for each kernel and what may come with it: (M, N, K, r, tile rows, split depth).
+COVER = [(4100, 4104, 264, 0, 256, False), (4100, 4104, 264, 40, 256, False), (1030, 4104, 2056, 0, 128, None),
+         (1030, 4104, 520, 24, 128, None), (70, 520, 4104, 16, 64, True), (300, 520, 264, 16, 64, False),
+         (16, 200, 8200, 16, 0, True)]
+
+
+@pytest.mark.parametrize("M,N,K,r,rows,split,dtype", [(*c, t) for c in COVER for t in ("bf16", "f16", "f32", "e4m3")
+                                                       if t != "e4m3" or c[3] == 0])
+def test_every_kernel(M, N, K, r, rows, split, dtype):
+    if dtype in ("bf16", "f16"):     # (the other types' stages hold other depths: their tiles differ)
+        plan = bnd.dora_matmul_plan_info(M, N, K, r, dtype)
+        assert plan["tile_rows"] == rows and split in (None, plan["splits"] > 1), plan
+    o, rng = operands(M, N, K, r, dtype, M + K)
+    check(o, rng, dtype, "bf16" if dtype == "e4m3" else dtype, ACTS[1 + K % 4], K % 16 == 8, True)
+
+
 def test_plain_product_without_any_epilogue():
     o, _ = operands(50, 70, 90, 0, "bf16", 5)
     y, u = bnd.dora_matmul(o["x"], o["w"])
@@ -165,7 +181,7 @@ def test_empty_products():
     assert dx.shape == (0, 16) and (dw == 0).all() and (db == 0).all() and (dc == 0).all()
 
 
-BWD = [(1, 1, 1), (3, 40, 64), (17, 129, 77), (64, 256, 256), (100, 264, 520), (333, 1001, 777), (600, 72, 1288),
+BWD = [(4100, 264, 4104), (264, 4104, 4112), (1, 1, 1), (3, 40, 64), (17, 129, 77), (64, 256, 256), (100, 264, 520), (333, 1001, 777), (600, 72, 1288),
        (1, 512, 640), (300, 2048, 64), (2000, 136, 128), (1544, 2568, 264)]
 
 
