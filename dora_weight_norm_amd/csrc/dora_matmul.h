@@ -57,9 +57,10 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
 
 struct MatmulBackwardPlan {
   bool du_direct;                               // du is written into the caller's array alone
-  bool direct;                                  // the products read x, w and du as they lie
+  bool direct;                                  // the products read x, w and du in their own layout,
+  bool copy;                                    // x and w from copies with a row stride of ldk
   int64_t rows;                                 // row blocks of the element-wise pass
-  int64_t ldn, ldm;                             // padded N and M
+  int64_t ldn, ldm, ldk;                        // padded N, M and K
   int cfg_dx, cfg_dw, splits_dx, splits_dw;
   size_t off_du, off_dut, off_wt, off_xt, off_sum, off_part;
   size_t ws_bytes;

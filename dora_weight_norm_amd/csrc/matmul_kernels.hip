@@ -1158,6 +1158,20 @@ hipError_t gemm(const GemmArgs& g, int dtype, int out_dtype, int cfg, hipStream_
   }
 }
 
+// Adds a copy of *src to the jobs and points *src at it.
+void add_pack(PackJobs& p, const void** src, int64_t rows, int64_t kb, int64_t lb, char* dst) {
+  const int j = p.n++;
+  p.src[j] = static_cast<const char*>(*src), p.dst[j] = dst, p.kb[j] = kb, p.lb[j] = lb;
+  p.first[j + 1] = p.first[j] + rows * (lb / 16);
+  *src = dst;
+}
+
+hipError_t launch_pack(const PackJobs& p, hipStream_t st) {
+  if (p.n == 0 || p.first[p.n] == 0) return hipSuccess;
+  hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)((p.first[p.n] + 255) / 256)), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
 hipError_t transpose(const void* src, int64_t rows, int64_t cols, int64_t lsrc, int64_t ld, int esz, void* dst,
                      hipStream_t st) {
   const dim3 grid((unsigned)((ld + 63) / 64 * ((cols + 63) / 64)));
@@ -1199,23 +1213,12 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
                          int out_dtype, char* ws, hipStream_t st) {
   const int esz = elem_size(dtype);
   PackJobs jobs{};
-  auto pack = [&](bool yes, const void** src, int64_t rows, int64_t depth, int64_t ld, size_t off) {
-    if (!yes) return;
-    const int j = jobs.n++;
-    jobs.src[j] = static_cast<const char*>(*src), jobs.dst[j] = ws + off;
-    jobs.kb[j] = depth * esz, jobs.lb[j] = ld * esz;
-    jobs.first[j + 1] = jobs.first[j] + rows * (ld * esz / 16);
-    *src = ws + off;
-  };
-  pack(p.pack_x, &x, M, K, p.ldx, p.off_x);
-  pack(p.pack_w, &w, N, K, p.ldw, p.off_w);
-  pack(p.pack_t, &t, M, r, p.ldt, p.off_t);
-  pack(p.pack_b, &b, N, r, p.ldb, p.off_b);
-  if (jobs.n > 0) {
-    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)((jobs.first[jobs.n] + 255) / 256)), dim3(256), 0, st, jobs);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  if (p.pack_x) add_pack(jobs, &x, M, K * esz, p.ldx * esz, ws + p.off_x);
+  if (p.pack_w) add_pack(jobs, &w, N, K * esz, p.ldw * esz, ws + p.off_w);
+  if (p.pack_t) add_pack(jobs, &t, M, r * esz, p.ldt * esz, ws + p.off_t);
+  if (p.pack_b) add_pack(jobs, &b, N, r * esz, p.ldb * esz, ws + p.off_b);
+  const hipError_t e = launch_pack(jobs, st);
+  if (e != hipSuccess) return e;
   GemmArgs g{};
   g.a = x, g.b = w, g.lda = p.ldx, g.ldb = p.ldw, g.K = K;
   g.a2 = r > 0 ? t : nullptr, g.b2 = r > 0 ? b : nullptr, g.lda2 = p.ldt, g.ldb2 = p.ldb, g.K2 = r;
@@ -1243,10 +1246,15 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.du_direct = du_direct && N % epc == 0;
   p.off_du = take(p.du_direct ? 0 : (size_t)(M * p.ldn) * esz);
   p.off_sum = take(need_sums ? (size_t)(p.rows * 2 * N) * 4 : 0);
-  p.direct = dtype != 1 && aligned_xw && N % epc == 0 && K % epc == 0;
-  p.off_wt = take(need_dx && !p.direct ? (size_t)(K * p.ldn) * esz : 0);
+  // 16-bit products read du, w and x as they lie, copied to whole chunks where
+  // their rows are none; fp32 ones (whose elements no transposing read takes)
+  // read transposed copies.
+  p.direct = dtype != 1;
+  p.ldk = up(K, epc);
+  p.copy = p.direct && (!aligned_xw || K % epc != 0);
+  p.off_wt = take(!need_dx ? 0 : (p.copy ? (size_t)(N * p.ldk) * esz : (p.direct ? 0 : (size_t)(K * p.ldn) * esz)));
   p.off_dut = take(need_dw && !p.direct ? (size_t)(N * p.ldm) * esz : 0);
-  p.off_xt = take(need_dw && !p.direct ? (size_t)(K * p.ldm) * esz : 0);
+  p.off_xt = take(!need_dw ? 0 : (p.copy ? (size_t)(M * p.ldk) * esz : (p.direct ? 0 : (size_t)(K * p.ldm) * esz)));
   size_t part = 0;
   if (need_dx) {
     choose_tile(M, K, up(N, KT) / KT, dtype, !p.direct, &p.cfg_dx, &p.splits_dx);
@@ -1300,15 +1308,23 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   GemmArgs g{};
   g.part = reinterpret_cast<float*>(ws + p.off_part);
   if (p.direct) {
+    if (p.copy) {
+      PackJobs jobs{};
+      if (dx) add_pack(jobs, &w, N, K * esz, p.ldk * esz, ws + p.off_wt);
+      if (dw) add_pack(jobs, &x, M, K * esz, p.ldk * esz, ws + p.off_xt);
+      e = launch_pack(jobs, st);
+      if (e != hipSuccess) return e;
+    }
+    const int64_t ldu = p.du_direct ? N : p.ldn, ldk = p.copy ? p.ldk : K;
     // dx: du along the depth, w across it; dw: both across it.
     if (dx && M > 0 && K > 0) {
-      g.a = d, g.b = w, g.lda = N, g.ldb = K, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
+      g.a = d, g.b = w, g.lda = ldu, g.ldb = ldk, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
       g.ep.y = dx;
       e = dtype == 0 ? launch_gemm_tr<bf16_t, false>(g, p.cfg_dx, st) : launch_gemm_tr<f16_t, false>(g, p.cfg_dx, st);
       if (e != hipSuccess) return e;
     }
     if (dw && N > 0 && K > 0) {
-      g.a = d, g.b = x, g.lda = N, g.ldb = K, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
+      g.a = d, g.b = x, g.lda = ldu, g.ldb = ldk, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
       g.ep.y = dw;
       e = dtype == 0 ? launch_gemm_tr<bf16_t, true>(g, p.cfg_dw, st) : launch_gemm_tr<f16_t, true>(g, p.cfg_dw, st);
     }
