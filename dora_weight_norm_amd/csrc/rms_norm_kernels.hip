@@ -25,7 +25,9 @@ constexpr float kE4m3Max = 448.f;
 // Inputs of more than this stream past the caches, which they would only
 // empty: measured at 8192 x 8192 bf16 to 8 bits 84 us with ordinary loads and
 // stores, 77.5 us with non-temporal ones; at 777 x 3583, which the caches
-// hold, 8.1 and 8.6 us.
+// hold, 8.1 and 8.6 us. Loads only where rows are whole 128-byte lines: two
+// rows share a line otherwise, which was then read twice (5568 x 3000: 27.2 us
+// with both, 22.6 with the stores alone).
 constexpr int64_t kStreamBytes = (int64_t)16 << 20;
 constexpr int64_t kFwdGrid = 1024;   // workgroups of 256 threads, four a compute unit
 // Smallest scale: rows whose largest |n| is below 448 times it (about 2^-91)
@@ -182,7 +184,7 @@ struct NormArgs {
 // 256 / NT rows where NT is 64. A workgroup walks rows gridDim.x apart: its
 // weights are read once, and a row's loads go out before the row ahead of it
 // is reduced.
-template <typename T, int NT, int C, bool STREAM>
+template <typename T, int NT, int C, bool STREAM, bool LINES>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs a) {
   constexpr int E = Elem<T>::epc;
   // (two sets of words: a wave one row ahead uses the other one)
@@ -196,11 +198,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
   auto load = [&](int64_t t) __attribute__((always_inline)) {
     const T* x = static_cast<const T*>(a.x) + t * a.d;
 #pragma unroll
-    for (int c = 0; c < C; ++c) xv[c] = load_row_chunk<T, STREAM>(x, (int64_t)(c * NT + lane) * E, a.d);
+    for (int c = 0; c < C; ++c) xv[c] = load_row_chunk<T, STREAM && LINES>(x, (int64_t)(c * NT + lane) * E, a.d);
     if (has_res) {
       const T* res = static_cast<const T*>(a.residual) + t * a.d;
 #pragma unroll
-      for (int c = 0; c < C; ++c) rv[c] = load_row_chunk<T, STREAM>(res, (int64_t)(c * NT + lane) * E, a.d);
+      for (int c = 0; c < C; ++c) rv[c] = load_row_chunk<T, STREAM && LINES>(res, (int64_t)(c * NT + lane) * E, a.d);
     }
   };
   if (t0 < a.T) load(t0);
@@ -530,8 +532,9 @@ struct RowShape {
   int nt, c;
 };
 
-// Forward. Many short rows take a wave each (no barrier); other rows take
-// 256 threads, 512 past two chunks a thread (four of 8192 bf16 elements ran
+// Forward. Many short rows take a wave each (no barrier; 5568 x 1000: 10.8 us,
+// 15.9 with 256 threads a row), up to two chunks a thread; other rows take 256
+// threads (5568 x 1456: 16.8 us, 19.2 with a wave of four chunks a thread), 512 past two chunks a thread (four of 8192 bf16 elements ran
 // two workgroups a compute unit for their registers: 80 against 77.5 us), or
 // 1024 where there are too few rows to fill the chip. Rows of up to 16384 elements stay in registers
 // (1024 threads have 128 registers each: two 16-bit chunks or four fp32).
@@ -541,7 +544,7 @@ RowShape forward_shape(int64_t T, int64_t d, int epc) {
     const int64_t c = (ch + nt - 1) / nt;
     return (int)(c <= 1 ? 1 : (c <= 2 ? 2 : (c <= 4 ? 4 : (c <= 8 ? 8 : 0))));
   };
-  if (ch <= 256 && (T >= 512 || ch <= 64)) return RowShape{64, fit(64)};
+  if (ch <= 128 && (T >= 512 || ch <= 64)) return RowShape{64, fit(64)};
   if (ch <= 512 && (T >= 512 || ch <= 256)) return RowShape{256, fit(256)};
   if (ch <= 2048 && T >= 512) return RowShape{512, fit(512)};
   return ch <= (epc == 8 ? 2048 : 4096) ? RowShape{1024, fit(1024)} : RowShape{0, 0};
@@ -579,15 +582,16 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
 #define DORA_NORM(NT, C)                                                                                   \
   if (r.nt == NT && r.c == C) {                                                                            \
     const dim3 grid(grid_of(NT == 64 ? (a.T + 3) / 4 : a.T, NT)), block(NT == 64 ? 256 : NT);              \
-    if (a.T * a.d * (int64_t)sizeof(T) > kStreamBytes)                                                     \
-      hipLaunchKernelGGL((rms_norm_kernel<T, NT, C, true>), grid, block, 0, st, a);                        \
+    if (a.T * a.d * (int64_t)sizeof(T) <= kStreamBytes)                                                    \
+      hipLaunchKernelGGL((rms_norm_kernel<T, NT, C, false, false>), grid, block, 0, st, a);                \
+    else if (a.d * (int64_t)sizeof(T) % 128 != 0)                                                          \
+      hipLaunchKernelGGL((rms_norm_kernel<T, NT, C, true, false>), grid, block, 0, st, a);                 \
     else                                                                                                   \
-      hipLaunchKernelGGL((rms_norm_kernel<T, NT, C, false>), grid, block, 0, st, a);                       \
+      hipLaunchKernelGGL((rms_norm_kernel<T, NT, C, true, true>), grid, block, 0, st, a);                  \
     return hipGetLastError();                                                                              \
   }
   DORA_NORM(64, 1)
   DORA_NORM(64, 2)
-  DORA_NORM(64, 4)
   DORA_NORM(256, 1)
   DORA_NORM(256, 2)
   DORA_NORM(512, 2)
