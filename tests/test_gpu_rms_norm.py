@@ -19,7 +19,9 @@ EPS = 1e-6
 SHAPES = [(1, 1), (1, 7), (3, 8), (5, 513), (2, 511), (64, 256), (600, 1000), (513, 2048), (700, 2049), (520, 3583),
           (1, 4096), (7, 8192), (516, 8200), (1, 16384), (3, 16385), (2, 40003), (530, 16000), (0, 64),
           # more than 16 MiB of 16-bit rows: past the caches, several rows a workgroup
-          (9000, 1000), (2200, 4100), (1040, 8200)]
+          (9000, 1000), (2200, 4100), (1040, 8200),
+          # and in whole 128-byte lines
+          (9000, 1024), (2100, 4096), (1030, 8192)]
 
 
 def rel_n(d):
