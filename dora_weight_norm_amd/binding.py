@@ -137,7 +137,7 @@ def load():
 
 
 def _call(name: str, *args) -> None:
-    st = getattr(load(), name)(*args)
+    st = getattr(_lib or load(), name)(*args)
     if st != 0:
         raise DoraError(name, st)
 
@@ -446,6 +446,9 @@ def dora_compose_backward(dy, base, lora, g, s: float, need_dg: bool = True, wno
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _TORCH_DT = {torch.bfloat16: DORA_BF16, torch.float32: DORA_F32, torch.float16: DORA_F16}
 _E4M3 = torch.float8_e4m3fn
+# (the handle alone, without a Stream object around it)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 # A call of a single token takes the GPU a few microseconds, so the checks below
@@ -459,11 +462,13 @@ def _refuse(t, name: str, shape, dtype, dev: int):
 
 
 def _want(t, name: str, shape, dtype, dev: int) -> int:
-    """The address of a contiguous tensor of exactly this shape, dtype and GPU."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_cuda
-            or t.get_device() != dev or not t.is_contiguous()):
-        _refuse(t, name, shape, dtype, dev)
-    return t.data_ptr()
+    """The address of a contiguous tensor of exactly this shape, dtype and GPU (a host tensor's index is -1)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, dev)
 
 
 def _maybe(t, name: str, shape, dtype, dev: int):
@@ -472,13 +477,17 @@ def _maybe(t, name: str, shape, dtype, dev: int):
 
 def _first(t, name: str) -> int:
     """The GPU of the 2-D tensor that a call takes its shapes and dtype from."""
+    try:
+        dev = t.get_device()
+        if dev >= 0 and t.dim() == 2 and t.is_contiguous():
+            return dev
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device, got {t.device}")
-    if t.dim() != 2 or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and 2-D, got {tuple(t.shape)}")
-    return t.get_device()
+    raise ValueError(f"{name} must be contiguous and 2-D, got {tuple(t.shape)}")
 
 
 def _type_code(dtype) -> int:
@@ -490,7 +499,7 @@ def _type_code(dtype) -> int:
 
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_raw_stream(dev)
     if stream.device_index != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
     return stream.cuda_stream
@@ -552,19 +561,20 @@ def _rms_norm(x, weight, eps, residual, h, rstd, want_rstd, stream, y=None, q=No
     code = _type_code(dtype)
     T, d = shape
     f32 = torch.float32
-    pw = _maybe(weight, "weight", (d,), f32, dev)
-    pres = _maybe(residual, "residual", shape, dtype, dev)
-    if h is not None and residual is None:
+    pw = pres = ph = prs = py = pq = ps = None
+    if weight is not None:
+        pw = _want(weight, "weight", (d,), f32, dev)
+    if residual is not None:
+        pres = _want(residual, "residual", shape, dtype, dev)
+        if h is None:
+            h = _new(stream, shape, dtype, dev)
+        ph = _want(h, "h", shape, dtype, dev)
+    elif h is not None:
         raise ValueError("h needs a residual (without one, h is x)")
-    ph = _maybe(h, "h", shape, dtype, dev)
-    prs = _maybe(rstd, "rstd", (T,), f32, dev)
-    if residual is not None and h is None:
-        h = _new(stream, shape, dtype, dev)
-        ph = h.data_ptr()
     if rstd is None and want_rstd:
         rstd = _new(stream, (T,), f32, dev)
-        prs = rstd.data_ptr()
-    py = pq = ps = None
+    if rstd is not None:
+        prs = _want(rstd, "rstd", (T,), f32, dev)
     if quant:
         q = _new(stream, shape, _E4M3, dev) if q is None else q
         scale = _new(stream, (T,), f32, dev) if scale is None else scale
