@@ -674,6 +674,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 // The waves' sums are added in wave order through LDS, then the epilogue runs
 // on one element a thread. Rows at any element address are read as they are;
 // only the last partial step of the depth is read with bounds.
+// A small product of more rows takes the same kernel, a workgroup for each
+// 16 x 16 of the result: its eight waves share the depth that one wave of a
+// 64-row tile walks alone.
 // ---------------------------------------------------------------------------
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -806,8 +809,9 @@ __global__ __launch_bounds__(kFewWaves * 64, TF <= 2 ? 2 : 1) void matmul_few_ro
   __shared__ float red[kFewWaves * R * TF * 256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i8 = lane & 7, chunk = lane >> 3;
-  const int split = blockIdx.x / g.n_nt;
-  const int64_t n0 = (int64_t)(blockIdx.x - split * g.n_nt) * (8 * R);
+  const int row_block = blockIdx.x / g.n_nt, split = row_block / g.n_mt;
+  const int64_t n0 = (int64_t)(blockIdx.x - row_block * g.n_nt) * (8 * R);
+  const int64_t m0 = (int64_t)(row_block - split * g.n_mt) * (8 * TF);
   // Columns and tokens past the end read the last one's and are not stored.
   const char *wp[R], *xp[TF], *bp[R], *tp[TF];
 #pragma unroll
@@ -818,7 +822,7 @@ __global__ __launch_bounds__(kFewWaves * 64, TF <= 2 ? 2 : 1) void matmul_few_ro
   }
 #pragma unroll
   for (int t = 0; t < TF; ++t) {
-    const int64_t m = t * 8 + i8 < g.M ? t * 8 + i8 : g.M - 1;
+    const int64_t m = m0 + t * 8 + i8 < g.M ? m0 + t * 8 + i8 : g.M - 1;
     xp[t] = static_cast<const char*>(g.a) + m * g.lda * ESZ;
     tp[t] = static_cast<const char*>(g.a2) + m * g.lda2 * ESZ;
   }
@@ -845,7 +849,7 @@ __global__ __launch_bounds__(kFewWaves * 64, TF <= 2 ? 2 : 1) void matmul_few_ro
   __syncthreads();
   for (int i = threadIdx.x; i < 64 * R * TF; i += kFewWaves * 64) {
     const int nl = i % (8 * R), ml = i / (8 * R);
-    const int64_t n = n0 + nl, m = ml;
+    const int64_t n = n0 + nl, m = m0 + ml;
     if (m >= g.M || n >= g.N) continue;
     const int at = ((nl / 8) * TF + ml / 8) * 256 + (16 * ((nl % 8) / 4) + ml % 8) * 4 + nl % 4;
     constexpr int kOther = (16 * 2 + 8) * 4;   // from sum (i, j) to sum (i + 8, j + 8)
@@ -1027,16 +1031,36 @@ int elem_size(int dtype) { return dtype == 1 ? 4 : (dtype == 3 ? 1 : 2); }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, bool few, int* cfg, int* splits) {
-  if (few && M <= 32) {
-    // One workgroup per 16 columns; the depth is split over workgroups too
-    // while they do not fill the chip and each wave keeps four steps.
-    *cfg = kFewRows;
-    const int64_t n = M <= 16 ? up(N, 16) / 16 : up(N, 32) / 32;
+// Workgroups of 16 x 16 of the few-rows kernel.
+int64_t few_blocks(int64_t M, int64_t N) { return up(M, 16) / 16 * (up(N, 16) / 16); }
+// 17 to 32 rows take 32 x 32 instead where 16 x 16 would need a second round,
+// so that w is read once (32 x 1001 x 1024 bf16: 5.1 us in 16 x 16, 8.6 in
+// 32 x 32; 48 x 4096 x 4096, two rounds and more: 27 against 22).
+bool few_wide(int64_t M, int64_t N) { return M > 16 && M <= 32 && few_blocks(M, N) > kCUs; }
+
+// `few`: the most stages that a workgroup of the few-rows kernel may take where
+// there are more than 32 rows, 0 where it cannot run. Rows off the 16-byte
+// grid are copied for the tiles and not here, where their loads cost more from
+// about 24 stages on (128 x 256 x 4093 fp16, 32 a workgroup: 17.2 us, 15.9 as
+// a tile).
+void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* cfg, int* splits) {
+  if (few > 0 && (M <= 32 || (stages >= 4 && few_blocks(M, N) <= kCUs))) {
+    // The depth is split over workgroups too while they do not fill the chip
+    // and each wave keeps four steps. More than 32 rows come here while one
+    // round of workgroups covers the result and none has more than `few` stages
+    // (64-row tile against this, us on the GPU: 64 x 256 x 256 fp32 9.6, 5.6;
+    // 256 x 256 x 1024 bf16 7.1, 4.8; 64 x 1001 x 4096 bf16 16.7, 12.4; but
+    // 64 x 4096 x 1024 bf16, four rounds, 7.2, 11.6). Below four stages the
+    // two differ by 1 us or less, which the host's share of the call hides.
+    const int64_t n = few_wide(M, N) ? up(N, 32) / 32 : few_blocks(M, N);
     int64_t s = n >= kCUs || n < 1 ? 1 : kCUs / n;
     if (s > stages / 16) s = stages / 16;
-    *splits = (int)(s < 1 ? 1 : s);
-    return;
+    if (s < 1) s = 1;
+    if (M <= 32 || stages <= few * s) {
+      *cfg = kFewRows;
+      *splits = (int)s;
+      return;
+    }
   }
   // The tile and the split that a model of the time puts first, in cycles. A
   // compute unit holds one workgroup of a 256-row tile or two of the others; a
@@ -1092,9 +1116,10 @@ hipError_t launch_join(const GemmArgs& g, hipStream_t st) {
 template <typename T, typename O, int R, int TF>
 hipError_t launch_few_rows(GemmArgs g, hipStream_t st) {
   g.n_nt = (int)((g.N + 8 * R - 1) / (8 * R));
+  g.n_mt = (int)((g.M + 8 * TF - 1) / (8 * TF));
   // (at most 128 registers, two workgroups a compute unit, where TF <= 2)
   constexpr int BATCH = (TF == 1 ? 4 : 2) / (Op<T>::esz == 1 ? 2 : 1);
-  hipLaunchKernelGGL((matmul_few_rows_kernel<T, O, R, TF, BATCH>), dim3((unsigned)(g.n_nt * g.splits)),
+  hipLaunchKernelGGL((matmul_few_rows_kernel<T, O, R, TF, BATCH>), dim3((unsigned)((int64_t)g.n_nt * g.n_mt * g.splits)),
                      dim3(kFewWaves * 64), 0, st, g);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
@@ -1127,7 +1152,7 @@ template <typename T, typename O>
 hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
   if (cfg == kFewRows)
     return g.M <= 8 ? launch_few_rows<T, O, 2, 1>(g, st)
-                    : (g.M <= 16 ? launch_few_rows<T, O, 2, 2>(g, st) : launch_few_rows<T, O, 4, 4>(g, st));
+                    : (few_wide(g.M, g.N) ? launch_few_rows<T, O, 4, 4>(g, st) : launch_few_rows<T, O, 2, 2>(g, st));
   split_stages(g, 128 / Op<T>::esz);
   hipError_t e = hipErrorInvalidValue;
   if (g.K2 > 0) {
@@ -1197,7 +1222,7 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   MatmulPlan p{};
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
-  choose_tile(M, N, up(K, KT) / KT, dtype, true, &p.cfg, &p.splits);
+  choose_tile(M, N, up(K, KT) / KT, dtype, K % epc == 0 ? 64 : 24, &p.cfg, &p.splits);
   auto operand = [&](int64_t rows, int64_t depth, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
     *pack = p.cfg != kFewRows && depth > 0 && (depth % epc != 0 || !(al & bit));
@@ -1264,11 +1289,11 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.off_xt = take(!need_dw ? 0 : (p.copy ? (size_t)(M * p.ldk) * esz : (p.direct ? 0 : (size_t)(K * p.ldm) * esz)));
   size_t part = 0;
   if (need_dx) {
-    choose_tile(M, K, up(N, KT) / KT, dtype, !p.direct, &p.cfg_dx, &p.splits_dx);
+    choose_tile(M, K, up(N, KT) / KT, dtype, p.direct ? 0 : 64, &p.cfg_dx, &p.splits_dx);
     if (p.splits_dx > 1) part = (size_t)(p.splits_dx * M * K) * 4;
   }
   if (need_dw) {
-    choose_tile(N, K, up(M, KT) / KT, dtype, !p.direct, &p.cfg_dw, &p.splits_dw);
+    choose_tile(N, K, up(M, KT) / KT, dtype, p.direct ? 0 : 64, &p.cfg_dw, &p.splits_dw);
     const size_t q = p.splits_dw > 1 ? (size_t)(p.splits_dw * N * K) * 4 : 0;
     part = q > part ? q : part;
   }

@@ -423,7 +423,7 @@ dora_status dora_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int64_t 
 /*
  * The plan dora_matmul would use, for diagnostics and tests: info[0 ..
  * n_info-1] are, in order, the rows of its tile (256, 128 or 64; 0: the
- * kernel for few rows; -1: nothing to do), the parts the depth is split into
+ * kernel for few rows and small products; -1: nothing to do), the parts the depth is split into
  * (more than one are added by a second launch), a bit for each operand that
  * is copied first (as in dora_matmul_workspace_size), and the workspace
  * bytes; further entries are -1. Host only.

@@ -113,6 +113,18 @@ def test_few_rows(M, N, K, r, dtype):
     check(o, rng, dtype, "bf16" if dtype == "e4m3" else dtype, ACTS[N % 5], True, True)
 
 
+# More than 32 rows: a workgroup for each 16 x 16 of the result, the depth in
+# one part or several.
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32", "e4m3"])
+@pytest.mark.parametrize("M,N,K,r", [(33, 130, 1037, 9), (64, 256, 520, 8), (250, 255, 520, 0), (49, 17, 8200, 16),
+                                     (4001, 9, 1024, 0)])
+def test_small_products_of_many_rows(M, N, K, r, dtype):
+    r = 0 if dtype == "e4m3" else r
+    assert bnd.dora_matmul_plan_info(M, N, K, r, dtype)["tile_rows"] == 0
+    o, rng = operands(M, N, K, r, dtype, M + N + K)
+    check(o, rng, dtype, "bf16" if dtype == "e4m3" else dtype, ACTS[N % 5], True, True)
+
+
 # One shape for each kernel and what may come with it: (M, N, K, r, tile rows, split depth).
 COVER = [(4100, 4104, 264, 0, 256, False), (4100, 4104, 264, 40, 256, False), (1030, 4104, 2056, 0, 128, None),
          (1030, 4104, 520, 24, 128, None), (70, 520, 4104, 16, 64, True), (300, 520, 264, 16, 64, False),
