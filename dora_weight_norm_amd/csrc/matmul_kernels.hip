@@ -8,10 +8,10 @@
 // first, which are then multiplied by s, so that the adapter costs r more
 // columns of depth and no pass over memory.
 //
-// Measured (MI355X, one box): 8192 x 8192 x 8192 with r = 384 in bf16 887 us,
-// 1.30 PFLOP/s (the vendor's product alone, without r, 679 us); 8192 x 28672 x
-// 8192 in e4m3 1.45 ms, 2.66 PFLOP/s (1.18 ms); 4096^3 110 us (88 us); one
-// token at 8192 x 8192 25 us, 5.6 TB/s (28 us); the backward at 4096^3 251 us,
+// Measured (MI355X, one box): 8192 x 8192 x 8192 with r = 384 in bf16 879 us,
+// 1.31 PFLOP/s (the vendor's product alone, without r, 679 us); 8192 x 28672 x
+// 8192 in e4m3 1.44 ms, 2.67 PFLOP/s (1.18 ms); 4096^3 110 us (88 us); one
+// token at 8192 x 8192 25 us, 5.6 TB/s (28 us); the backward at 4096^3 252 us,
 // 1.09 PFLOP/s (its two products alone 214 us). On random operands the matrix
 // cores sustain 1.73 PFLOP/s in bf16.
 #include "dora_device.h"
