@@ -1313,7 +1313,9 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   // (and into the caller's array beside it).
   char* d = p.du_direct ? static_cast<char*>(du) : ws + p.off_du;
   void* du2 = p.du_direct ? nullptr : du;
-  float* sums = (dbias || dcol) ? reinterpret_cast<float*>(ws + p.off_sum) : nullptr;
+  // (without rows the workspace may be null: whether sums are wanted is not read off their address)
+  const bool want_sums = dbias || dcol;
+  float* sums = want_sums ? reinterpret_cast<float*>(ws + p.off_sum) : nullptr;
   if (M > 0 && N > 0) {
     const int64_t strips = (N + 7) / 8;
     int64_t tx = up(strips, 64);
@@ -1333,7 +1335,7 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (sums && N > 0) {
+  if (want_sums && N > 0) {
     e = launch_column_sum(sums, M > 0 ? (int)p.rows : 0, 2 * N, dbias, N, dcol, st);
     if (e != hipSuccess) return e;
   }

@@ -136,3 +136,18 @@ def test_block_refuses_mixed_types():
         block.adapted_linear(x, p.up, p.up.m)
     with pytest.raises((ValueError, TypeError)):
         bnd.dora_rms_norm(x, p.norm_weight, 1e-6, residual=draw(rng, (8, 64), "bf16"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_empty_batch_has_zero_gradients(dtype):
+    p, rng = make(dtype, 64, 96, 8)
+    x, dout = draw(rng, (0, 64), dtype), draw(rng, (0, 64), dtype)
+    out, saved = block.forward(x, x.clone(), p)
+    assert out.shape == (0, 64)
+    stale = [torch.full((n,), float("nan"), device="cuda") for n in (64, 64, 96, 96, 768, 768) * 4]
+    del stale
+    g = block.backward(dout, saved, p)
+    assert g["x"].shape == (0, 64) and (g["norm_weight"] == 0).all()
+    for side in ("up", "down"):
+        for k in ("A", "B", "m", "bias"):
+            assert (g[side][k] == 0).all(), (side, k)

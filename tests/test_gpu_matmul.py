@@ -343,3 +343,20 @@ def test_refusals_of_the_binding():
         bnd.dora_matmul_backward(x, x, None, w)
     with pytest.raises(bnd.DoraError):
         bnd.dora_matmul(x, w, s=float("inf"))
+
+
+@pytest.mark.parametrize("needs", [(True, True), (True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_backward_without_rows_writes_its_sums(dtype, needs):
+    dt = TORCH_DT[dtype]
+
+    def z(*shape):
+        return torch.empty(*shape, dtype=dt, device="cuda")
+
+    # the blocks that the outputs will be made of hold NaN
+    stale = [torch.full((n,), float("nan"), device="cuda") for n in (8, 8, 8, 8, 128, 128)]
+    del stale
+    dx, dw, db, dc, du = bnd.dora_matmul_backward(z(0, 8), z(0, 8), z(0, 16), z(8, 16).zero_(), need_dx=needs[0],
+                                                  need_dw=needs[1])
+    assert du.shape == (0, 8) and (dx is None or dx.shape == (0, 16))
+    assert (db == 0).all() and (dc == 0).all() and (dw is None or (dw == 0).all())
