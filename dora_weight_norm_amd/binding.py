@@ -127,6 +127,8 @@ def load():
         "dora_matmul_backward_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, ctypes.POINTER(_c_sz)]),
         "dora_matmul_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i, _c_p,
                                         _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+        "dora_matmul_backward_rows": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p,
+                                             _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -647,7 +649,8 @@ def dora_matmul(x, w, row_scale=None, col_scale=None, t=None, b=None, s: float =
     residual [M, N] of the output's dtype. out_dtype is x's, and for float8
     one of the other three (default bfloat16). act: none, relu, gelu,
     gelu_tanh or silu. Returns (y, u); u, the product that the backward
-    takes, is None unless `save` (or a buffer for it) is given.
+    takes, is None unless `save` (or a buffer for it) is given. A row_scale
+    that the product had goes to the backward too.
     """
     dev, dtype = _first(x, "x"), x.dtype
     e8 = dtype is _E4M3
@@ -694,13 +697,15 @@ GRAD_DX, GRAD_DW, GRAD_SUMS, GRAD_DU, GRAD_ALIGNED = 1, 2, 4, 8, 16   # DORA_GRA
 
 def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "none", need_dx: bool = True,
                          need_dw: bool = True, need_dbias: bool = True, need_dcol_scale: bool = True,
-                         workspace=None, stream=None):
-    """Gradients of dora_matmul from its u (bfloat16, float16 or float32).
+                         workspace=None, stream=None, row_scale=None):
+    """Gradients of dora_matmul from its u (bfloat16, float16 or float32),
+    with the row_scale, col_scale, bias and act that it had.
 
     Returns (dx, dw, dbias, dcol_scale, du): dx [M, K], dw [N, K], dbias and
     dcol_scale float32 [N] (each None if not needed), and du [M, N], the
-    gradient of u. x is read for dw and w for dx; either may be None where
-    its product is not needed, but not both. The residual's gradient is dy.
+    gradient of x w^T + s * t b^T (of u, where there is no row_scale). x is
+    read for dw and w for dx; either may be None where its product is not
+    needed. The residual's gradient is dy; row_scale's is not computed.
     """
     dev, dtype = _first(dy, "dy"), dy.dtype
     code = _type_code(dtype)
@@ -719,6 +724,7 @@ def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "non
         _want(w, "w", (N, K), dtype, dev)
     f32 = torch.float32
     pcol, pbias = _maybe(col_scale, "col_scale", (N,), f32, dev), _maybe(bias, "bias", (N,), f32, dev)
+    prow = _maybe(row_scale, "row_scale", (M,), f32, dev)
     act_code = _act(act)
     du = _new(stream, out, dtype, dev)
     dx = _new(stream, (M, K), dtype, dev) if need_dx else None
@@ -730,7 +736,7 @@ def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "non
                + GRAD_ALIGNED * ((not need_dw or x.data_ptr() % 16 == 0) and (not need_dx or w.data_ptr() % 16 == 0)))
     need = _size_of("dora_matmul_backward_workspace_size", M, N, K, code, outputs)
     workspace = _space(workspace, need, stream, dev)
-    _call("dora_matmul_backward", dy.data_ptr(), pu, _addr(x) if need_dw else None, _addr(w) if need_dx else None,
-          code, M, N, K, pcol, pbias, act_code, _addr(du), _addr(dx), _addr(dw), _addr(dbias), _addr(dcol),
-          _addr(workspace), need, _raw_stream(stream, dev))
+    _call("dora_matmul_backward_rows", dy.data_ptr(), pu, _addr(x) if need_dw else None,
+          _addr(w) if need_dx else None, code, M, N, K, prow, pcol, pbias, act_code, _addr(du), _addr(dx), _addr(dw),
+          _addr(dbias), _addr(dcol), _addr(workspace), need, _raw_stream(stream, dev))
     return dx, dw, dbias, dcol, du

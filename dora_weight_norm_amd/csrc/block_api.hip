@@ -186,6 +186,14 @@ dora_status dora_matmul_backward(const void* dy, const void* u, const void* x, c
                                  int64_t N, int64_t K, const float* col_scale, const float* bias, int act, void* du,
                                  void* dx, void* dw, float* dbias, float* dcol_scale, void* workspace,
                                  size_t workspace_bytes, void* stream) {
+  return dora_matmul_backward_rows(dy, u, x, w, dtype, M, N, K, nullptr, col_scale, bias, act, du, dx, dw, dbias,
+                                   dcol_scale, workspace, workspace_bytes, stream);
+}
+
+dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void* x, const void* w, int dtype,
+                                      int64_t M, int64_t N, int64_t K, const float* row_scale, const float* col_scale,
+                                      const float* bias, int act, void* du, void* dx, void* dw, float* dbias,
+                                      float* dcol_scale, void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_dtype(dtype)) return DORA_ERR_UNSUPPORTED_DTYPE;
   const int64_t es = esize(dtype);
   if (!matmul_sizes_ok(M, N, K, 0, es) || !matmul_sizes_ok(K, K, M, N, es) || !valid_act(act))
@@ -196,19 +204,19 @@ dora_status dora_matmul_backward(const void* dy, const void* u, const void* x, c
   if (dw != nullptr && M * K > 0 && x == nullptr) return DORA_ERR_INVALID_ARG;
   const size_t e = (size_t)es;
   const Span in[] = {{dy, M * N * es, e}, {u, M * N * es, e}, {dw ? x : nullptr, M * K * es, e},
-                     {dx ? w : nullptr, N * K * es, e}, {col_scale, N * 4, 4}, {bias, N * 4, 4}};
+                     {dx ? w : nullptr, N * K * es, e}, {col_scale, N * 4, 4}, {bias, N * 4, 4}, {row_scale, M * 4, 4}};
   const Span out[] = {{du, M * N * es, e}, {dx, M * K * es, e}, {dw, N * K * es, e}, {dbias, N * 4, 4},
                       {dcol_scale, N * 4, 4}};
   const unsigned same[] = {1u, 0u, 0u, 0u, 0u};   // du may be dy itself
-  if (!buffers_ok(in, 6, out, 5, same)) return DORA_ERR_INVALID_ARG;
+  if (!buffers_ok(in, 7, out, 5, same)) return DORA_ERR_INVALID_ARG;
   const dora::MatmulBackwardPlan p =
       dora::plan_matmul_backward(M, N, K, dtype, dx != nullptr, dw != nullptr, dbias != nullptr || dcol_scale != nullptr,
                                  du != nullptr && aligned(du, 16),
                                  (dw == nullptr || aligned(x, 16)) && (dx == nullptr || aligned(w, 16)));
-  const dora_status st = workspace_ok(workspace, workspace_bytes, p.ws_bytes, in, 6, out, 5);
+  const dora_status st = workspace_ok(workspace, workspace_bytes, p.ws_bytes, in, 7, out, 5);
   if (st != DORA_OK) return st;
-  return hip_status(dora::launch_matmul_backward(p, dy, u, x, w, dtype, M, N, K, col_scale, bias, act, du, dx, dw,
-                                                 dbias, dcol_scale, static_cast<char*>(workspace),
+  return hip_status(dora::launch_matmul_backward(p, dy, u, x, w, dtype, M, N, K, row_scale, col_scale, bias, act, du,
+                                                 dx, dw, dbias, dcol_scale, static_cast<char*>(workspace),
                                                  static_cast<hipStream_t>(stream)));
 }
 

@@ -72,8 +72,8 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
                          int64_t K, const void* t, const void* b, int64_t r, float s, const Epilogue& ep,
                          int out_dtype, char* ws, hipStream_t st);
 hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, const void* u, const void* x,
-                                  const void* w, int dtype, int64_t M, int64_t N, int64_t K, const float* col_scale,
-                                  const float* bias, int act, void* du, void* dx, void* dw, float* dbias,
-                                  float* dcol, char* ws, hipStream_t st);
+                                  const void* w, int dtype, int64_t M, int64_t N, int64_t K, const float* row_scale,
+                                  const float* col_scale, const float* bias, int act, void* du, void* dx, void* dw,
+                                  float* dbias, float* dcol, char* ws, hipStream_t st);
 
 }  // namespace dora

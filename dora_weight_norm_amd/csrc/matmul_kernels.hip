@@ -937,13 +937,14 @@ __global__ __launch_bounds__(256) void transpose_kernel(const U* src, int64_t ro
   }
 }
 
-// Element-wise part of the backward: z from u, dz = dy act'(z), du = col_scale
-// dz (rounded to the storage type: it is the products' operand), and this row
-// block's sums of dz and dz u over its rows, in increasing order.
+// Element-wise part of the backward: z from u, dz = dy act'(z), du = row_scale
+// col_scale dz (rounded to the storage type: it is the operand of both
+// products, which the matrix cores take in 16 bits), and this row block's sums
+// of dz and dz u over its rows, in increasing order (u holds the row scale).
 template <typename T>
-__global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u, const float* col_scale,
-                                                         const float* bias, int act, int64_t M, int64_t N, T* du,
-                                                         int64_t ldu, T* du2, float* sums) {
+__global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u, const float* row_scale,
+                                                         const float* col_scale, const float* bias, int act, int64_t M,
+                                                         int64_t N, T* du, int64_t ldu, T* du2, float* sums) {
   __shared__ float lanes[16][256];
   const int64_t strip = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t n = strip * 8;
@@ -974,6 +975,7 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
     for (int i = 0; i < U; ++i) {
       const int64_t m = m0 + i * step;
       if (m >= M) continue;
+      const float rs = row_scale ? row_scale[m] : 1.f;
       float y[8], v[8], o[8];
       unpack8<T>(ry[i], y);
       unpack8<T>(ru[i], v);
@@ -985,7 +987,7 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
         const float dz = y[e] * o[e];
         sb[e] += dz;
         sc[e] = fmaf(dz, v[e], sc[e]);
-        o[e] = cs[e] * dz;
+        o[e] = cs[e] * dz * rs;
       }
       if (du2) store8<T>(du2 + m * N + n, nv, o);
       // (a padded row's tail, up to the next strip of eight, is written as zeros)
@@ -1303,9 +1305,9 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
 }
 
 hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, const void* u, const void* x,
-                                  const void* w, int dtype, int64_t M, int64_t N, int64_t K, const float* col_scale,
-                                  const float* bias, int act, void* du, void* dx, void* dw, float* dbias,
-                                  float* dcol, char* ws, hipStream_t st) {
+                                  const void* w, int dtype, int64_t M, int64_t N, int64_t K, const float* row_scale,
+                                  const float* col_scale, const float* bias, int act, void* du, void* dx, void* dw,
+                                  float* dbias, float* dcol, char* ws, hipStream_t st) {
   const int esz = elem_size(dtype);
   hipError_t e = hipSuccess;
   // The element-wise pass writes du into the caller's array where that can be
@@ -1324,8 +1326,8 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     const dim3 grid((unsigned)((strips + tx - 1) / tx), (unsigned)p.rows);
 #define DORA_BWD(T)                                                                                             \
   hipLaunchKernelGGL((matmul_bwd_kernel<T>), grid, block, 0, st, static_cast<const T*>(dy),                     \
-                     static_cast<const T*>(u), col_scale, bias, act, M, N, reinterpret_cast<T*>(d), p.ldn,         \
-                     static_cast<T*>(du2), sums)
+                     static_cast<const T*>(u), row_scale, col_scale, bias, act, M, N, reinterpret_cast<T*>(d),  \
+                     p.ldn, static_cast<T*>(du2), sums)
     switch (dtype) {
       case 0: DORA_BWD(bf16_t); break;
       case 2: DORA_BWD(f16_t); break;

@@ -476,8 +476,8 @@ dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K,
                                                 size_t* ws_bytes);
 
 /*
- * Backward of the product (bf16, fp16 or fp32), from the u of the forward;
- * the residual's gradient is dy itself:
+ * Backward of a product without row_scale (bf16, fp16 or fp32), from the u of
+ * the forward; the residual's gradient is dy itself:
  *
  *   z = col_scale[n] * u + bias[n]     dz = dy * act'(z)
  *   dbias[n] = sum_m dz                dcol_scale[n] = sum_m dz * u
@@ -495,6 +495,22 @@ dora_status dora_matmul_backward(const void* dy, const void* u, const void* x, c
                                  int64_t N, int64_t K, const float* col_scale, const float* bias, int act, void* du,
                                  void* dx, void* dw, float* dbias, float* dcol_scale, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/*
+ * The same of a product with row_scale, fp32 [M] or NULL. u holds it, so z,
+ * dz, dbias and dcol_scale are as above, and du is the gradient of the sum
+ * that the row scale multiplies:
+ *
+ *   du = row_scale[m] * col_scale[n] * dz, rounded to the storage type
+ *   dx = du w                          dw = du^T x
+ *
+ * The pair's gradients follow from this du by dora_matmul_backward, as above.
+ * row_scale itself has no gradient here. Same workspace and errors.
+ */
+dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void* x, const void* w, int dtype,
+                                      int64_t M, int64_t N, int64_t K, const float* row_scale, const float* col_scale,
+                                      const float* bias, int act, void* du, void* dx, void* dw, float* dbias,
+                                      float* dcol_scale, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -152,3 +152,15 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         bnd.dora_matmul_backward(x, x, x, x)
     with pytest.raises(TypeError):
         bnd.dora_matmul_workspace_size(4, 4, 4, 0, torch.int8)
+
+
+def test_matmul_backward_refuses_a_bad_row_scale():
+    def call(row_scale, du=None, ws=0x8000000):
+        return bnd.load().dora_matmul_backward_rows(P(0x1000000), P(0x2000000), P(0x3000000), P(0x4000000), 0, 4, 32, 64,
+                                                    P(row_scale), None, None, 0, P(du), P(0x5000000), P(0x6000000),
+                                                    None, None, P(ws), 1 << 24, None)
+
+    assert call(0x9000002) == 1
+    assert call(0x5000000) == 1 and call(0x6000004) == 1 and call(0x7000000, du=0x7000000) == 1
+    assert call(0x8000010) == 1                                 # in the workspace
+    assert call(0x9000000, ws=None) == 4

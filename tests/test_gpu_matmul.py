@@ -360,3 +360,48 @@ def test_backward_without_rows_writes_its_sums(dtype, needs):
                                                   need_dw=needs[1])
     assert du.shape == (0, 8) and (dx is None or dx.shape == (0, 16))
     assert (db == 0).all() and (dc == 0).all() and (dw is None or (dw == 0).all())
+
+
+@pytest.mark.parametrize("dtype,M,N,K", [("f32", 12, 20, 24), ("bf16", 70, 136, 200), ("bf16", 33, 77, 129),
+                                         ("f16", 300, 264, 72)])
+def test_backward_with_a_row_scale(dtype, M, N, K):
+    rng = np.random.default_rng(21)
+    x, w, dy = draw(rng, (M, K), dtype), draw(rng, (N, K), dtype, K ** -0.5), draw(rng, (M, N), dtype)
+    rows, c, bias = vec(rng, M, 0.4), vec(rng, N, 0.2), vec(rng, N, 0.3, 0.0)
+    _, u = bnd.dora_matmul(x, w, row_scale=rows, col_scale=c, bias=bias, act="silu", save=True)
+    got = bnd.dora_matmul_backward(dy, u, x, w, row_scale=rows, col_scale=c, bias=bias, act="silu")
+    plain = bnd.dora_matmul_backward(dy, u, x, w, col_scale=c, bias=bias, act="silu")
+    assert torch.equal(got[2], plain[2]) and torch.equal(got[3], plain[3])
+
+    H = [host(v) for v in (dy, u, x, w, c, bias)]
+    _, _, _, _, du = B.matmul_backward(*H, "silu")
+    du = du * host(rows)[:, None]
+    z = B.preactivation(H[1], H[4], H[5])
+    edz = np.abs(H[0]) * EPS32 * (4 * np.abs(z) + 16 * (1 + np.abs(z)) + 2)
+    tol = rounded(dtype, du, np.abs(host(rows))[:, None] * np.abs(H[4])[None] * edz + 2 * EPS32 * np.abs(du))
+    close(got[4], du, tol, "du")
+    dx, dw = du @ H[3], du.T @ H[2]
+    close(got[0], dx, rounded(dtype, dx, (N + 4) * EPS32 * (np.abs(du) @ np.abs(H[3])) + tol @ np.abs(H[3])), "dx")
+    close(got[1], dw, rounded(dtype, dw, (M + 4) * EPS32 * (np.abs(du).T @ np.abs(H[2])) + tol.T @ np.abs(H[2])), "dw")
+
+
+def test_row_scaled_gradients_against_differences():
+    """As test_gradients_against_differences, of a product whose rows are scaled."""
+    rng = np.random.default_rng(22)
+    M, N, K, r, s = 12, 20, 24, 8, 0.5
+    x, w, t, b = (draw(rng, sh, "f32", 0.5) for sh in ((M, K), (N, K), (M, r), (N, r)))
+    rows, c, bias, dy = vec(rng, M, 0.5), vec(rng, N), vec(rng, N, 0.3, 0.0), draw(rng, (M, N), "f32")
+    kw = dict(row_scale=rows, col_scale=c, bias=bias, act="gelu")
+    _, u = bnd.dora_matmul(x, w, t=t, b=b, s=s, save=True, **kw)
+    dx, dw, db, dc, du = bnd.dora_matmul_backward(dy, u, x, w, **kw)
+    dt, dB, _, _, _ = bnd.dora_matmul_backward(du, du, t, b, need_dbias=False, need_dcol_scale=False)
+    vals = dict(x=host(x), w=host(w), col_scale=host(c), bias=host(bias), t=host(t), b=host(b))
+    grads = dict(x=host(dx), w=host(dw), col_scale=host(dc), bias=host(db), t=s * host(dt), b=s * host(dB))
+
+    def loss(**over):
+        return (B.matmul(**{**vals, **over}, row_scale=host(rows), s=s, name="gelu")[0] * host(dy)).sum()
+
+    for k, g in grads.items():
+        d, e = rng.standard_normal(g.shape), 1e-5
+        num = (loss(**{k: vals[k] + e * d}) - loss(**{k: vals[k] - e * d})) / (2 * e)
+        assert abs((g * d).sum() - num) <= 1e-4 * np.linalg.norm(g) * np.linalg.norm(d), k
