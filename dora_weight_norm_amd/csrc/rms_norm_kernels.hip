@@ -169,6 +169,22 @@ __device__ __forceinline__ float scale_of(uint32_t top_bits) {
   return top_bits == 0 ? 1.f : (s < kMinScale ? kMinScale : s);
 }
 
+// The quotient n / scale, correctly rounded in fp32 without a division a value:
+// n times the rounded reciprocal is within a step of it, and adding the exact
+// remainder times the reciprocal gives the nearest value (Markstein 1990). The
+// product alone put values beside the border of two 8-bit steps on the wrong
+// side of it; the two operations more cost 0.7 us of 78 at 8192 x 8192. An
+// infinite scale leaves 0 (NaN where n is infinite), as the division does.
+struct RowQuotient {
+  float inv, s;
+  __device__ __forceinline__ explicit RowQuotient(float scale)
+      : inv(1.f / scale), s(scale <= 3.402823466e38f ? scale : 0.f) {}
+  __device__ __forceinline__ float operator()(float n) const {
+    const float q = n * inv;
+    return fmaf(fmaf(-q, s, n), inv, q);
+  }
+};
+
 struct NormArgs {
   const void* x;
   const void* residual;
@@ -254,13 +270,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
     }
     if (a.q) {   // uniform over the grid
       top = row_max_bits<NT>(top, reinterpret_cast<uint32_t*>(red[par]) + (NT > 64 ? NT / 64 : 0));
-      const float s = scale_of(top), inv = 1.f / s;
+      const float s = scale_of(top);
+      const RowQuotient quotient(s);
       if (lane == 0) a.scale[t] = s;
       uint8_t* qr = a.q + t * a.d;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[c][e] *= inv;
+        for (int e = 0; e < E; ++e) f[c][e] = quotient(f[c][e]);
         store_row_q<E, STREAM>(qr, (int64_t)(c * NT + lane) * E, a.d, f[c]);
       }
     }
@@ -297,7 +314,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs a) {
     q = row_sum<NT>(q, red[par]);
     const float rs = 1.f / sqrtf(q / (float)a.d + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rs;
-    float inv = 0.f;
+    float s = 1.f;
     if (a.q) {
       uint32_t top = 0;
       for (int64_t k = (int64_t)threadIdx.x * E; k < a.d; k += NT * E) {
@@ -311,10 +328,10 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs a) {
         }
       }
       top = row_max_bits<NT>(top, reinterpret_cast<uint32_t*>(red[par]) + NT / 64);
-      const float s = scale_of(top);
-      inv = 1.f / s;
+      s = scale_of(top);
       if (threadIdx.x == 0) a.scale[t] = s;
     }
+    const RowQuotient quotient(s);
     for (int64_t k = (int64_t)threadIdx.x * E; k < a.d; k += NT * E) {
       float f[E], w[E];
       load(k, f);
@@ -325,7 +342,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs a) {
       if (a.y) store_row_chunk<T>(static_cast<T*>(a.y) + t * a.d, k, a.d, f);
       if (a.q) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] *= inv;
+        for (int e = 0; e < E; ++e) f[e] = quotient(f[e]);
         store_row_q<E>(a.q + t * a.d, k, a.d, f);
       }
     }

@@ -358,7 +358,7 @@ dora_status dora_compose_backward(const void* dy, const void* base, const void* 
  *   rstd[t] = 1 / sqrt(mean_j h[t,j]^2 + eps)
  *   n[t,j]  = h[t,j] * rstd[t] * weight[j]
  *   y = n in the storage type;  scale[t] = max_j |n[t,j]| / 448 and
- *   q = n / scale[t] in e4m3 (both round to nearest even)
+ *   q = n / scale[t] (the fp32 quotient) in e4m3 (both round to nearest even)
  *
  * x, residual, h, y: [T, d] of `dtype`; q: [T, d] bytes; weight: fp32 [d] or
  * NULL (ones); scale, rstd: fp32 [T]. residual NULL: h is x, and the h

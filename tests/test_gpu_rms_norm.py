@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_helpers import EPS32, close, draw, host, rounded, vec
+from block_helpers import EPS32, TORCH_DT, close, draw, host, rounded, vec
 from dora_weight_norm_amd import binding as bnd
 from oracle import block_oracle as B
 
@@ -198,3 +198,42 @@ def test_norm_refuses_wrong_buffers():
         bnd.dora_rms_norm(x, w, 0.0)
     with pytest.raises(bnd.DoraError):
         bnd.dora_rms_norm(x, w, EPS, y=x)
+
+
+@pytest.mark.parametrize("T,d", [(3, 700), (600, 640), (64, 8192), (2, 20000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_8_bit_rows_are_the_nearest_to_the_quotient(T, d, dtype):
+    """q is the fp32 quotient n / scale, rounded once: bit by bit, on values beside the borders of the 8-bit steps."""
+    rng = np.random.default_rng(T + d)
+    # borders between neighbouring e4m3 values (17, 19, .. 31 in units of a half step) at a few exponents, each off
+    # by an fp32 step or so
+    edge = (17 + 2 * rng.integers(0, 8, (T, d))) * 2.0 ** rng.integers(-3, 4, (T, d)) * rng.choice([-1, 1], (T, d))
+    edge[:, 0] = 448
+    row = np.exp(rng.uniform(-2, 2, (T, 1))) / 100
+    w = torch.from_numpy((1 + 0.3 * rng.random(d)).astype(np.float32)).cuda()
+    x = torch.from_numpy((edge * row / (1 if dtype != "f32" else host(w)[None])).astype(np.float32)).cuda()
+    x = x.to(TORCH_DT[dtype])
+    if dtype != "f32":
+        w = None
+    q, scale, h, rstd = bnd.dora_rms_norm_quant(x, w, 1e-6)
+    f = np.float32
+    n = x.float().cpu().numpy() * rstd.cpu().numpy()[:, None]
+    if w is not None:
+        n = n * w.cpu().numpy()[None]
+    assert n.dtype == f
+    assert np.array_equal(scale.cpu().numpy(), np.abs(n).max(1) / f(448))
+    want = torch.from_numpy(n / scale.cpu().numpy()[:, None]).to(torch.float8_e4m3fn)
+    off = (q.cpu().float() != want.float())
+    assert not off.any(), f"{off.sum()} of {off.numel()} values"
+
+
+def test_8_bit_rows_of_infinite_scale():
+    """n past fp32's range: its scale is infinite, the finite values are 0 and the infinite ones NaN."""
+    x = torch.ones(2, 600, device="cuda")
+    x[:, 7] = -2
+    w = torch.full((600,), 3.0e38, device="cuda")
+    w[100:] = 1
+    q, scale, _, _ = bnd.dora_rms_norm_quant(x, w, EPS)
+    v = host(q)
+    assert np.isinf(host(scale)).all()
+    assert np.isnan(v[:, 7]).all() and (np.delete(v, 7, 1) == 0).all()
