@@ -74,50 +74,64 @@ struct Op<e4m3_t> {
   }
 };
 
-// Activations (dora_act) and their slopes, fp32.
+// Activations (dora_act) and their slopes, in fp32 arithmetic. F32: the result
+// is stored in fp32, and the device library's exponential, error function and
+// division are used, whose errors are a step or two of it (2048^3 with GELU:
+// 144 us, 140 with the forms below). Results of 16 bits take the forms below,
+// whose errors relative to the result are far below half of their steps
+// (2^-11 in fp16) in the tails too.
 constexpr float kTanhK = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kTanhC = 0.044715f;
 
-// 1 / (1 + e^-v) by the hardware's exponential of base two and reciprocal (one
-// unit in the last place each; the product with log2(e) adds |v| 2^-24
-// relative): a correctly rounded division and expf cost the epilogue of the
-// 8192 x 28672 product about as much again as its stores.
+// 1 / (1 + e^-v). 16 bits: by the hardware's exponential of base two and
+// reciprocal (one unit in the last place each; the product with log2(e) adds
+// |v| 2^-23 relative): a correctly rounded division and expf cost the epilogue
+// of the 8192 x 28672 product about as much again as its stores.
+template <bool F32>
 __device__ __forceinline__ float logistic(float v) {
+  if constexpr (F32) return 1.f / (1.f + expf(-v));
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896f * v));
 }
 
-// Phi(z) = (1 + erf(z / sqrt 2)) / 2 by Abramowitz and Stegun 7.1.26: with t =
-// 1 / (1 + p x), erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2) within 1.5e-7, an
-// absolute error below fp32's own at 1; a third of erff's instructions.
+// Phi(z) = erfc(-z / sqrt 2) / 2. 16 bits: with x = |z| / sqrt 2 and t = 1 / (1 +
+// p x), erfc(x) = (a1 t + ... + a8 t^8) e^(-x^2), a fit of e^(x^2) erfc(x) in
+// the relative error, at most 1.1e-7 for x up to 11 (found by weighted least
+// squares); with fp32's roundings (16 + 2 z^2) 2^-24 of Phi, a few steps of
+// fp32 where the tail matters. Results below 2^-126 may be 0.
+template <bool F32>
 __device__ __forceinline__ float normal_cdf(float z) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  const float h = 0.5f * (q * t) * __builtin_amdgcn_exp2f(-1.44269504088896f * (x * x));   // erfc(x) / 2
+  if constexpr (F32) return 0.5f * erfcf(z * -0.70710678118654752f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.332f * 0.70710678118654752f, fabsf(z), 1.f));
+  float q = fmaf(t, -0.129304167f, 0.42600419f);
+  q = fmaf(t, q, -0.29990073f);
+  q = fmaf(t, q, 0.366505857f);
+  q = fmaf(t, q, 0.067685469f);
+  q = fmaf(t, q, 0.196667373f);
+  q = fmaf(t, q, 0.184907024f);
+  q = fmaf(t, q, 0.187434877f);
+  const float h = 0.5f * (q * t) * __builtin_amdgcn_exp2f(-0.72134752044448f * (z * z));   // erfc(x) / 2
   return z < 0.f ? h : 1.f - h;
 }
 
+template <bool F32>
 __device__ __forceinline__ float act1(float z, int act) {
   switch (act) {
     case 1: return z < 0.f ? 0.f : z;
-    case 2: return z * normal_cdf(z);
+    case 2: return z * normal_cdf<F32>(z);
     // z / 2 (1 + tanh(v)) = z / (1 + exp(-2 v))
-    case 3: return z * logistic(z * fmaf(2.f * kTanhK * kTanhC, z * z, 2.f * kTanhK));
-    case 4: return z * logistic(z);
+    case 3: return z * logistic<F32>(z * fmaf(2.f * kTanhK * kTanhC, z * z, 2.f * kTanhK));
+    case 4: return z * logistic<F32>(z);
     default: return z;
   }
 }
 
 // N values at once, so that the (uniform) choice is made once.
-template <int N>
+template <int N, bool F32>
 __device__ __forceinline__ void act_all(float (&z)[N], int act) {
   switch (act) {
-#define DORA_ACT(A)                                      \
-  case A:                                                \
-    for (int e = 0; e < N; ++e) z[e] = act1(z[e], A);    \
+#define DORA_ACT(A)                                           \
+  case A:                                                     \
+    for (int e = 0; e < N; ++e) z[e] = act1<F32>(z[e], A);    \
     break;
     DORA_ACT(1)
     DORA_ACT(2)
@@ -128,16 +142,20 @@ __device__ __forceinline__ void act_all(float (&z)[N], int act) {
   }
 }
 
+template <bool F32>
 __device__ __forceinline__ float slope_of(float z, int act) {
   switch (act) {
     case 1: return z > 0.f ? 1.f : (z != z ? z : 0.f);
-    case 2: return normal_cdf(z) + z * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.72134752044448f * (z * z));
+    case 2: {
+      const float e = -0.72134752044448f * (z * z);   // e^(-z^2 / 2) = 2^e
+      return normal_cdf<F32>(z) + z * 0.3989422804014327f * (F32 ? exp2f(e) : __builtin_amdgcn_exp2f(e));
+    }
     case 3: {
-      const float p = logistic(z * fmaf(2.f * kTanhK * kTanhC, z * z, 2.f * kTanhK));
+      const float p = logistic<F32>(z * fmaf(2.f * kTanhK * kTanhC, z * z, 2.f * kTanhK));
       return p + z * p * (1.f - p) * 2.f * kTanhK * fmaf(3.f * kTanhC * z, z, 1.f);
     }
     case 4: {
-      const float p = logistic(z);
+      const float p = logistic<F32>(z);
       return p * (1.f + z * (1.f - p));
     }
     default: return 1.f;
@@ -145,12 +163,12 @@ __device__ __forceinline__ float slope_of(float z, int act) {
 }
 
 // z to the activation's slope there, N values at once.
-template <int N>
+template <int N, bool F32>
 __device__ __forceinline__ void slope_all(float (&z)[N], int act) {
   switch (act) {
-#define DORA_SLOPE(A)                                    \
-  case A:                                                \
-    for (int e = 0; e < N; ++e) z[e] = slope_of(z[e], A); \
+#define DORA_SLOPE(A)                                           \
+  case A:                                                       \
+    for (int e = 0; e < N; ++e) z[e] = slope_of<F32>(z[e], A);  \
     break;
     DORA_SLOPE(0)
     DORA_SLOPE(1)
@@ -252,7 +270,7 @@ __device__ __forceinline__ void epilogue_rows(const Epilogue& ep, float (&v)[8 *
   if (ep.u) put(ep.u);
 #pragma unroll
   for (int e = 0; e < 8 * R; ++e) v[e] = fmaf(cs[e % 8], v[e], bs[e % 8]);
-  act_all<8 * R>(v, ep.act);
+  act_all<8 * R, std::is_same<O, float>::value>(v, ep.act);
   if (ep.residual) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -270,7 +288,7 @@ template <typename O>
 __device__ __forceinline__ void epilogue1(const Epilogue& ep, float v, float cs, float bs, int64_t m, int64_t off) {
   if (ep.row_scale) v *= ep.row_scale[m];
   if (ep.u) static_cast<O*>(ep.u)[off] = from_f32<O>(v);
-  v = act1(fmaf(cs, v, bs), ep.act);
+  v = act1<std::is_same<O, float>::value>(fmaf(cs, v, bs), ep.act);
   if (ep.residual) v += to_f32(static_cast<const O*>(ep.residual)[off]);
   static_cast<O*>(ep.y)[off] = from_f32<O>(v);
 }
@@ -981,7 +999,7 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
       unpack8<T>(ru[i], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = fmaf(cs[e], v[e], bs[e]);
-      slope_all<8>(o, act);
+      slope_all<8, std::is_same<T, float>::value>(o, act);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float dz = y[e] * o[e];

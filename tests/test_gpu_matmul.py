@@ -14,6 +14,7 @@ half a step of each of their terms.
 import numpy as np
 import pytest
 import torch
+from scipy.special import expit, ndtr
 
 from block_helpers import EPS32, HALF, TINY, TORCH_DT, close, draw, host, rounded, vec
 from dora_weight_norm_amd import binding as bnd
@@ -405,3 +406,61 @@ def test_row_scaled_gradients_against_differences():
         d, e = rng.standard_normal(g.shape), 1e-5
         num = (loss(**{k: vals[k] + e * d}) - loss(**{k: vals[k] - e * d})) / (2 * e)
         assert abs((g * d).sum() - num) <= 1e-4 * np.linalg.norm(g) * np.linalg.norm(d), k
+
+
+# The tails too: each output relative to its own value, with no product and no residual to hide it. An 8-term
+# polynomial (2 half steps of fp32), its Horner steps, reciprocal, exponential and products make 16 of them, and
+# the exponent's three roundings 1.5 z^2; the logistic forms have 8 and twice or four times the exponent's size.
+# Below 2^-126 the factor may be 0, which |z| < 16 multiplies.
+def value_err(z, name):
+    v = np.abs(z)
+    if name == "gelu":
+        n = 16 + 2 * v * v
+    elif name == "gelu_tanh":
+        n = 8 + 4 * 2 * np.sqrt(2 / np.pi) * (v + 0.044715 * v ** 3)
+    else:
+        n = 8 + 2 * v if name == "silu" else 0 * v
+    return np.abs(exact_act(z, name)) * n * EPS32 + 2.0 ** -122
+
+
+def exact_act(z, name):
+    if name == "gelu":
+        return z * ndtr(z)
+    if name == "gelu_tanh":
+        return z * expit(2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3))
+    return z * expit(z) if name == "silu" else B.act(z, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("M", [1, 40])
+def test_activations_relative_to_their_value(M, name, dtype):
+    z = torch.linspace(-12.5, 12.5, 4001).cuda()
+    x = torch.empty(M, 0, device="cuda", dtype=TORCH_DT[dtype])
+    w = torch.empty(4001, 0, device="cuda", dtype=TORCH_DT[dtype])
+    y, _ = bnd.dora_matmul(x, w, bias=z, act=name)
+    zz = np.broadcast_to(host(z)[None], (M, 4001))
+    close(y, exact_act(zz, name), rounded(dtype, exact_act(zz, name), value_err(zz, name)), name)
+
+
+@pytest.mark.parametrize("name", ACTS)
+def test_slopes_relative_to_their_terms(name):
+    z = torch.linspace(-12.5, 12.5, 4000).cuda().view(1, -1)
+    w = torch.zeros(4000, 1, device="cuda")
+    du = bnd.dora_matmul_backward(torch.ones_like(z), z, None, w, act=name, need_dw=False, need_dbias=False,
+                                  need_dcol_scale=False)[4]
+    v = host(z)
+    a = np.abs(v)
+    if name == "gelu":
+        p, q = ndtr(v), v * np.exp(-0.5 * v * v) / np.sqrt(2 * np.pi)
+        n, extra = 16 + 2 * a * a, 0
+    elif name in ("silu", "gelu_tanh"):
+        k = 2 * np.sqrt(2 / np.pi) if name == "gelu_tanh" else 0.5
+        e = k * (a + 0.044715 * a ** 3) if name == "gelu_tanh" else a
+        p = expit(np.sign(v) * e)
+        g = k * (1 + 3 * 0.044715 * v * v) if name == "gelu_tanh" else 1.0
+        # (1 - p is off by p's half steps, however small it is)
+        q, n, extra = v * p * expit(-np.sign(v) * e) * g, 12 + 6 * e, 4 * EPS32 * a * g * p
+    else:
+        p, q, n, extra = B.slope(v, name), 0 * v, 0, 0
+    close(du, p + q, rounded("f32", p + q, n * EPS32 * (np.abs(p) + np.abs(q)) + extra + 2.0 ** -118), name)
