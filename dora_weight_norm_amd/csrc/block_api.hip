@@ -72,6 +72,11 @@ bool matmul_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t r, int64_t es) {
          K * es < kMaxRowBytes && r * es < kMaxRowBytes && N < kMaxRowBytes;
 }
 
+// The backward's products run along M and N too.
+bool backward_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t es) {
+  return matmul_sizes_ok(M, N, K, 0, es) && M * es < kMaxRowBytes && N * es < kMaxRowBytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -174,7 +179,7 @@ dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K,
                                                 size_t* ws_bytes) {
   if (!valid_dtype(dtype)) return DORA_ERR_UNSUPPORTED_DTYPE;
   if (ws_bytes == nullptr || outputs < 0 || outputs >= 2 * DORA_GRAD_ALIGNED ||
-      !matmul_sizes_ok(M, N, K, 0, esize(dtype)) || !matmul_sizes_ok(K, K, M, N, esize(dtype)))
+      !backward_sizes_ok(M, N, K, esize(dtype)))
     return DORA_ERR_INVALID_ARG;
   *ws_bytes = dora::plan_matmul_backward(M, N, K, dtype, outputs & DORA_GRAD_DX, outputs & DORA_GRAD_DW,
                                          outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU, outputs & DORA_GRAD_ALIGNED)
@@ -196,8 +201,7 @@ dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void*
                                       float* dcol_scale, void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_dtype(dtype)) return DORA_ERR_UNSUPPORTED_DTYPE;
   const int64_t es = esize(dtype);
-  if (!matmul_sizes_ok(M, N, K, 0, es) || !matmul_sizes_ok(K, K, M, N, es) || !valid_act(act))
-    return DORA_ERR_INVALID_ARG;
+  if (!backward_sizes_ok(M, N, K, es) || !valid_act(act)) return DORA_ERR_INVALID_ARG;
   const bool rows = M > 0 && N > 0;
   if (rows && (dy == nullptr || u == nullptr)) return DORA_ERR_INVALID_ARG;
   if (dx != nullptr && N * K > 0 && w == nullptr) return DORA_ERR_INVALID_ARG;

@@ -164,3 +164,15 @@ def test_matmul_backward_refuses_a_bad_row_scale():
     assert call(0x5000000) == 1 and call(0x6000004) == 1 and call(0x7000000, du=0x7000000) == 1
     assert call(0x8000010) == 1                                 # in the workspace
     assert call(0x9000000, ws=None) == 4
+
+
+def test_matmul_backward_takes_every_depth_that_the_product_takes():
+    sz = ctypes.c_size_t()
+    lib = bnd.load()
+    for M, N, K in ((16, 8, 100000), (8, 100000, 16), (100000, 8, 16), (16, 8, (1 << 22) - 8)):
+        assert lib.dora_matmul_workspace_size(M, N, K, 0, 0, 15, ctypes.byref(sz)) == 0
+        assert lib.dora_matmul_backward_workspace_size(M, N, K, 0, 31, ctypes.byref(sz)) == 0, (M, N, K)
+        assert _mm_bwd(M=M, N=N, K=K, x=0x10000000, w=0x30000000, dx=0x50000000, dw=0x70000000, ws=None) == 4
+    assert lib.dora_matmul_backward_workspace_size(16, 8, 1 << 22, 0, 31, ctypes.byref(sz)) == 1
+    assert lib.dora_matmul_backward_workspace_size(16, 1 << 22, 8, 0, 31, ctypes.byref(sz)) == 1
+    assert lib.dora_matmul_backward_workspace_size(1 << 22, 16, 8, 0, 31, ctypes.byref(sz)) == 1

@@ -464,3 +464,11 @@ def test_slopes_relative_to_their_terms(name):
     else:
         p, q, n, extra = B.slope(v, name), 0 * v, 0, 0
     close(du, p + q, rounded("f32", p + q, n * EPS32 * (np.abs(p) + np.abs(q)) + extra + 2.0 ** -118), name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(16, 8, 100000), (5, 17, 131071), (70, 100000, 24)])
+def test_backward_of_long_rows(M, N, K, dtype):
+    rng, dy, u, x, w, c, bias = backward_case(M, N, K, dtype, 31)
+    got = bnd.dora_matmul_backward(dy, u, x, w, col_scale=c, bias=bias, act="silu")
+    check_backward(got, dy, u, x, w, c, bias, "silu", dtype)
