@@ -152,7 +152,9 @@ __device__ __forceinline__ float slope_of(float z, int act) {
     }
     case 3: {
       const float p = logistic<F32>(z * fmaf(2.f * kTanhK * kTanhC, z * z, 2.f * kTanhK));
-      return p + z * p * (1.f - p) * 2.f * kTanhK * fmaf(3.f * kTanhC * z, z, 1.f);
+      // (past 32 p is 0 or 1 and the other term 0: z^2 may be infinite there)
+      const float c = fminf(fmaxf(z, -32.f), 32.f);
+      return p + c * p * (1.f - p) * 2.f * kTanhK * fmaf(3.f * kTanhC * c, c, 1.f);
     }
     case 4: {
       const float p = logistic<F32>(z);

@@ -472,3 +472,17 @@ def test_backward_of_long_rows(M, N, K, dtype):
     rng, dy, u, x, w, c, bias = backward_case(M, N, K, dtype, 31)
     got = bnd.dora_matmul_backward(dy, u, x, w, col_scale=c, bias=bias, act="silu")
     check_backward(got, dy, u, x, w, c, bias, "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ACTS)
+def test_slopes_far_out(name, dtype):
+    """Where z^2 is past fp32's range the slope is that of the line that the activation has become."""
+    z = torch.tensor([[1e15, -1e15, 2e19, -2e19, 1e25, -1e25, 3e38, -3e38]], device="cuda").to(TORCH_DT[dtype])
+    du = bnd.dora_matmul_backward(torch.ones_like(z), z, None, torch.zeros(8, 1, device="cuda", dtype=z.dtype),
+                                  act=name, need_dw=False, need_dbias=False, need_dcol_scale=False)[4]
+    want = [1.0, 1.0 if name == "none" else 0.0] * 4
+    assert host(du)[0].tolist() == want
+    y, _ = bnd.dora_matmul(torch.empty(1, 0, device="cuda", dtype=z.dtype),
+                           torch.empty(8, 0, device="cuda", dtype=z.dtype), bias=z[0].float(), act=name)
+    assert torch.equal(y, torch.where((z > 0) | (name == "none"), z, torch.zeros_like(z)))
