@@ -144,6 +144,15 @@ def _call(name: str, *args) -> None:
         raise DoraError(name, st)
 
 
+def _call_on(dev: int, name: str, *args) -> None:
+    """_call with GPU `dev`, the tensors' and the stream's, as the current one."""
+    if _current_device() == dev:
+        _call(name, *args)
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args)
+
+
 def dora_version() -> int:
     return load().dora_version()
 
@@ -201,12 +210,22 @@ def _workspace(t, name: str, need: int, device):
         raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes; {need} are needed")
 
 
-def _on(stream):
+# (the index alone, without the checks around it)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on(stream, device=None):
     """Allocations made inside belong to `stream` (torch's caching allocator
     then reuses their memory only after the work queued on `stream`), so
     temporaries freed on return cannot be handed to other work while the
-    kernels launched on `stream` still use them."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    kernels launched on `stream` still use them. Without a stream, `device`
+    (of the tensors) is the current GPU inside: the null stream and the
+    library's launches are the current GPU's."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device is not None and device.index != _current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
 
 
 def dora_norm_chunk_size(d_out: int, d_in: int, budget_bytes: int = DEFAULT_BUDGET) -> int:
@@ -262,7 +281,7 @@ def dora_factored_norm(W, A, B, s: float, budget_bytes: int = DEFAULT_BUDGET, m=
         _out_like(m, "m", (d_out,), torch.float32, dev)
         if g is not None:
             _out_like(g, "g", (d_out,), torch.float32, dev)
-    with _on(stream):
+    with _on(stream, dev):
         if workspace is None and ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         if wnorm is None:
@@ -314,7 +333,7 @@ def dora_factored_norm_noalloc(W, A, B, s: float, budget_bytes: int = DEFAULT_BU
         _out_like(m, "m", (d_out,), torch.float32, dev)
         if g is not None:
             _out_like(g, "g", (d_out,), torch.float32, dev)
-    with _on(stream):
+    with _on(stream, dev):
         if wnorm is None:
             wnorm = torch.empty(d_out, dtype=torch.float32, device=dev)
         if m is not None and g is None:
@@ -332,7 +351,7 @@ def dora_magnitude_scale(m, wnorm, eps: float = 1e-6, g=None, stream=None):
     _out_like(wnorm, "wnorm", m.shape, torch.float32, m.device)
     if g is not None:
         _out_like(g, "g", m.shape, torch.float32, m.device)
-    with _on(stream):
+    with _on(stream, m.device):
         if g is None:
             g = torch.empty_like(m)
         _call("dora_magnitude_scale", _ptr(m), _ptr(wnorm), eps, m.numel(), _ptr(g), _stream(stream))
@@ -347,7 +366,7 @@ def dora_norm_to_dtype(wnorm, dtype, out=None, stream=None):
     tdt = {DORA_BF16: torch.bfloat16, DORA_F32: torch.float32, DORA_F16: torch.float16}[_dtype_code(dtype)]
     if out is not None:
         _out_like(out, "out", wnorm.shape, tdt, wnorm.device)
-    with _on(stream):
+    with _on(stream, wnorm.device):
         if out is None:
             out = torch.empty(wnorm.shape, dtype=tdt, device=wnorm.device)
         _call("dora_norm_to_dtype", _ptr(wnorm), wnorm.numel(), _dtype_code(dtype), _ptr(out), _stream(stream))
@@ -369,7 +388,7 @@ def _compose_call(name, base, lora, g, s, out, stream):
     dt = _dtype_code(base.dtype)
     if out is not None:
         _out_like(out, "out", base.shape, base.dtype, base.device)
-    with _on(stream):
+    with _on(stream, base.device):
         if out is None:
             out = torch.empty_like(base)
         _call(name, _ptr(base), _ptr(lora), _ptr(g), s, dt, T, d_out, _ptr(out), _stream(stream))
@@ -429,7 +448,7 @@ def dora_compose_backward(dy, base, lora, g, s: float, need_dg: bool = True, wno
     ws_bytes = dora_compose_backward_workspace_size(T, d_out) if need_dg else 0
     if workspace is not None and ws_bytes > 0:
         _workspace(workspace, "workspace", ws_bytes, dev)
-    with _on(stream):
+    with _on(stream, dev):
         d_base = torch.empty_like(dy) if d_base is None else d_base
         d_lora = torch.empty_like(dy) if d_lora is None else d_lora
         dg = torch.empty(d_out, dtype=torch.float32, device=dev) if need_dg else None
@@ -584,7 +603,8 @@ def _rms_norm(x, weight, eps, residual, h, rstd, want_rstd, stream, y=None, q=No
     else:
         y = _new(stream, shape, dtype, dev) if y is None else y
         py = _want(y, "y", shape, dtype, dev)
-    _call("dora_rms_norm", x.data_ptr(), pres, pw, eps, code, T, d, ph, py, pq, ps, prs, _raw_stream(stream, dev))
+    _call_on(dev, "dora_rms_norm", x.data_ptr(), pres, pw, eps, code, T, d, ph, py, pq, ps, prs,
+             _raw_stream(stream, dev))
     return y, q, scale, (x if residual is None else h), rstd
 
 
@@ -628,8 +648,8 @@ def dora_rms_norm_backward(dy, h, rstd, weight, dh=None, need_dweight: bool = Tr
         dweight = _new(stream, (d,), f32, dev)
     pdx, pdw = _want(dx, "dx", shape, dtype, dev), _maybe(dweight, "dweight", (d,), f32, dev)
     workspace = _space(workspace, need, stream, dev)
-    _call("dora_rms_norm_backward", dy.data_ptr(), pdh, ph, prs, pw, code, T, d, pdx, pdw, _addr(workspace), need,
-          _raw_stream(stream, dev))
+    _call_on(dev, "dora_rms_norm_backward", dy.data_ptr(), pdh, ph, prs, pw, code, T, d, pdx, pdw, _addr(workspace),
+             need, _raw_stream(stream, dev))
     return dx, dweight
 
 
@@ -687,8 +707,8 @@ def dora_matmul(x, w, row_scale=None, col_scale=None, t=None, b=None, s: float =
         u = _new(stream, out, odt, dev)
     py, pu = _want(y, "y", out, odt, dev), _maybe(u, "u", out, odt, dev)
     workspace = _space(workspace, need, stream, dev)
-    _call("dora_matmul", px, pw, code, M, N, K, prow, pcol, pt, pb, r, s, pbias, act_code, pres, out_code, py, pu,
-          _addr(workspace), need, _raw_stream(stream, dev))
+    _call_on(dev, "dora_matmul", px, pw, code, M, N, K, prow, pcol, pt, pb, r, s, pbias, act_code, pres, out_code, py,
+             pu, _addr(workspace), need, _raw_stream(stream, dev))
     return y, u
 
 
@@ -736,7 +756,7 @@ def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "non
                + GRAD_ALIGNED * ((not need_dw or x.data_ptr() % 16 == 0) and (not need_dx or w.data_ptr() % 16 == 0)))
     need = _size_of("dora_matmul_backward_workspace_size", M, N, K, code, outputs)
     workspace = _space(workspace, need, stream, dev)
-    _call("dora_matmul_backward_rows", dy.data_ptr(), pu, _addr(x) if need_dw else None,
-          _addr(w) if need_dx else None, code, M, N, K, prow, pcol, pbias, act_code, _addr(du), _addr(dx), _addr(dw),
-          _addr(dbias), _addr(dcol), _addr(workspace), need, _raw_stream(stream, dev))
+    _call_on(dev, "dora_matmul_backward_rows", dy.data_ptr(), pu, _addr(x) if need_dw else None,
+             _addr(w) if need_dx else None, code, M, N, K, prow, pcol, pbias, act_code, _addr(du), _addr(dx),
+             _addr(dw), _addr(dbias), _addr(dcol), _addr(workspace), need, _raw_stream(stream, dev))
     return dx, dw, dbias, dcol, du

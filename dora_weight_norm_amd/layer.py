@@ -46,7 +46,7 @@ def dora_linear(x, W, A, B, m, s: float, eps: float = 1e-6, budget_bytes: int = 
         raise ValueError("shapes must be x [..., d_in], W [d_out, d_in], A [r, d_in], B [d_out, r]")
     lead = x.shape[:-1]
     x2 = x.reshape(-1, d_in).contiguous()
-    st = torch.cuda.current_stream() if stream is None else stream
+    st = torch.cuda.current_stream(x.device if x.is_cuda else None) if stream is None else stream
     with torch.cuda.stream(st):
         base = torch.mm(x2, W.t())
         lora = torch.mm(torch.mm(x2, A.t()), B.t())

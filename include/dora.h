@@ -28,7 +28,9 @@
  *     a pointer. Its only host state is the device address of the
  *     dora_factored_norm_noalloc scratch array on each GPU, looked up once
  *     per GPU and never changed.
- *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
+ *   - `stream` is a hipStream_t passed as void* (NULL = the null stream of
+ *     the current GPU). The current GPU is the one that the stream and the
+ *     buffers belong to.
  *     All work is enqueued asynchronously on it; results are valid once
  *     the stream has reached that point. Calls enqueue kernels only (no
  *     memset, copy, allocation or host synchronisation; counters a call
