@@ -567,9 +567,9 @@ def dora_matmul_workspace_size(M: int, N: int, K: int, r: int, dtype, aligned_op
 
 
 def dora_matmul_plan_info(M: int, N: int, K: int, r: int, dtype, aligned_operands: int = 15) -> dict:
-    buf = (_c_i64 * 4)()
-    _call("dora_matmul_plan_info", M, N, K, r, _operand_code(dtype), aligned_operands, buf, 4)
-    return dict(zip(("tile_rows", "splits", "copies", "workspace_bytes"), list(buf)))
+    buf = (_c_i64 * 5)()
+    _call("dora_matmul_plan_info", M, N, K, r, _operand_code(dtype), aligned_operands, buf, 5)
+    return dict(zip(("tile_rows", "splits", "copies", "workspace_bytes", "few_rows"), list(buf)))
 
 
 def dora_matmul_backward_workspace_size(M: int, N: int, K: int, dtype, outputs: int = 31) -> int:

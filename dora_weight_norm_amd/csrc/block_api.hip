@@ -142,8 +142,9 @@ dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, in
                                             : dora::MatmulPlan{};
   const int rows = p.cfg == dora::kTile256 ? 256 : (p.cfg == dora::kTile128 ? 128 : (p.cfg == dora::kTile64 ? 64 : 0));
   const int copies = (p.pack_x ? 1 : 0) | (p.pack_w ? 2 : 0) | (p.pack_t ? 4 : 0) | (p.pack_b ? 8 : 0);
-  const int64_t vals[] = {M > 0 && N > 0 ? rows : -1, p.splits, copies, (int64_t)p.ws_bytes};
-  for (int i = 0; i < n_info; ++i) info[i] = i < 4 ? vals[i] : -1;
+  const int few = p.cfg == dora::kFew8 ? 8 : (p.cfg == dora::kFew16 ? 16 : (p.cfg == dora::kFew32 ? 32 : -1));
+  const int64_t vals[] = {M > 0 && N > 0 ? rows : -1, p.splits, copies, (int64_t)p.ws_bytes, few};
+  for (int i = 0; i < n_info; ++i) info[i] = i < 5 ? vals[i] : -1;
   return DORA_OK;
 }
 

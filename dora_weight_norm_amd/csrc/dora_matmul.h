@@ -39,8 +39,9 @@ struct GemmArgs {
   Epilogue ep;
 };
 
-// Kernels: tiles of 256, 128 or 64 rows and columns, or the few-rows kernel.
-enum MatmulTile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFewRows = 3 };
+// Kernels: tiles of 256, 128 or 64 rows and columns, or the few-rows kernel on
+// 8 rows by 16 columns, 16 by 16 or 32 by 32.
+enum MatmulTile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4, kFew32 = 5 };
 
 struct MatmulPlan {
   int cfg;

@@ -1055,31 +1055,57 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workgroups of 16 x 16 of the few-rows kernel.
 int64_t few_blocks(int64_t M, int64_t N) { return up(M, 16) / 16 * (up(N, 16) / 16); }
-// 17 to 32 rows take 32 x 32 instead where 16 x 16 would need a second round,
-// so that w is read once (32 x 1001 x 1024 bf16: 5.1 us in 16 x 16, 8.6 in
-// 32 x 32; 48 x 4096 x 4096, two rounds and more: 27 against 22).
-bool few_wide(int64_t M, int64_t N) { return M > 16 && M <= 32 && few_blocks(M, N) > kCUs; }
+// The most parts of the depth that n workgroups of it are split into: while
+// they do not fill the chip and each wave keeps four steps.
+int64_t few_splits(int64_t n, int64_t stages) {
+  int64_t s = n >= kCUs || n < 1 ? 1 : kCUs / n;
+  if (s > stages / 16) s = stages / 16;
+  return s < 1 ? 1 : s;
+}
+// 17 to 32 rows take 32 x 32, which reads w once instead of twice, where 16 x
+// 16 would need a second round (48 x 4096 x 4096, two rounds and more: 27 us
+// against 22; 32 x 1001 x 1024 bf16: 5.1 us in 16 x 16, 8.6 in 32 x 32). So do
+// long depths of more than 512 columns, from 64 stages on for rows off the
+// 16-byte grid, whose every load takes two lines, and 128 for others, if a
+// workgroup of 16 x 16 would have 48 of them or more. Measured, 16 x 16 against
+// 32 x 32, us on the GPU:
+//   17 and 32 x 1001 x 8189 fp16   25.2, 20.3 and 24.5, 23.6
+//   17 and 32 x 2048 x 4093 fp16   23.9, 19.0 and 23.5, 21.8
+//   17 and 32 x 1500 x 3581 fp16   21.9, 21.9 and 22.1, 25.3 (56 stages)
+//   17 and 32 x 1001 x 8192 bf16   15.6, 14.0 and 15.6, 15.2
+//   17 and 32 x 2048 x 8192 bf16   19.9, 17.5 and 18.6, 19.3
+//   17 and 32 x 2048 x 4096 bf16   11.0, 11.0 and 10.8, 12.7 (64 stages)
+//   17 and 32 x 2048 x 16384 e4m3  19.1, 15.2 and 18.0, 17.9
+//   17 and 32 x 256 x 32765 fp16   26.4, 28.0 and 25.9, 31.5
+// fp32, whose matrix instructions are the slow part, gains nowhere (17 x 2048
+// x 4096: 20.4, 22.1).
+bool few_wide(int64_t M, int64_t N, int64_t stages, int dtype, bool on_grid) {
+  if (M <= 16 || M > 32) return false;
+  const int64_t n = few_blocks(M, N);
+  if (n > kCUs) return true;
+  return dtype != 1 && n > 64 && stages >= (on_grid ? 128 : 64) && stages >= 48 * few_splits(n, stages);
+}
 
 // `few`: the most stages that a workgroup of the few-rows kernel may take where
 // there are more than 32 rows, 0 where it cannot run. Rows off the 16-byte
 // grid are copied for the tiles and not here, where their loads cost more from
 // about 24 stages on (128 x 256 x 4093 fp16, 32 a workgroup: 17.2 us, 15.9 as
 // a tile).
+constexpr int kFewOnGrid = 64, kFewOffGrid = 24;
 void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* cfg, int* splits) {
   if (few > 0 && (M <= 32 || (stages >= 4 && few_blocks(M, N) <= kCUs))) {
-    // The depth is split over workgroups too while they do not fill the chip
-    // and each wave keeps four steps. More than 32 rows come here while one
-    // round of workgroups covers the result and none has more than `few` stages
+    // Up to 32 rows come here at any depth and alignment (17 x 1001 x 8189
+    // fp16: 20 us, 32 as a tile behind copies; 32 x 8192 x 4093: 45.5, 40.9).
+    // More than 32 rows come here while one round of workgroups covers the
+    // result and none has more than `few` stages
     // (64-row tile against this, us on the GPU: 64 x 256 x 256 fp32 9.6, 5.6;
     // 256 x 256 x 1024 bf16 7.1, 4.8; 64 x 1001 x 4096 bf16 16.7, 12.4; but
     // 64 x 4096 x 1024 bf16, four rounds, 7.2, 11.6). Below four stages the
     // two differ by 1 us or less, which the host's share of the call hides.
-    const int64_t n = few_wide(M, N) ? up(N, 32) / 32 : few_blocks(M, N);
-    int64_t s = n >= kCUs || n < 1 ? 1 : kCUs / n;
-    if (s > stages / 16) s = stages / 16;
-    if (s < 1) s = 1;
+    const bool wide = few_wide(M, N, stages, dtype, few == kFewOnGrid);
+    const int64_t s = few_splits(wide ? up(N, 32) / 32 : few_blocks(M, N), stages);
     if (M <= 32 || stages <= few * s) {
-      *cfg = kFewRows;
+      *cfg = M <= 8 ? kFew8 : (wide ? kFew32 : kFew16);
       *splits = (int)s;
       return;
     }
@@ -1172,9 +1198,9 @@ hipError_t launch_gemm_tr(GemmArgs g, int cfg, hipStream_t st) {
 
 template <typename T, typename O>
 hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
-  if (cfg == kFewRows)
-    return g.M <= 8 ? launch_few_rows<T, O, 2, 1>(g, st)
-                    : (few_wide(g.M, g.N) ? launch_few_rows<T, O, 4, 4>(g, st) : launch_few_rows<T, O, 2, 2>(g, st));
+  if (cfg == kFew8) return launch_few_rows<T, O, 2, 1>(g, st);
+  if (cfg == kFew16) return launch_few_rows<T, O, 2, 2>(g, st);
+  if (cfg == kFew32) return launch_few_rows<T, O, 4, 4>(g, st);
   split_stages(g, 128 / Op<T>::esz);
   hipError_t e = hipErrorInvalidValue;
   if (g.K2 > 0) {
@@ -1244,10 +1270,10 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   MatmulPlan p{};
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
-  choose_tile(M, N, up(K, KT) / KT, dtype, K % epc == 0 ? 64 : 24, &p.cfg, &p.splits);
+  choose_tile(M, N, up(K, KT) / KT, dtype, K % epc == 0 ? kFewOnGrid : kFewOffGrid, &p.cfg, &p.splits);
   auto operand = [&](int64_t rows, int64_t depth, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
-    *pack = p.cfg != kFewRows && depth > 0 && (depth % epc != 0 || !(al & bit));
+    *pack = p.cfg < kFew8 && depth > 0 && (depth % epc != 0 || !(al & bit));
     *ld = *pack ? up(depth, epc) : depth;
     *at = off;
     if (*pack) off = up256(off + (size_t)(rows * *ld) * esz);
@@ -1311,11 +1337,11 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.off_xt = take(!need_dw ? 0 : (p.copy ? (size_t)(M * p.ldk) * esz : (p.direct ? 0 : (size_t)(K * p.ldm) * esz)));
   size_t part = 0;
   if (need_dx) {
-    choose_tile(M, K, up(N, KT) / KT, dtype, p.direct ? 0 : 64, &p.cfg_dx, &p.splits_dx);
+    choose_tile(M, K, up(N, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dx, &p.splits_dx);
     if (p.splits_dx > 1) part = (size_t)(p.splits_dx * M * K) * 4;
   }
   if (need_dw) {
-    choose_tile(N, K, up(M, KT) / KT, dtype, p.direct ? 0 : 64, &p.cfg_dw, &p.splits_dw);
+    choose_tile(N, K, up(M, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dw, &p.splits_dw);
     const size_t q = p.splits_dw > 1 ? (size_t)(p.splits_dw * N * K) * 4 : 0;
     part = q > part ? q : part;
   }

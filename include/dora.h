@@ -427,8 +427,9 @@ dora_status dora_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int64_t 
  * n_info-1] are, in order, the rows of its tile (256, 128 or 64; 0: the
  * kernel for few rows and small products; -1: nothing to do), the parts the depth is split into
  * (more than one are added by a second launch), a bit for each operand that
- * is copied first (as in dora_matmul_workspace_size), and the workspace
- * bytes; further entries are -1. Host only.
+ * is copied first (as in dora_matmul_workspace_size), the workspace bytes, and
+ * the rows that a workgroup of the few-rows kernel takes (8, 16 or 32; -1 for
+ * a tile); further entries are -1. Host only.
  */
 dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, int aligned_operands,
                                   int64_t* info, int n_info);

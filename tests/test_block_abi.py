@@ -176,3 +176,20 @@ def test_matmul_backward_takes_every_depth_that_the_product_takes():
     assert lib.dora_matmul_backward_workspace_size(16, 8, 1 << 22, 0, 31, ctypes.byref(sz)) == 1
     assert lib.dora_matmul_backward_workspace_size(16, 1 << 22, 8, 0, 31, ctypes.byref(sz)) == 1
     assert lib.dora_matmul_backward_workspace_size(1 << 22, 16, 8, 0, 31, ctypes.byref(sz)) == 1
+
+
+def test_which_blocks_few_rows_take():
+    def few(M, N, K, dtype, r=0):
+        return bnd.dora_matmul_plan_info(M, N, K, r, dtype)["few_rows"]
+
+    assert few(1, 8192, 8192, "bf16") == few(8, 300, 64, "f32") == 8
+    assert few(9, 8192, 8192, "bf16") == few(16, 28672, 8192, "e4m3") == 16
+    # 17 to 32 rows: more than one round of 16 x 16, or a long depth of enough columns
+    for M in (17, 32):
+        for dtype in ("bf16", "f16", "f32", "e4m3"):
+            assert few(M, 2064, 1024, dtype) == 32 and few(M, 2048, 1024, dtype) == 16
+        assert few(M, 1001, 8189, "f16") == 32 and few(M, 1001, 8192, "bf16") == 32
+        assert few(M, 1001, 4093, "f16") == 16 and few(M, 2048, 4096, "bf16") == 16
+        assert few(M, 2048, 16384, "e4m3") == 32 and few(M, 2048, 8192, "e4m3") == 16
+        assert few(M, 2048, 8192, "f32") == 16 and few(M, 256, 32765, "f16") == 16
+    assert few(64, 256, 256, "f32") == 16 and few(64, 64, 64, "bf16") == -1

@@ -486,3 +486,17 @@ def test_slopes_far_out(name, dtype):
     y, _ = bnd.dora_matmul(torch.empty(1, 0, device="cuda", dtype=z.dtype),
                            torch.empty(8, 0, device="cuda", dtype=z.dtype), bias=z[0].float(), act=name)
     assert torch.equal(y, torch.where((z > 0) | (name == "none"), z, torch.zeros_like(z)))
+
+
+# 17 to 32 rows in blocks of 32 x 32: many columns, or a long depth in one part or several (a stage of depth is 128
+# bytes, so that the 8-bit types need twice the depth; fp32 takes 16 x 16 there).
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32", "e4m3"])
+@pytest.mark.parametrize("M,N,K,r,wide", [(17, 2065, 1037, 9, "bf16 f16 f32 e4m3"), (32, 4104, 520, 24, "bf16 f16 f32 e4m3"),
+                                          (31, 8200, 77, 0, "bf16 f16 f32 e4m3"), (17, 530, 17000, 5, "bf16 f16"),
+                                          (29, 1001, 8189, 0, "bf16 f16"), (24, 2048, 16392, 16, "bf16 f16 e4m3"),
+                                          (32, 2100, 0, 40, "bf16 f16 f32 e4m3")])
+def test_few_rows_in_blocks_of_32(M, N, K, r, wide, dtype):
+    r = 0 if dtype == "e4m3" else r
+    assert bnd.dora_matmul_plan_info(M, N, K, r, dtype)["few_rows"] == (32 if dtype in wide.split() else 16)
+    o, rng = operands(M, N, K, r, dtype, M + N + K)
+    check(o, rng, dtype, "bf16" if dtype == "e4m3" else dtype, ACTS[N % 5], True, True)
