@@ -500,3 +500,32 @@ def test_few_rows_in_blocks_of_32(M, N, K, r, wide, dtype):
     assert bnd.dora_matmul_plan_info(M, N, K, r, dtype)["few_rows"] == (32 if dtype in wide.split() else 16)
     o, rng = operands(M, N, K, r, dtype, M + N + K)
     check(o, rng, dtype, "bf16" if dtype == "e4m3" else dtype, ACTS[N % 5], True, True)
+
+
+# Each tile with its depth in one part and in several, by type (the plan is asserted): (M, N, K, tile rows, split).
+TILES = {"bf16": [(300, 520, 264, 64, False), (2097, 17, 1312, 64, True), (4154, 453, 40, 128, False),
+                  (66, 4207, 5224, 128, True), (2193, 3701, 40, 256, False), (5449, 433, 4840, 256, True)],
+         "f16": [(66, 4207, 5224, 128, True), (2193, 3701, 40, 256, False)],
+         "f32": [(300, 520, 264, 64, False), (2209, 17, 424, 64, True), (4154, 453, 32, 128, False),
+                 (1500, 2056, 264, 128, False), (4165, 65, 1328, 128, True)],
+         "e4m3": [(70, 300, 272, 64, False), (70, 520, 4104, 64, True), (4154, 453, 48, 128, False),
+                  (76, 5590, 7520, 128, True), (2193, 3701, 48, 256, False)]}
+
+
+@pytest.mark.parametrize("dtype,M,N,K,rows,split", [(t, *c) for t in TILES for c in TILES[t]])
+def test_every_tile_of_every_type(dtype, M, N, K, rows, split):
+    plan = bnd.dora_matmul_plan_info(M, N, K, 0, dtype)
+    assert plan["tile_rows"] == rows and (plan["splits"] > 1) == split, plan
+    for out in ("bf16", "f16", "f32") if dtype == "e4m3" else (dtype,):
+        for r in (0,) if dtype == "e4m3" else (0, 24):
+            o, rng = operands(M, N, K, r, dtype, M + K)
+            check(o, rng, dtype, out, ACTS[1 + (M + r) % 4], r == 0, True)
+
+
+# The backward's products with their depth in several parts, and fp32's 128-row tile.
+@pytest.mark.parametrize("M,N,K,dtype", [(66, 5224, 4207, "bf16"), (4840, 5449, 433, "bf16"), (66, 5224, 4208, "f16"),
+                                         (4165, 1328, 65, "f32"), (264, 1500, 2056, "f32"), (1500, 264, 2056, "f32")])
+def test_backward_of_every_tile(M, N, K, dtype):
+    rng, dy, u, x, w, c, bias = backward_case(M, N, K, dtype, 41)
+    got = bnd.dora_matmul_backward(dy, u, x, w, col_scale=c, bias=bias, act="gelu")
+    check_backward(got, dy, u, x, w, c, bias, "gelu", dtype)
