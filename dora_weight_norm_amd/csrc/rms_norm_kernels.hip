@@ -29,7 +29,9 @@ constexpr float kE4m3Max = 448.f;
 // stores, 77.5 us with non-temporal ones; at 777 x 3583, which the caches
 // hold, 8.1 and 8.6 us. Loads only where rows are whole 128-byte lines: two
 // rows share a line otherwise, which was then read twice (5568 x 3000: 27.2 us
-// with both, 22.6 with the stores alone).
+// with both, 22.6 with the stores alone). The backward's loads by the same rule,
+// its stores through the caches (9000 x 1000 bf16: 48.8 us with non-temporal
+// loads, 38.1 without; 2200 x 4100 38.4, 30.0; 5568 x 3000 43.6, 45.0).
 constexpr int64_t kStreamBytes = (int64_t)16 << 20;
 constexpr int64_t kFwdGrid = 1024;   // workgroups of 256 threads, four a compute unit
 // Smallest scale: rows whose largest |n| is below 448 times it (about 2^-91)
@@ -631,9 +633,10 @@ hipError_t launch_bwd(NormBwdArgs a, float* dweight, hipStream_t st) {
   const int64_t grid = backward_grid(a.T, a.d, Elem<T>::epc);
   if (grid > 0) {
     hipError_t e = hipErrorInvalidValue;
+    const bool stream = a.T * a.d * (int64_t)sizeof(T) > kStreamBytes && a.d * (int64_t)sizeof(T) % 128 == 0;
 #define DORA_NORM_BWD(NT, C)                                                                            \
   if (r.nt == NT && r.c == C) {                                                                         \
-    if (a.T * a.d * (int64_t)sizeof(T) > kStreamBytes)                                                  \
+    if (stream)                                                                                         \
       hipLaunchKernelGGL((rms_norm_bwd_kernel<T, NT, C, true>), dim3((unsigned)grid), dim3(NT), 0, st, a);  \
     else                                                                                                \
       hipLaunchKernelGGL((rms_norm_bwd_kernel<T, NT, C, false>), dim3((unsigned)grid), dim3(NT), 0, st, a); \
