@@ -31,6 +31,9 @@ constexpr int64_t kMaxElems = (int64_t)1 << 33;
 // Bytes of one row of a product's operand (the tile kernel's 32-bit offsets
 // span 256 rows).
 constexpr int64_t kMaxRowBytes = (int64_t)1 << 23;
+// Rows of a product: 64 of them a workgroup of 256 threads, and a launch takes
+// less than 2^32 threads.
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
 
 bool size_ok(int64_t a, int64_t b) {
   return a >= 0 && b >= 0 && a < kMaxDim && b < kMaxDim && (b == 0 || a <= kMaxElems / b);
@@ -69,7 +72,7 @@ int64_t operand_size(int dt) { return dt == DORA_E4M3 ? 1 : esize(dt); }
 
 bool matmul_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t r, int64_t es) {
   return size_ok(M, K) && size_ok(N, K) && size_ok(M, N) && size_ok(M, r) && size_ok(N, r) &&
-         K * es < kMaxRowBytes && r * es < kMaxRowBytes && N < kMaxRowBytes;
+         M < kMaxRows && K * es < kMaxRowBytes && r * es < kMaxRowBytes && N < kMaxRowBytes;
 }
 
 // The backward's products run along M and N too.

@@ -457,7 +457,8 @@ dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, in
  * y and u are each rounded once. `workspace` (256-byte aligned) holds at
  * least dora_matmul_workspace_size bytes; its contents on entry are ignored.
  * K == 0 gives u = s t b^T (0 without a pair); M == 0 or N == 0 does nothing.
- * Rows of x, w, t, b take less than 2^23 bytes.
+ * Rows of x, w, t, b take less than 2^23 bytes, N is less than 2^23, M less
+ * than 2^30, and no matrix has more than 2^33 elements.
  * Errors: DORA_ERR_INVALID_ARG (sizes, s not finite, unknown act, a pair in
  * e4m3, missing, misaligned or overlapping pointers),
  * DORA_ERR_UNSUPPORTED_DTYPE, DORA_ERR_WORKSPACE, DORA_ERR_HIP.
@@ -492,7 +493,8 @@ dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K,
  * those of two more products: with du as dy, act none and col_scale NULL,
  * x = t and w = b give s^-1 dt (dx) and s^-1 db (dw). Sums are fp32 in a
  * fixed order, without atomics; act' of relu at 0 is 0.
- * Errors: as dora_matmul; M and N too are limited to rows of 2^23 bytes.
+ * Errors: as dora_matmul; M and N too are limited to rows of less than 2^23
+ * bytes.
  */
 dora_status dora_matmul_backward(const void* dy, const void* u, const void* x, const void* w, int dtype, int64_t M,
                                  int64_t N, int64_t K, const float* col_scale, const float* bias, int act, void* du,

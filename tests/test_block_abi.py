@@ -193,3 +193,14 @@ def test_which_blocks_few_rows_take():
         assert few(M, 2048, 16384, "e4m3") == 32 and few(M, 2048, 8192, "e4m3") == 16
         assert few(M, 2048, 8192, "f32") == 16 and few(M, 256, 32765, "f16") == 16
     assert few(64, 256, 256, "f32") == 16 and few(64, 64, 64, "bf16") == -1
+
+
+def test_rows_past_a_launch_are_refused():
+    sz = ctypes.c_size_t()
+    f = bnd.load().dora_matmul_workspace_size
+    # a 64-row tile has 256 threads: 2^30 rows are 2^32 threads, more than a launch takes
+    assert f(1 << 30, 4, 4, 0, 0, 15, ctypes.byref(sz)) == 1
+    assert f((1 << 30) - 1, 4, 4, 0, 0, 15, ctypes.byref(sz)) == 0
+    far = dict(x=0x1000000, w=0x2000000, col_scale=None, bias=None, y=0x10_0000_0000, ws=0x100_0000_0000)
+    assert _mm(M=1 << 30, N=4, K=4, **far) == 1
+    assert _mm(M=4, N=1 << 23, K=4) == 1 and _mm(M=1 << 17, N=64, K=1 << 17) == 1
