@@ -66,7 +66,10 @@ def adapted_linear(x, layer: AdaptedLayer, g, act: str = "none", residual=None, 
 
 def adapted_linear_backward(dy, u, t, x, layer: AdaptedLayer, g, act: str = "none", stream=None):
     """Gradients of adapted_linear: a dict with x, A, B (storage dtype), g and bias (float32 [d_out]); the
-    residual's is dy. W is frozen."""
+    residual's is dy. W is frozen.
+
+    The products take no scale or addend, so s is applied to dA, dB and the adapter's part of dx after they are
+    rounded, which rounds each a second time, and dx is rounded once more as their sum."""
     dx, _, dbias, dg, du = bnd.dora_matmul_backward(dy, u, None, layer.W, col_scale=g, bias=layer.bias, act=act,
                                                     need_dw=False, need_dbias=layer.bias is not None, stream=stream)
     plain = dict(need_dbias=False, need_dcol_scale=False, stream=stream)

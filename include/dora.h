@@ -375,7 +375,7 @@ dora_status dora_compose_backward(const void* dy, const void* base, const void* 
  * scale and q NaN; an infinity (or a sum of squares past fp32's range) makes
  * rstd 0, so that n is 0, or NaN at the infinity, and scale and q are then
  * NaN as well. T == 0 does nothing; d == 0 has no norm and is refused when
- * scale or rstd is asked for.
+ * scale or rstd is asked for. T and d are below 2^31, T * d at most 2^33.
  * Errors: DORA_ERR_INVALID_ARG (sizes, eps not finite or <= 0, missing,
  * misaligned or overlapping pointers), DORA_ERR_UNSUPPORTED_DTYPE,
  * DORA_ERR_HIP.
@@ -425,11 +425,11 @@ dora_status dora_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int64_t 
 /*
  * The plan dora_matmul would use, for diagnostics and tests: info[0 ..
  * n_info-1] are, in order, the rows of its tile (256, 128 or 64; 0: the
- * kernel for few rows and small products; -1: nothing to do), the parts the depth is split into
- * (more than one are added by a second launch), a bit for each operand that
- * is copied first (as in dora_matmul_workspace_size), the workspace bytes, and
- * the rows that a workgroup of the few-rows kernel takes (8, 16 or 32; -1 for
- * a tile); further entries are -1. Host only.
+ * kernel for few rows and small products; -1: nothing to do), the parts the
+ * depth is split into (more than one are added by a second launch), a bit for
+ * each operand that is copied first (as in dora_matmul_workspace_size), the
+ * workspace bytes, and the rows that a workgroup of the few-rows kernel takes
+ * (8, 16 or 32; -1 for a tile); further entries are -1. Host only.
  */
 dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, int aligned_operands,
                                   int64_t* info, int n_info);
@@ -445,8 +445,8 @@ dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, in
  * r == 0, and none in e4m3). row_scale fp32 [M], col_scale and bias fp32 [N],
  * residual [M, N], each or NULL. y, u and residual are of `out_dtype`, which
  * is `dtype` except for e4m3 (any of the three). u, if not NULL, receives the
- * product before the column scale, for the backward. y may be residual
- * itself.
+ * product before the column scale, for the backward (with a row_scale:
+ * dora_matmul_backward_rows). y may be residual itself.
  *
  * With w = W, b = B, s the adapter's and col_scale = g of dora_factored_norm,
  * y is the whole DoRA layer g * (x W^T + s t B^T) + bias in one launch, with
@@ -454,8 +454,17 @@ dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, in
  * dora_rms_norm as x and row_scale, col_scale carries the weight rows' scales.
  *
  * Products accumulate in fp32 on the matrix cores, the epilogue is fp32, and
- * y and u are each rounded once. `workspace` (256-byte aligned) holds at
- * least dora_matmul_workspace_size bytes; its contents on entry are ignored.
+ * y and u are each rounded once. The 8-bit matrix instructions align each
+ * group of eight products to the largest of them and drop what lies 2^-13
+ * below it: an e4m3 sum is off by up to 7 * 2^-13 of the sum of its products'
+ * sizes more (about 2^-17 of it on normal data). Activations are accurate
+ * relative to their value, in the tails too: an fp32 result to (16 + 2 z^2)
+ * 2^-24 for gelu and (8 + 4 |e|) 2^-24 for the others, e being the argument of
+ * their exponential; 16-bit results far below half a step. What is below
+ * 2^-122 may be 0.
+ *
+ * `workspace` (256-byte aligned) holds at least dora_matmul_workspace_size
+ * bytes; its contents on entry are ignored.
  * K == 0 gives u = s t b^T (0 without a pair); M == 0 or N == 0 does nothing.
  * Rows of x, w, t, b take less than 2^23 bytes, N is less than 2^23, M less
  * than 2^30, and no matrix has more than 2^33 elements.
