@@ -529,3 +529,37 @@ def test_backward_of_every_tile(M, N, K, dtype):
     rng, dy, u, x, w, c, bias = backward_case(M, N, K, dtype, 41)
     got = bnd.dora_matmul_backward(dy, u, x, w, col_scale=c, bias=bias, act="gelu")
     check_backward(got, dy, u, x, w, c, bias, "gelu", dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [(5, 300, 530), (16, 40, 2064), (24, 2100, 272), (64, 130, 1040), (300, 520, 272),
+                                   (2193, 3701, 48)])
+def test_a_nan_stays_in_its_row_and_column(M, N, K, dtype):
+    o, _ = operands(M, N, K, 0, dtype, 51)
+    clean, _ = bnd.dora_matmul(**o)
+    for name, i in (("x", M - 1), ("w", 3)):
+        bits = o[name].view(torch.uint8) if dtype == "e4m3" else o[name]
+        bits[i, K - 1] = 0x7F if dtype == "e4m3" else float("nan")
+    y, _ = bnd.dora_matmul(**o)
+    assert torch.isnan(y[M - 1]).all() and torch.isnan(y[:, 3]).all()
+    rows, cols = torch.arange(M - 1), torch.tensor([j for j in range(N) if j != 3])
+    assert torch.equal(y[rows][:, cols], clean[rows][:, cols])
+
+
+def test_offsets_past_32_bits():
+    """Outputs of more than 2^31 elements (forward, element-wise backward, both of its products): the last rows."""
+    rng = np.random.default_rng(61)
+    M, N, K, n = 70001, 33000, 24, 300
+    x, w, c, bias = draw(rng, (M, K), "bf16"), draw(rng, (N, K), "bf16", 0.2), vec(rng, N, 0.2), vec(rng, N, 0.3, 0.0)
+    y, u = bnd.dora_matmul(x, w, col_scale=c, bias=bias, act="silu", save=True)
+    o = dict(x=x[-n:], w=w, col_scale=c, bias=bias)
+    ry, ru = B.matmul(**{k: host(v) for k, v in o.items()}, name="silu")
+    close(u[-n:], ru, rounded("bf16", ru, product_err(o) + 2 * EPS32 * np.abs(ru)), "u")
+    close(y[-n:], ry, rounded("bf16", ry, out_err(o, ru, ry, None, "silu")), "y")
+    # rows of zero gradient but for the last ones: dx and dw are theirs
+    y.zero_()
+    y[-n:] = draw(rng, (n, N), "bf16")
+    got = bnd.dora_matmul_backward(y, u, x, w, col_scale=c, bias=bias, act="silu")
+    assert not got[0][:-n].any() and not got[4][:-n].any()
+    last = (got[0][-n:], got[1], got[2], got[3], got[4][-n:])
+    check_backward(last, y[-n:], u[-n:], x[-n:], w, c, bias, "silu", "bf16")

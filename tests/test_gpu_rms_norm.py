@@ -237,3 +237,38 @@ def test_8_bit_rows_of_infinite_scale():
     v = host(q)
     assert np.isinf(host(scale)).all()
     assert np.isnan(v[:, 7]).all() and (np.delete(v, 7, 1) == 0).all()
+
+
+@pytest.mark.parametrize("down", [60, 88, 100])
+def test_8_bit_rows_of_tiny_values(down):
+    """As above with n near 2^-down, past which the scale stays at 2^-100."""
+    rng = np.random.default_rng(down)
+    T, d, f = 40, 4000, np.float32
+    x = draw(rng, (T, d), "f32")
+    w = torch.from_numpy((rng.random(d) + 0.5).astype(f) * f(2.0 ** -down)).cuda()
+    q, scale, _, rstd = bnd.dora_rms_norm_quant(x, w, 1e-6)
+    n = x.cpu().numpy() * rstd.cpu().numpy()[:, None] * w.cpu().numpy()[None]
+    assert np.array_equal(scale.cpu().numpy(), np.maximum(np.abs(n).max(1) / f(448), f(2.0 ** -100)))
+    want = torch.from_numpy(n / scale.cpu().numpy()[:, None]).to(torch.float8_e4m3fn)
+    assert torch.equal(q.cpu().float(), want.float())
+
+
+def test_offsets_past_32_bits():
+    T, d, n = 270001, 8200, 40
+    rng = np.random.default_rng(12)
+    x, w = torch.zeros(T, d, device="cuda", dtype=torch.bfloat16), vec(rng, d)
+    x[-n:] = draw(rng, (n, d), "bf16")
+    want = bnd.dora_rms_norm_quant(x[-n:].clone(), w, EPS)
+    q, scale, _, rstd = bnd.dora_rms_norm_quant(x, w, EPS)
+    y, _, _ = bnd.dora_rms_norm(x, w, EPS)
+    ref, _, _ = B.rms_norm(host(x[-n:]), None, host(w), EPS)
+    close(y[-n:], ref, rounded("bf16", ref, np.abs(ref) * rel_n(d)), "y")
+    close(scale[-n:], host(want[1]), host(want[1]) * 2 * rel_n(d), "scale")
+    v = ref / host(scale[-n:])[:, None]
+    close(q[-n:], v, np.maximum(np.abs(v) * 2.0 ** -4, 2.0 ** -10) + np.abs(v) * (rel_n(d) + 4 * EPS32), "q")
+    dx, dw = bnd.dora_rms_norm_backward(x, x, rstd, w, dx=y)
+    rdx, rdw = B.rms_norm_backward(host(x[-n:]), host(x[-n:]), host(rstd[-n:]), host(w))
+    close(dx[-n:], rdx, bwd_tol(host(x[-n:]), host(x[-n:]), host(rstd[-n:]), host(w), rdx, None, "bf16"), "dx")
+    a = np.abs(host(x[-n:]))
+    close(dw, rdw, (n + 4) * EPS32 * (a * a * host(rstd[-n:])[:, None]).sum(0) + 1e-30, "dweight")
+    assert not dx[:-n].any()
