@@ -8,12 +8,12 @@
 // first, which are then multiplied by s, so that the adapter costs r more
 // columns of depth and no pass over memory.
 //
-// Measured (MI355X, one box): 8192 x 8192 x 8192 with r = 384 in bf16 879 us,
-// 1.31 PFLOP/s (the vendor's product alone, without r, 679 us); 8192 x 28672 x
-// 8192 in e4m3 1.44 ms, 2.67 PFLOP/s (1.18 ms); 4096^3 110 us (88 us); one
-// token at 8192 x 8192 25 us, 5.6 TB/s (28 us); the backward at 4096^3 252 us,
-// 1.09 PFLOP/s (its two products alone 214 us). On random operands the matrix
-// cores sustain 1.73 PFLOP/s in bf16.
+// Measured (MI355X, one box): 8192 x 8192 x 8192 with r = 384 in bf16 908 us,
+// 1.27 PFLOP/s (the vendor's product alone, without r, 686 us); 8192 x 28672 x
+// 8192 in e4m3 1.48 ms, 2.60 PFLOP/s (1.20 ms); 4096^3 with r = 64 113 us
+// (87 us without); one token at 8192 x 8192 25 us, 5.6 TB/s (29 us); the
+// backward at 4096^3 254 us, 1.08 PFLOP/s (the vendor's two products 219 us).
+// On random operands the matrix cores sustain 1.73 PFLOP/s in bf16.
 #include "dora_device.h"
 #include "dora_launch.h"
 #include "dora_matmul.h"

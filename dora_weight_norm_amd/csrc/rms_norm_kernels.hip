@@ -14,8 +14,8 @@
 // alignment take the same 16-byte loads and stores (gfx950 reads and writes
 // them at any element address); only a row's last partial chunk goes element
 // by element. Rows too long for the registers are read again for each step.
-// Measured: 8192 x 8192 bf16 to 8 bits 79 us, 5.95 TB/s (to bf16 6.05 TB/s);
-// its backward at 8192 x 4096 50 us with the weight's gradient, 5.4 TB/s.
+// Measured: 8192 x 8192 bf16 to 8 bits 79 us, 5.9 TB/s (to bf16 6.05 TB/s);
+// its backward at 8192 x 4096 50 us with the weight's gradient, 5.3 TB/s.
 #include "dora_device.h"
 #include "dora_launch.h"
 
