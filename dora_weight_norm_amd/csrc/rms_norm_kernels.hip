@@ -16,176 +16,12 @@
 // by element. Rows too long for the registers are read again for each step.
 // Measured: 8192 x 8192 bf16 to 8 bits 79 us, 5.9 TB/s (to bf16 6.05 TB/s);
 // its backward at 8192 x 4096 50 us with the weight's gradient, 5.3 TB/s.
-#include "dora_device.h"
 #include "dora_launch.h"
+#include "dora_rows.h"
 
 namespace dora {
 
 namespace {
-
-constexpr float kE4m3Max = 448.f;
-// Inputs of more than this stream past the caches, which they would only
-// empty: measured at 8192 x 8192 bf16 to 8 bits 84 us with ordinary loads and
-// stores, 77.5 us with non-temporal ones; at 777 x 3583, which the caches
-// hold, 8.1 and 8.6 us. Loads only where rows are whole 128-byte lines: two
-// rows share a line otherwise, which was then read twice (5568 x 3000: 27.2 us
-// with both, 22.6 with the stores alone). The backward's loads by the same rule,
-// its stores through the caches (9000 x 1000 bf16: 48.8 us with non-temporal
-// loads, 38.1 without; 2200 x 4100 38.4, 30.0; 5568 x 3000 43.6, 45.0).
-constexpr int64_t kStreamBytes = (int64_t)16 << 20;
-constexpr int64_t kFwdGrid = 1024;   // workgroups of 256 threads, four a compute unit
-// Smallest scale: rows whose largest |n| is below 448 times it (about 2^-91)
-// keep it, so that the reciprocal stays finite.
-constexpr float kMinScale = 0x1p-100f;
-
-typedef u32x4 u32x4_any __attribute__((aligned(1)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_any __attribute__((aligned(1)));
-typedef uint32_t u32_any __attribute__((aligned(1)));
-
-// One 16-byte chunk of a row: elements [k, k + E), zeros past d. STREAM: the
-// rows pass the caches by (see kStreamBytes).
-template <typename T, bool STREAM = false>
-__device__ __forceinline__ u32x4 load_row_chunk(const T* row, int64_t k, int64_t d) {
-  constexpr int E = Elem<T>::epc;
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (k + E <= d) {
-    const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + k);
-    if constexpr (STREAM) return __builtin_nontemporal_load(p);
-    return *p;
-  }
-  if (k < d) {
-    T tmp[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) tmp[e] = (k + e < d) ? row[k + e] : T(0);
-    __builtin_memcpy(&v, tmp, 16);
-  }
-  return v;
-}
-
-template <typename T, bool STREAM = false>
-__device__ __forceinline__ void store_row_chunk(T* row, int64_t k, int64_t d, const float (&f)[Elem<T>::epc]) {
-  constexpr int E = Elem<T>::epc;
-  if (k + E <= d) {
-    if constexpr (STREAM)
-      __builtin_nontemporal_store(pack<T, E>(f), reinterpret_cast<u32x4_any*>(row + k));
-    else
-      *reinterpret_cast<u32x4_any*>(row + k) = pack<T, E>(f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (k + e < d) row[k + e] = from_f32<T>(f[e]);
-  }
-}
-
-// E fp32 values to e4m3 (OCP, round to nearest even), four to a word.
-template <int E, bool STREAM = false>
-__device__ __forceinline__ void store_row_q(uint8_t* row, int64_t k, int64_t d, const float (&f)[E]) {
-  uint32_t w[E / 4];
-#pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], 0, false);
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], v, true);
-    w[i] = (uint32_t)v;
-  }
-  if (k + E <= d) {
-    if constexpr (E == 8) {
-      const u32x2 p = {w[0], w[1]};
-      if constexpr (STREAM)
-        __builtin_nontemporal_store(p, reinterpret_cast<u32x2_any*>(row + k));
-      else
-        *reinterpret_cast<u32x2_any*>(row + k) = p;
-    } else {
-      *reinterpret_cast<u32_any*>(row + k) = w[0];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (k + e < d) row[k + e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
-  }
-}
-
-// E weights (fp32) of a chunk; ones where there are none, zeros past d.
-template <int E>
-__device__ __forceinline__ void load_weight(const float* w, int64_t k, int64_t d, float (&f)[E]) {
-  if (w == nullptr) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = 1.f;
-  } else if (k + E <= d) {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const u32x4 v = *reinterpret_cast<const u32x4_any*>(w + k + 4 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[4 * i + e] = __uint_as_float(v[e]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = (k + e < d) ? w[k + e] : 0.f;
-  }
-}
-
-// Sum over the NT threads that share a row, in a fixed order: inside each
-// wave by lane exchanges, then over the waves in increasing order. `slot`
-// names the LDS words used, a different one for each call before a barrier.
-template <int NT>
-__device__ __forceinline__ float row_sum(float v, float* lds) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) v += lds[i];
-  }
-  return v;
-}
-
-// Largest |value| over the row, carried as its bits: among non-negative
-// floats the order of the bits is the order of the values, and a NaN's bits
-// are above infinity's, so a NaN anywhere comes out as a NaN.
-template <int NT>
-__device__ __forceinline__ uint32_t row_max_bits(uint32_t v, uint32_t* lds) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)v, m, 64);
-    v = o > v ? o : v;
-  }
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) v = lds[i] > v ? lds[i] : v;
-  }
-  return v;
-}
-
-__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
-
-// scale = top / 448: 1 for a row of zeros, at least kMinScale otherwise; NaN
-// or infinite where top is.
-__device__ __forceinline__ float scale_of(uint32_t top_bits) {
-  const float top = __uint_as_float(top_bits);
-  const float s = top / kE4m3Max;
-  return top_bits == 0 ? 1.f : (s < kMinScale ? kMinScale : s);
-}
-
-// The quotient n / scale, correctly rounded in fp32 without a division a value:
-// n times the rounded reciprocal is within a step of it, and adding the exact
-// remainder times the reciprocal gives the nearest value (Markstein 1990). The
-// product alone put values beside the border of two 8-bit steps on the wrong
-// side of it; the two operations more cost 0.7 us of 78 at 8192 x 8192. An
-// infinite scale leaves 0 (NaN where n is infinite), as the division does.
-struct RowQuotient {
-  float inv, s;
-  __device__ __forceinline__ explicit RowQuotient(float scale)
-      : inv(1.f / scale), s(scale <= 3.402823466e38f ? scale : 0.f) {}
-  __device__ __forceinline__ float operator()(float n) const {
-    const float q = n * inv;
-    return fmaf(fmaf(-q, s, n), inv, q);
-  }
-};
 
 struct NormArgs {
   const void* x;
@@ -546,55 +382,6 @@ __global__ __launch_bounds__(kSumCols* kSumSplit) void column_sum_kernel(const f
   } else if (out1) {
     out1[j - n0] = acc;
   }
-}
-
-// Threads and chunks a thread that hold a row of d elements; nt 0: too long.
-struct RowShape {
-  int nt, c;
-};
-
-// Forward. Many short rows take a wave each (no barrier; 5568 x 1000: 10.8 us,
-// 15.9 with 256 threads a row), up to two chunks a thread; other rows take 256
-// threads (5568 x 1456: 16.8 us, 19.2 with a wave of four chunks a thread), 512 past two chunks a thread (four of 8192 bf16 elements ran
-// two workgroups a compute unit for their registers: 80 against 77.5 us), or
-// 1024 where there are too few rows to fill the chip. Rows of up to 16384 elements stay in registers
-// (1024 threads have 128 registers each: two 16-bit chunks or four fp32).
-RowShape forward_shape(int64_t T, int64_t d, int epc) {
-  const int64_t ch = (d + epc - 1) / epc;
-  auto fit = [&](int nt) {
-    const int64_t c = (ch + nt - 1) / nt;
-    return (int)(c <= 1 ? 1 : (c <= 2 ? 2 : (c <= 4 ? 4 : (c <= 8 ? 8 : 0))));
-  };
-  if (ch <= 128 && (T >= 512 || ch <= 64)) return RowShape{64, fit(64)};
-  if (ch <= 512 && (T >= 512 || ch <= 256)) return RowShape{256, fit(256)};
-  if (ch <= 2048 && T >= 512) return RowShape{512, fit(512)};
-  return ch <= (epc == 8 ? 2048 : 4096) ? RowShape{1024, fit(1024)} : RowShape{0, 0};
-}
-
-// Backward: workgroups of 64 to 512 threads, at most four chunks a thread
-// (weights and sums are held beside them).
-RowShape backward_shape(int64_t d, int epc) {
-  const int64_t ch = (d + epc - 1) / epc;
-  if (ch <= 64) return RowShape{64, 1};
-  if (ch <= 256) return RowShape{256, 1};
-  if (ch <= 512) return RowShape{256, 2};
-  if (ch <= 1024) return RowShape{512, 2};
-  return ch <= 2048 ? RowShape{512, 4} : RowShape{0, 0};
-}
-
-// Workgroups of the backward: enough waves to fill the chip (256 compute
-// units), few enough that the dweight partials stay small beside the rows.
-int64_t backward_grid(int64_t T, int64_t d, int epc) {
-  const RowShape r = backward_shape(d, epc);
-  const int64_t g = r.nt == 64 ? 2048 : (r.nt == 256 ? 512 : 256);
-  return T < g ? T : g;
-}
-
-// Workgroups of the forward: one a row (or four rows), up to what the chip
-// holds at once; past that each takes several rows.
-unsigned grid_of(int64_t n, int nt) {
-  const int64_t most = nt == 1024 ? 512 : kFwdGrid;
-  return (unsigned)(n < most ? n : most);
 }
 
 template <typename T>
