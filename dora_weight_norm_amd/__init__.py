@@ -18,6 +18,14 @@ __all__ = [
     "dora_rms_norm_backward",
     "dora_matmul",
     "dora_matmul_backward",
+    "Int8Rows",
+    "dora_layer_norm",
+    "dora_layer_norm_quant",
+    "dora_layer_norm_backward",
+    "dora_quantize_rows",
+    "dora_dequantize_rows",
+    "dora_matmul_int8",
+    "dora_matmul_backward_int8",
 ]
 
 

@@ -15,6 +15,7 @@ import contextlib
 import ctypes
 import functools
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -52,6 +53,19 @@ __all__ = [
     "dora_matmul_plan_info",
     "dora_matmul_backward",
     "dora_matmul_backward_workspace_size",
+    "DORA_I8",
+    "Int8Rows",
+    "dora_layer_norm",
+    "dora_layer_norm_quant",
+    "dora_layer_norm_backward",
+    "dora_layer_norm_backward_workspace_size",
+    "dora_quantize_rows",
+    "dora_dequantize_rows",
+    "dora_matmul_int8",
+    "dora_matmul_int8_workspace_size",
+    "dora_matmul_int8_plan_info",
+    "dora_matmul_backward_int8",
+    "dora_matmul_backward_int8_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdora.so")
@@ -59,7 +73,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdora.so"
 DORA_BF16 = 0
 DORA_F32 = 1
 DORA_F16 = 2
-DORA_E4M3 = 3   # 8-bit operands of dora_matmul only
+DORA_E4M3 = 3   # 8-bit operands of dora_matmul and 8-bit outputs of the norms
+DORA_I8 = 4     # 8-bit integers, where an output's 8-bit type is chosen
 DEFAULT_BUDGET = 256 << 20
 NOALLOC_SCRATCH_BYTES = 32 << 20   # DORA_NOALLOC_SCRATCH_BYTES
 
@@ -129,6 +144,21 @@ def load():
                                         _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
         "dora_matmul_backward_rows": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p,
                                              _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+        "dora_layer_norm": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_f, _c_i, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i, _c_p,
+                                   _c_p, _c_p, _c_p]),
+        "dora_layer_norm_backward_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i, ctypes.POINTER(_c_sz)]),
+        "dora_layer_norm_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_p, _c_p, _c_p,
+                                            _c_p, _c_sz, _c_p]),
+        "dora_quantize_rows": (_c_i, [_c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+        "dora_dequantize_rows": (_c_i, [_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i, _c_p, _c_p]),
+        "dora_matmul_int8_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i, ctypes.POINTER(_c_sz)]),
+        "dora_matmul_int8_plan_info": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i, ctypes.POINTER(_c_i64), _c_i]),
+        "dora_matmul_int8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_f,
+                                    _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+        "dora_matmul_backward_int8_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, _c_i,
+                                                            ctypes.POINTER(_c_sz)]),
+        "dora_matmul_backward_int8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64,
+                                             _c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -759,4 +789,262 @@ def dora_matmul_backward(dy, u, x, w, col_scale=None, bias=None, act: str = "non
     _call_on(dev, "dora_matmul_backward_rows", dy.data_ptr(), pu, _addr(x) if need_dw else None,
              _addr(w) if need_dx else None, code, M, N, K, prow, pcol, pbias, act_code, _addr(du), _addr(dx),
              _addr(dw), _addr(dbias), _addr(dcol), _addr(workspace), need, _raw_stream(stream, dev))
+    return dx, dw, dbias, dcol, du
+
+
+# ---------------------------------------------------------------------------
+# Rows held in 8-bit integers: the layer norm that writes them, packing, the
+# integer product, and the backward that reads them as checkpoints.
+# ---------------------------------------------------------------------------
+class Int8Rows(NamedTuple):
+    """Rows in 8-bit integers: q int8 [T, d]; scale float32 [T] with group 0, else [T, ceil(d / group)]."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    group: int = 0
+
+
+class _Int8RowsArg(ctypes.Structure):
+    _fields_ = [("q", _c_p), ("scale", _c_p), ("group", _c_i64)]
+
+
+_Q8_CODE = {torch.int8: DORA_I8, _E4M3: DORA_E4M3}
+GROUPS = (0, 32, 64, 128, 256)
+HELD_X, HELD_W = 1, 2   # DORA_HELD_*
+
+
+def _scale_shape(T: int, d: int, group: int) -> tuple:
+    if group not in GROUPS:
+        raise ValueError(f"group must be one of {GROUPS}, got {group!r}")
+    return (T, -(-d // group)) if group else (T,)
+
+
+def dora_layer_norm_backward_workspace_size(T: int, d: int, dtype) -> int:
+    return _size_of("dora_layer_norm_backward_workspace_size", T, d, _dtype_code(dtype))
+
+
+def dora_matmul_int8_workspace_size(M: int, N: int, K: int, r: int, aligned_operands: int = 15) -> int:
+    return _size_of("dora_matmul_int8_workspace_size", M, N, K, r, aligned_operands)
+
+
+def dora_matmul_int8_plan_info(M: int, N: int, K: int, r: int, aligned_operands: int = 15) -> dict:
+    buf = (_c_i64 * 5)()
+    _call("dora_matmul_int8_plan_info", M, N, K, r, aligned_operands, buf, 5)
+    return dict(zip(("tile_rows", "splits", "copies", "workspace_bytes", "few_rows"), list(buf)))
+
+
+def dora_matmul_backward_int8_workspace_size(M: int, N: int, K: int, dtype, outputs: int = 31, held: int = 3) -> int:
+    """`outputs`: the sum of the GRAD_ constants that apply; `held`: of the HELD_ ones."""
+    return _size_of("dora_matmul_backward_int8_workspace_size", M, N, K, _dtype_code(dtype), outputs, held)
+
+
+def _layer_norm(x, weight, bias, eps, residual, h, mean, rstd, want_stats, stream, y=None, q=None, scale=None,
+                q_dtype=None, want_y=True):
+    dev, dtype, shape = _first(x, "x"), x.dtype, x.shape
+    code = _type_code(dtype)
+    T, d = shape
+    f32 = torch.float32
+    ph = py = pq = ps = None
+    pw, pb = _maybe(weight, "weight", (d,), f32, dev), _maybe(bias, "bias", (d,), f32, dev)
+    pres = _maybe(residual, "residual", shape, dtype, dev)
+    if residual is not None:
+        h = _new(stream, shape, dtype, dev) if h is None else h
+        ph = _want(h, "h", shape, dtype, dev)
+    elif h is not None:
+        raise ValueError("h needs a residual (without one, h is x)")
+    if want_stats:
+        mean = _new(stream, (T,), f32, dev) if mean is None else mean
+        rstd = _new(stream, (T,), f32, dev) if rstd is None else rstd
+    pm, prs = _maybe(mean, "mean", (T,), f32, dev), _maybe(rstd, "rstd", (T,), f32, dev)
+    if q_dtype is not None:
+        if q_dtype not in _Q8_CODE:
+            raise TypeError(f"q_dtype must be int8 or float8_e4m3fn, got {q_dtype}")
+        q = _new(stream, shape, q_dtype, dev) if q is None else q
+        scale = _new(stream, (T,), f32, dev) if scale is None else scale
+        pq, ps = _want(q, "q", shape, q_dtype, dev), _want(scale, "scale", (T,), f32, dev)
+    if y is None and want_y:
+        y = _new(stream, shape, dtype, dev)
+    py = _maybe(y, "y", shape, dtype, dev)
+    _call_on(dev, "dora_layer_norm", x.data_ptr(), pres, pw, pb, eps, code, T, d, ph, py, pq, _Q8_CODE.get(q_dtype, 0),
+             ps, pm, prs, _raw_stream(stream, dev))
+    return y, q, scale, (x if residual is None else h), mean, rstd
+
+
+def dora_layer_norm(x, weight, bias, eps: float, residual=None, y=None, h=None, mean=None, rstd=None,
+                    want_stats: bool = True, stream=None):
+    """y = (h - mean) * rstd * weight + bias with h = x + residual, over each row.
+
+    x, residual [T, d] of one dtype (bfloat16, float16 or float32), weight and
+    bias float32 [d] or None. Returns (y, h, mean, rstd): h is x itself without
+    a residual; mean and rstd float32 [T] (None with want_stats False).
+    """
+    y, _, _, h, mean, rstd = _layer_norm(x, weight, bias, eps, residual, h, mean, rstd, want_stats, stream, y=y)
+    return y, h, mean, rstd
+
+
+def dora_layer_norm_quant(x, weight, bias, eps: float, q_dtype=torch.int8, residual=None, q=None, scale=None, h=None,
+                          mean=None, rstd=None, want_stats: bool = True, y=None, stream=None):
+    """dora_layer_norm with its output in 8 bits: q [T, d] of q_dtype (int8 or
+    float8_e4m3fn) and scale float32 [T], the row's largest |value| / 127 or / 448.
+    Returns (q, scale, h, mean, rstd). y, if a buffer for it is given, receives
+    the output in x's dtype as well."""
+    _, q, scale, h, mean, rstd = _layer_norm(x, weight, bias, eps, residual, h, mean, rstd, want_stats, stream, y=y,
+                                             q=q, scale=scale, q_dtype=q_dtype, want_y=False)
+    return q, scale, h, mean, rstd
+
+
+def dora_layer_norm_backward(dy, h, mean, rstd, weight, dh=None, need_dweight: bool = True, need_dbias: bool = True,
+                             dx=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """Gradients of dora_layer_norm from its h, mean and rstd. Returns (dx,
+    dweight, dbias): dx is the gradient of x and of the residual, dh (optional)
+    what reaches h directly is added to it; dweight and dbias float32 [d], None
+    where not needed."""
+    dev, dtype, shape = _first(dy, "dy"), dy.dtype, dy.shape
+    code = _type_code(dtype)
+    T, d = shape
+    f32 = torch.float32
+    ph = _want(h, "h", shape, dtype, dev)
+    pm, prs = _want(mean, "mean", (T,), f32, dev), _want(rstd, "rstd", (T,), f32, dev)
+    pw, pdh = _maybe(weight, "weight", (d,), f32, dev), _maybe(dh, "dh", shape, dtype, dev)
+    if dweight is not None and not need_dweight or dbias is not None and not need_dbias:
+        raise ValueError("a gradient's buffer is given but the gradient is not needed")
+    need = dora_layer_norm_backward_workspace_size(T, d, code) if need_dweight or need_dbias else 0
+    dx = _new(stream, shape, dtype, dev) if dx is None else dx
+    dweight = _new(stream, (d,), f32, dev) if need_dweight and dweight is None else dweight
+    dbias = _new(stream, (d,), f32, dev) if need_dbias and dbias is None else dbias
+    pdx = _want(dx, "dx", shape, dtype, dev)
+    pdw, pdb = _maybe(dweight, "dweight", (d,), f32, dev), _maybe(dbias, "dbias", (d,), f32, dev)
+    workspace = _space(workspace, need, stream, dev)
+    _call_on(dev, "dora_layer_norm_backward", dy.data_ptr(), pdh, ph, pm, prs, pw, code, T, d, pdx, pdw, pdb,
+             _addr(workspace), need, _raw_stream(stream, dev))
+    return dx, dweight, dbias
+
+
+def dora_quantize_rows(x, group: int = 0, q=None, scale=None, stream=None):
+    """x [T, d] as int8 rows: (q int8 [T, d], scale float32), scale = max |x| / 127
+    over a row ([T], group 0) or over each group of 32, 64, 128 or 256 columns of
+    it ([T, ceil(d / group)]), and q = x / scale to the nearest integer."""
+    dev, shape = _first(x, "x"), x.shape
+    code = _type_code(x.dtype)
+    T, d = shape
+    scales = _scale_shape(T, d, group)
+    q = _new(stream, shape, torch.int8, dev) if q is None else q
+    scale = _new(stream, scales, torch.float32, dev) if scale is None else scale
+    pq, ps = _want(q, "q", shape, torch.int8, dev), _want(scale, "scale", scales, torch.float32, dev)
+    _call_on(dev, "dora_quantize_rows", x.data_ptr(), code, T, d, group, pq, ps, _raw_stream(stream, dev))
+    return q, scale
+
+
+def dora_dequantize_rows(q, scale, group: int = 0, dtype=torch.bfloat16, out=None, stream=None):
+    """The values q * scale that int8 rows stand for, [T, d] rounded once to `dtype` (bfloat16, float16 or float32)."""
+    dev, shape = _first(q, "q"), q.shape
+    T, d = shape
+    pq = _want(q, "q", shape, torch.int8, dev)
+    ps = _want(scale, "scale", _scale_shape(T, d, group), torch.float32, dev)
+    code = _type_code(dtype)
+    out = _new(stream, shape, dtype, dev) if out is None else out
+    po = _want(out, "out", shape, dtype, dev)
+    _call_on(dev, "dora_dequantize_rows", pq, ps, T, d, group, code, po, _raw_stream(stream, dev))
+    return out
+
+
+def dora_matmul_int8(x, w, row_scale, w_scale, col_scale=None, t=None, b=None, s: float = 1.0, bias=None,
+                     act: str = "none", residual=None, out_dtype=torch.bfloat16, save: bool = False, y=None, u=None,
+                     workspace=None, stream=None):
+    """y = act(col_scale * u + bias) + residual with u = row_scale * w_scale * (x w^T) + s * t b^T.
+
+    x int8 [M, K] with row_scale float32 [M] and w int8 [N, K] with w_scale
+    float32 [N] are int8 rows with one scale a row; t [M, r] and b [N, r] of
+    out_dtype, both or neither (neither with float32); col_scale, bias float32
+    [N]; residual [M, N] of out_dtype. Returns (y, u); u, the product that the
+    backward takes, is None unless `save` (or a buffer for it) is given.
+    """
+    dev = _first(x, "x")
+    M, K = x.shape
+    _first(w, "w")
+    N = w.shape[0]
+    i8, f32 = torch.int8, torch.float32
+    px, pw = _want(x, "x", (M, K), i8, dev), _want(w, "w", (N, K), i8, dev)
+    prow, pws = _want(row_scale, "row_scale", (M,), f32, dev), _want(w_scale, "w_scale", (N,), f32, dev)
+    out_code = _type_code(out_dtype)
+    r, pt, pb = 0, None, None
+    al = ((px & 15) == 0) | ((pw & 15) == 0) << 1
+    if t is not None or b is not None:
+        if t is None or b is None:
+            raise ValueError("t and b come together")
+        if out_dtype is f32:
+            raise TypeError("a low-rank pair does not go with float32 outputs of the integer product")
+        _first(t, "t")
+        r = t.shape[1]
+        pt, pb = _want(t, "t", (M, r), out_dtype, dev), _want(b, "b", (N, r), out_dtype, dev)
+        al |= ((pt & 15) == 0) << 2 | ((pb & 15) == 0) << 3
+    out = (M, N)
+    pcol, pbias = _maybe(col_scale, "col_scale", (N,), f32, dev), _maybe(bias, "bias", (N,), f32, dev)
+    pres = _maybe(residual, "residual", out, out_dtype, dev)
+    act_code = _act(act)
+    need = _size_of("dora_matmul_int8_workspace_size", M, N, K, r, al)
+    y = _new(stream, out, out_dtype, dev) if y is None else y
+    if u is None and save:
+        u = _new(stream, out, out_dtype, dev)
+    py, pu = _want(y, "y", out, out_dtype, dev), _maybe(u, "u", out, out_dtype, dev)
+    workspace = _space(workspace, need, stream, dev)
+    _call_on(dev, "dora_matmul_int8", px, prow, pw, pws, M, N, K, pcol, pt, pb, r, s, pbias, act_code, pres, out_code,
+             py, pu, _addr(workspace), need, _raw_stream(stream, dev))
+    return y, u
+
+
+def _held(v, name: str, shape, dtype, dev: int):
+    """(address, structure) of an operand in the storage type or as Int8Rows; the other one is None."""
+    if not isinstance(v, Int8Rows):
+        return _want(v, name, shape, dtype, dev), None
+    pq = _want(v.q, f"{name}.q", shape, torch.int8, dev)
+    ps = _want(v.scale, f"{name}.scale", _scale_shape(*shape, v.group), torch.float32, dev)
+    return None, _Int8RowsArg(pq, ps, v.group)
+
+
+def dora_matmul_backward_int8(dy, u, x, w, col_scale=None, bias=None, act: str = "none", need_dx: bool = True,
+                              need_dw: bool = True, need_dbias: bool = True, need_dcol_scale: bool = True,
+                              workspace=None, stream=None, row_scale=None):
+    """dora_matmul_backward with any of u, x and w given as Int8Rows.
+
+    u and x are activations packed in the forward (dora_quantize_rows), w a
+    frozen 8-bit base. u's values are taken in fp32, x's and w's as operands of
+    dy's dtype. Arguments and results otherwise as there: (dx, dw, dbias,
+    dcol_scale, du).
+    """
+    dev, dtype = _first(dy, "dy"), dy.dtype
+    code = _type_code(dtype)
+    M, N = out = dy.shape
+    if need_dx and w is None or need_dw and x is None:
+        raise ValueError("dx needs w, and dw needs x")
+    K = 0
+    for v, name in ((w, "w"), (x, "x")):
+        if v is not None:
+            v = v.q if isinstance(v, Int8Rows) else v
+            _first(v, name)
+            K = v.shape[1]
+    pu, u8 = _held(u, "u", out, dtype, dev)
+    px, x8 = (None, None) if x is None else _held(x, "x", (M, K), dtype, dev)
+    pw, w8 = (None, None) if w is None else _held(w, "w", (N, K), dtype, dev)
+    f32 = torch.float32
+    pcol, pbias = _maybe(col_scale, "col_scale", (N,), f32, dev), _maybe(bias, "bias", (N,), f32, dev)
+    prow = _maybe(row_scale, "row_scale", (M,), f32, dev)
+    act_code = _act(act)
+    du = _new(stream, out, dtype, dev)
+    dx = _new(stream, (M, K), dtype, dev) if need_dx else None
+    dw = _new(stream, (N, K), dtype, dev) if need_dw else None
+    dbias = _new(stream, (N,), f32, dev) if need_dbias else None
+    dcol = _new(stream, (N,), f32, dev) if need_dcol_scale else None
+    if not need_dx:
+        pw = w8 = None
+    if not need_dw:
+        px = x8 = None
+    outputs = (GRAD_DX * need_dx + GRAD_DW * need_dw + GRAD_SUMS * (need_dbias or need_dcol_scale)
+               + GRAD_DU * (du.data_ptr() % 16 == 0) + GRAD_ALIGNED * ((px or 0) % 16 == 0 and (pw or 0) % 16 == 0))
+    held = HELD_X * (x8 is not None) + HELD_W * (w8 is not None)
+    need = _size_of("dora_matmul_backward_int8_workspace_size", M, N, K, code, outputs, held)
+    workspace = _space(workspace, need, stream, dev)
+    ref = [None if v is None else ctypes.byref(v) for v in (u8, x8, w8)]
+    _call_on(dev, "dora_matmul_backward_int8", dy.data_ptr(), pu, ref[0], px, ref[1], pw, ref[2], code, M, N, K, prow,
+             pcol, pbias, act_code, _addr(du), _addr(dx), _addr(dw), _addr(dbias), _addr(dcol), _addr(workspace), need,
+             _raw_stream(stream, dev))
     return dx, dw, dbias, dcol, du

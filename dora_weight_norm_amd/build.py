@@ -25,7 +25,8 @@ RESOURCE_REPORT = os.path.join(BUILD_DIR, "kernel_resources.txt")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["dora_api.hip", "block_api.hip", "norm_kernels.hip", "compose_kernels.hip", "rms_norm_kernels.hip",
-           "matmul_kernels.hip"]
+           "matmul_kernels.hip", "layer_norm_kernels.hip", "int8_rows_kernels.hip", "int8_matmul_kernels.hip",
+           "int8_api.hip"]
 
 COMMON_FLAGS = [
     "--offload-arch=gfx950",

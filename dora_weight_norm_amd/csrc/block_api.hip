@@ -1,86 +1,12 @@
 // C ABI of the block around the adapted layer: the residual RMS norm and the
 // matrix product with its epilogue, and their backward passes. Argument
 // checks run on the host before anything is enqueued.
-#include <math.h>
-
 #include "../../include/dora.h"
-#include "dora_check.h"
+#include "block_check.h"
 #include "dora_launch.h"
 #include "dora_matmul.h"
 
-using dora::aligned;
-using dora::esize;
-using dora::hip_status;
-using dora::kAlign;
-using dora::kMaxDim;
-using dora::overlap;
-using dora::valid_dtype;
-
-namespace {
-
-// One buffer of a call: its bytes, and the alignment its elements need.
-struct Span {
-  const void* p;
-  int64_t bytes;
-  size_t align;
-};
-
-// Every element of a tensor is reached with 64-bit arithmetic far from its
-// limits, and every launch stays within its grid.
-constexpr int64_t kMaxElems = (int64_t)1 << 33;
-// Bytes of one row of a product's operand (the tile kernel's 32-bit offsets
-// span 256 rows).
-constexpr int64_t kMaxRowBytes = (int64_t)1 << 23;
-// Rows of a product: 64 of them a workgroup of 256 threads, and a launch takes
-// less than 2^32 threads.
-constexpr int64_t kMaxRows = (int64_t)1 << 30;
-
-bool size_ok(int64_t a, int64_t b) {
-  return a >= 0 && b >= 0 && a < kMaxDim && b < kMaxDim && (b == 0 || a <= kMaxElems / b);
-}
-
-// Inputs and outputs are aligned; no output overlaps an input or another
-// output, except input i that output o may be exactly (bit i of same[o]).
-bool buffers_ok(const Span* in, int n_in, const Span* out, int n_out, const unsigned* same) {
-  for (int i = 0; i < n_in; ++i)
-    if (!aligned(in[i].p, in[i].align)) return false;
-  for (int o = 0; o < n_out; ++o) {
-    if (!aligned(out[o].p, out[o].align)) return false;
-    for (int i = 0; i < n_in; ++i) {
-      if ((same[o] >> i & 1u) && out[o].p == in[i].p) continue;
-      if (overlap(out[o].p, out[o].bytes, in[i].p, in[i].bytes)) return false;
-    }
-    for (int q = o + 1; q < n_out; ++q)
-      if (overlap(out[o].p, out[o].bytes, out[q].p, out[q].bytes)) return false;
-  }
-  return true;
-}
-
-dora_status workspace_ok(const void* ws, size_t have, size_t need, const Span* in, int n_in, const Span* out,
-                         int n_out) {
-  if (need == 0) return DORA_OK;
-  if (have < need || ws == nullptr || !aligned(ws, kAlign)) return DORA_ERR_WORKSPACE;
-  for (int i = 0; i < n_in; ++i)
-    if (overlap(ws, (int64_t)need, in[i].p, in[i].bytes)) return DORA_ERR_INVALID_ARG;
-  for (int o = 0; o < n_out; ++o)
-    if (overlap(ws, (int64_t)need, out[o].p, out[o].bytes)) return DORA_ERR_INVALID_ARG;
-  return DORA_OK;
-}
-
-bool valid_act(int act) { return act >= DORA_ACT_NONE && act <= DORA_ACT_SILU; }
-int64_t operand_size(int dt) { return dt == DORA_E4M3 ? 1 : esize(dt); }
-
-bool matmul_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t r, int64_t es) {
-  return size_ok(M, K) && size_ok(N, K) && size_ok(M, N) && size_ok(M, r) && size_ok(N, r) &&
-         M < kMaxRows && K * es < kMaxRowBytes && r * es < kMaxRowBytes && N < kMaxRowBytes;
-}
-
-// The backward's products run along M and N too.
-bool backward_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t es) {
-  return matmul_sizes_ok(M, N, K, 0, es) && M * es < kMaxRowBytes && N * es < kMaxRowBytes;
-}
-
-}  // namespace
+using namespace dora;
 
 extern "C" {
 
@@ -143,11 +69,7 @@ dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, in
   if (info == nullptr || n_info < 0 || !matmul_sizes_ok(M, N, K, r, operand_size(dtype))) return DORA_ERR_INVALID_ARG;
   const dora::MatmulPlan p = M > 0 && N > 0 ? dora::plan_matmul(M, N, K, r, dtype, aligned_operands)
                                             : dora::MatmulPlan{};
-  const int rows = p.cfg == dora::kTile256 ? 256 : (p.cfg == dora::kTile128 ? 128 : (p.cfg == dora::kTile64 ? 64 : 0));
-  const int copies = (p.pack_x ? 1 : 0) | (p.pack_w ? 2 : 0) | (p.pack_t ? 4 : 0) | (p.pack_b ? 8 : 0);
-  const int few = p.cfg == dora::kFew8 ? 8 : (p.cfg == dora::kFew16 ? 16 : (p.cfg == dora::kFew32 ? 32 : -1));
-  const int64_t vals[] = {M > 0 && N > 0 ? rows : -1, p.splits, copies, (int64_t)p.ws_bytes, few};
-  for (int i = 0; i < n_info; ++i) info[i] = i < 5 ? vals[i] : -1;
+  plan_fields(p, M > 0 && N > 0, info, n_info);
   return DORA_OK;
 }
 
@@ -175,7 +97,7 @@ dora_status dora_matmul(const void* x, const void* w, int dtype, int64_t M, int6
   const dora_status st = workspace_ok(workspace, workspace_bytes, p.ws_bytes, in, 8, out, 2);
   if (st != DORA_OK) return st;
   const dora::Epilogue ep{row_scale, col_scale, bias, residual, y, u, act};
-  return hip_status(dora::launch_matmul(p, x, w, dtype, M, N, K, t, b, r, s, ep, out_dtype,
+  return hip_status(dora::launch_matmul(p, x, w, dtype, M, N, K, t, b, r, s, ep, nullptr, out_dtype,
                                         static_cast<char*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
@@ -186,7 +108,8 @@ dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K,
       !backward_sizes_ok(M, N, K, esize(dtype)))
     return DORA_ERR_INVALID_ARG;
   *ws_bytes = dora::plan_matmul_backward(M, N, K, dtype, outputs & DORA_GRAD_DX, outputs & DORA_GRAD_DW,
-                                         outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU, outputs & DORA_GRAD_ALIGNED)
+                                         outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU, outputs & DORA_GRAD_ALIGNED,
+                                         false, false)
                   .ws_bytes;
   return DORA_OK;
 }
@@ -220,11 +143,11 @@ dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void*
   const dora::MatmulBackwardPlan p =
       dora::plan_matmul_backward(M, N, K, dtype, dx != nullptr, dw != nullptr, dbias != nullptr || dcol_scale != nullptr,
                                  du != nullptr && aligned(du, 16),
-                                 (dw == nullptr || aligned(x, 16)) && (dx == nullptr || aligned(w, 16)));
+                                 (dw == nullptr || aligned(x, 16)) && (dx == nullptr || aligned(w, 16)), false, false);
   const dora_status st = workspace_ok(workspace, workspace_bytes, p.ws_bytes, in, 7, out, 5);
   if (st != DORA_OK) return st;
   return hip_status(dora::launch_matmul_backward(p, dy, u, x, w, dtype, M, N, K, row_scale, col_scale, bias, act, du,
-                                                 dx, dw, dbias, dcol_scale, static_cast<char*>(workspace),
+                                                 dx, dw, dbias, dcol_scale, dora::HeldInt8{}, static_cast<char*>(workspace),
                                                  static_cast<hipStream_t>(stream)));
 }
 

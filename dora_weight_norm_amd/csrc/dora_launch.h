@@ -43,6 +43,32 @@ hipError_t launch_rms_norm(const void* x, const void* residual, const float* wei
 size_t rms_norm_bwd_workspace_bytes(int64_t T, int64_t d, int dtype);
 hipError_t launch_rms_norm_bwd(const void* dy, const void* dh, const void* h, const float* rstd, const float* weight,
                                int dtype, int64_t T, int64_t d, void* dx, float* dweight, void* ws, hipStream_t st);
+// Rows in 8-bit integers: q [rows][d] and the scales of each row's groups of
+// `group` columns (0: one scale a row).
+struct Int8Rows {
+  const uint8_t* q;
+  const float* scale;
+  int64_t group;
+};
+// Scales of a row, and log2 of a group's columns (62 where the row is one).
+inline int64_t scales_of(int64_t d, int64_t group) { return group ? (d + group - 1) / group : 1; }
+inline int group_shift(int64_t group) {
+  int s = 0;
+  while (group && ((int64_t)1 << s) < group) ++s;
+  return group ? s : 62;
+}
+hipError_t launch_layer_norm(const void* x, const void* residual, const float* weight, const float* bias, float eps,
+                             int dtype, int64_t T, int64_t d, void* h, void* y, void* q, int q_int8, float* scale,
+                             float* mean, float* rstd, hipStream_t st);
+size_t layer_norm_bwd_workspace_bytes(int64_t T, int64_t d, int dtype);
+hipError_t launch_layer_norm_bwd(const void* dy, const void* dh, const void* h, const float* mean, const float* rstd,
+                                 const float* weight, int dtype, int64_t T, int64_t d, void* dx, float* dweight,
+                                 float* dbias, void* ws, hipStream_t st);
+hipError_t launch_quantize_rows(const void* x, int dtype, int64_t T, int64_t d, int64_t group, void* q, float* scale,
+                                hipStream_t st);
+// x [T][d] at a row stride of ld elements (zeros from d on, up to a whole chunk).
+hipError_t launch_dequantize_rows(const Int8Rows& r, int64_t T, int64_t d, int64_t ld, int dtype, void* x,
+                                  hipStream_t st);
 size_t fast_kernel_lds_bytes(int cfg);
 size_t gen_kernel_lds_bytes(int cfg);
 

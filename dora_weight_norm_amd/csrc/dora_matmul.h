@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "dora_launch.h"
+
 namespace dora {
 
 // What follows the product, per element:
@@ -36,6 +38,11 @@ struct GemmArgs {
   int stages;              // stages of the whole depth
   int stages_per_split;
   float* part;             // [splits][M][N] fp32 partial sums (splits > 1)
+  // 8-bit integers: the columns' scales; with a pair also the rows' (the
+  // epilogue's otherwise) and 1 / s.
+  const float* w_scale;
+  const float* pair_rows;
+  float inv_s;
   Epilogue ep;
 };
 
@@ -52,7 +59,12 @@ struct MatmulPlan {
   size_t ws_bytes;
 };
 
-// The product's plan; `al` is a bit mask of the operands whose pointers are
+// Operand type of the products in 8-bit integers, beside the C ABI's codes.
+constexpr int kInt8Operands = 4;
+hipError_t gemm_int8(const GemmArgs& g, int out_dtype, int cfg, hipStream_t st);
+
+// The product's plan (dtype: a C ABI code or kInt8Operands, whose t and b are of
+// 16 bits); `al` is a bit mask of the operands whose pointers are
 // 16-byte aligned (1 x, 2 w, 4 t, 8 b).
 MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, int al);
 
@@ -60,21 +72,27 @@ struct MatmulBackwardPlan {
   bool du_direct;                               // du is written into the caller's array alone
   bool direct;                                  // the products read x, w and du in their own layout,
   bool copy;                                    // x and w from copies with a row stride of ldk
+  bool x8, w8;                                  // x, w are int8 rows, brought back into such copies
   int64_t rows;                                 // row blocks of the element-wise pass
   int64_t ldn, ldm, ldk;                        // padded N, M and K
   int cfg_dx, cfg_dw, splits_dx, splits_dw;
-  size_t off_du, off_dut, off_wt, off_xt, off_sum, off_part;
+  size_t off_du, off_dut, off_wt, off_xt, off_w8, off_x8, off_sum, off_part;
   size_t ws_bytes;
 };
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
-                                        bool need_sums, bool du_direct, bool aligned_xw);
+                                        bool need_sums, bool du_direct, bool aligned_xw, bool x8, bool w8);
+
+// Operands of the backward that are held as int8 rows (q null: they are not).
+struct HeldInt8 {
+  Int8Rows u, x, w;
+};
 
 hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int dtype, int64_t M, int64_t N,
                          int64_t K, const void* t, const void* b, int64_t r, float s, const Epilogue& ep,
-                         int out_dtype, char* ws, hipStream_t st);
+                         const float* w_scale, int out_dtype, char* ws, hipStream_t st);
 hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, const void* u, const void* x,
                                   const void* w, int dtype, int64_t M, int64_t N, int64_t K, const float* row_scale,
                                   const float* col_scale, const float* bias, int act, void* du, void* dx, void* dw,
-                                  float* dbias, float* dcol, char* ws, hipStream_t st);
+                                  float* dbias, float* dcol, const HeldInt8& held, char* ws, hipStream_t st);
 
 }  // namespace dora

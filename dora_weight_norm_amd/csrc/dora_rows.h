@@ -9,6 +9,8 @@ namespace dora {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
+constexpr float kInt8Max = 127.f;
+enum : int { kQE4m3 = 0, kQInt8 = 1 };   // what 8-bit rows hold
 // Inputs of more than this stream past the caches, which they would only
 // empty: measured at 8192 x 8192 bf16 to 8 bits 84 us with ordinary loads and
 // stores, 77.5 us with non-temporal ones; at 777 x 3583, which the caches
@@ -63,16 +65,9 @@ __device__ __forceinline__ void store_row_chunk(T* row, int64_t k, int64_t d, co
   }
 }
 
-// E fp32 values to e4m3 (OCP, round to nearest even), four to a word.
+// E bytes of a row chunk, four to a word.
 template <int E, bool STREAM = false>
-__device__ __forceinline__ void store_row_q(uint8_t* row, int64_t k, int64_t d, const float (&f)[E]) {
-  uint32_t w[E / 4];
-#pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], 0, false);
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], v, true);
-    w[i] = (uint32_t)v;
-  }
+__device__ __forceinline__ void store_row_bytes(uint8_t* row, int64_t k, int64_t d, const uint32_t (&w)[E / 4]) {
   if (k + E <= d) {
     if constexpr (E == 8) {
       const u32x2 p = {w[0], w[1]};
@@ -88,6 +83,43 @@ __device__ __forceinline__ void store_row_q(uint8_t* row, int64_t k, int64_t d, 
     for (int e = 0; e < E; ++e)
       if (k + e < d) row[k + e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
   }
+}
+
+// E bytes of a row from column k on, zeros past d.
+template <int E, bool STREAM = false>
+__device__ __forceinline__ void load_row_bytes(const uint8_t* row, int64_t k, int64_t d, uint32_t (&w)[E / 4]) {
+  if (k + E <= d) {
+    if constexpr (E == 8) {
+      const u32x2_any* p = reinterpret_cast<const u32x2_any*>(row + k);
+      u32x2 v;
+      if constexpr (STREAM)
+        v = __builtin_nontemporal_load(p);
+      else
+        v = *p;
+      w[0] = v[0], w[1] = v[1];
+    } else {
+      w[0] = *reinterpret_cast<const u32_any*>(row + k);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) w[i] = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (k + e < d) w[e / 4] |= (uint32_t)row[k + e] << (8 * (e % 4));
+  }
+}
+
+// E fp32 values to e4m3 (OCP, round to nearest even), four to a word.
+template <int E, bool STREAM = false>
+__device__ __forceinline__ void store_row_q(uint8_t* row, int64_t k, int64_t d, const float (&f)[E]) {
+  uint32_t w[E / 4];
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], v, true);
+    w[i] = (uint32_t)v;
+  }
+  store_row_bytes<E, STREAM>(row, k, d, w);
 }
 
 // E weights (fp32) of a chunk; ones where there are none, zeros past d.
@@ -148,11 +180,11 @@ __device__ __forceinline__ uint32_t row_max_bits(uint32_t v, uint32_t* lds) {
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-// scale = top / 448: 1 for a row of zeros, at least kMinScale otherwise; NaN
-// or infinite where top is.
-__device__ __forceinline__ float scale_of(uint32_t top_bits) {
+// scale = top / most (448 in e4m3, 127 in integers): 1 for a row of zeros, at
+// least kMinScale otherwise; NaN or infinite where top is.
+__device__ __forceinline__ float scale_of(uint32_t top_bits, float most = kE4m3Max) {
   const float top = __uint_as_float(top_bits);
-  const float s = top / kE4m3Max;
+  const float s = top / most;
   return top_bits == 0 ? 1.f : (s < kMinScale ? kMinScale : s);
 }
 
@@ -170,7 +202,58 @@ struct RowQuotient {
     const float q = n * inv;
     return fmaf(fmaf(-q, s, n), inv, q);
   }
+  // The integer nearest to n / scale (not to the rounded quotient), ties to the
+  // even one, as a float. A quotient that rounds to a tie comes from one side of
+  // it or from the tie itself, which the sign of the exact remainder tells: rows
+  // of few significant bits meet it often (half of the row's largest value is
+  // 63.5 steps). NaN, of rows with a NaN or an infinity, gives 0.
+  __device__ __forceinline__ float whole(float n) const {
+    const float q = (*this)(n);
+    const float k = rintf(q), d = q - k;
+    const float r = fmaf(-q, s, n);
+    const float w = fabsf(d) == 0.5f && r * d > 0.f ? k + 2.f * d : k;
+    return w == w ? w : 0.f;
+  }
 };
+
+// E values of |v| <= 127 that are whole, as bytes.
+template <int E>
+__device__ __forceinline__ void bytes_of(const float (&v)[E], uint32_t (&w)[E / 4]) {
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    const uint32_t a = (uint32_t)(int)v[4 * i], b = (uint32_t)(int)v[4 * i + 1];
+    const uint32_t c = (uint32_t)(int)v[4 * i + 2], d = (uint32_t)(int)v[4 * i + 3];
+    // (bytes 0 of two words each, then the two halves)
+    w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u),
+                                 0x05040100u);
+  }
+}
+
+// E fp32 values of a row chunk as 8-bit integers.
+template <int E, bool STREAM = false>
+__device__ __forceinline__ void store_row_int8(uint8_t* row, int64_t k, int64_t d, const float (&f)[E],
+                                               const RowQuotient& quotient) {
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = quotient.whole(f[e]);
+  uint32_t w[E / 4];
+  bytes_of<E>(v, w);
+  store_row_bytes<E, STREAM>(row, k, d, w);
+}
+
+// E fp32 values of a row chunk in the 8-bit type that `kind` names.
+template <int E, bool STREAM = false>
+__device__ __forceinline__ void store_row_8(uint8_t* row, int64_t k, int64_t d, const float (&f)[E],
+                                            const RowQuotient& quotient, int kind) {
+  if (kind == kQInt8) {
+    store_row_int8<E, STREAM>(row, k, d, f, quotient);
+  } else {
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = quotient(f[e]);
+    store_row_q<E, STREAM>(row, k, d, v);
+  }
+}
 
 // Threads and chunks a thread that hold a row of d elements; nt 0: too long.
 struct RowShape {
@@ -183,7 +266,7 @@ struct RowShape {
 // two workgroups a compute unit for their registers: 80 against 77.5 us), or
 // 1024 where there are too few rows to fill the chip. Rows of up to 16384 elements stay in registers
 // (1024 threads have 128 registers each: two 16-bit chunks or four fp32).
-RowShape forward_shape(int64_t T, int64_t d, int epc) {
+[[maybe_unused]] RowShape forward_shape(int64_t T, int64_t d, int epc) {
   const int64_t ch = (d + epc - 1) / epc;
   auto fit = [&](int nt) {
     const int64_t c = (ch + nt - 1) / nt;
@@ -208,7 +291,7 @@ RowShape backward_shape(int64_t d, int epc) {
 
 // Workgroups of the backward: enough waves to fill the chip (256 compute
 // units), few enough that the dweight partials stay small beside the rows.
-int64_t backward_grid(int64_t T, int64_t d, int epc) {
+[[maybe_unused]] int64_t backward_grid(int64_t T, int64_t d, int epc) {
   const RowShape r = backward_shape(d, epc);
   const int64_t g = r.nt == 64 ? 2048 : (r.nt == 256 ? 512 : 256);
   return T < g ? T : g;
@@ -216,7 +299,7 @@ int64_t backward_grid(int64_t T, int64_t d, int epc) {
 
 // Workgroups of the forward: one a row (or four rows), up to what the chip
 // holds at once; past that each takes several rows.
-unsigned grid_of(int64_t n, int nt) {
+[[maybe_unused]] unsigned grid_of(int64_t n, int nt) {
   const int64_t most = nt == 1024 ? 512 : kFwdGrid;
   return (unsigned)(n < most ? n : most);
 }

@@ -15,6 +15,11 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 struct e4m3_t {
   uint8_t v;
 };
+struct int8x_t {   // 8-bit integers
+  int8_t v;
+};
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // Operand types: bytes of an element, 16-byte chunks of a lane's fragment,
 // and one matrix instruction step over 2 * FC chunks of depth.
@@ -59,6 +64,29 @@ struct Op<e4m3_t> {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_bit_cast(i32x8, pa), __builtin_bit_cast(i32x8, pb),
                                                            c, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
   }
+};
+
+template <>
+struct Op<int8x_t> {
+  static constexpr int esz = 1, fc = 1;
+  // Integer sums, in the registers that hold fp32 ones elsewhere (0 has the
+  // same bits in both).
+  static __device__ __forceinline__ f32x16 run(const u32x4* a, const u32x4* b, f32x16 c) {
+    return __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                                          __builtin_bit_cast(i32x4, a[0]), __builtin_bit_cast(i32x4, b[0]),
+                                          __builtin_bit_cast(i32x16, c), 0, 0, 0));
+  }
+};
+
+// The low-rank pair's type: the operands' own, but 16 bits, the output's,
+// beside 8-bit integers.
+template <typename T, typename O>
+struct PairType {
+  using type = T;
+};
+template <typename O>
+struct PairType<int8x_t, O> {
+  using type = std::conditional_t<sizeof(O) == 2, O, bf16_t>;   // (fp32 outputs come without a pair)
 };
 
 // Activations (dora_act) and their slopes, in fp32 arithmetic. F32: the result
@@ -384,16 +412,22 @@ __device__ __forceinline__ u32x4 read_tr(const char* unit, int r0, int s, int la
 // ---------------------------------------------------------------------------
 template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT, bool BT>
 __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g) {
-  constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, E = 16 / ESZ, KT = 128 / ESZ;
+  constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, KT = 128 / ESZ;
   constexpr int NW = WM * WN, MT = WM * MB * 32, NT = WN * NB * 32;
   constexpr int UNIT = (MT > NT ? MT : NT) * 128;           // bytes of a ring unit
   constexpr int ABLK = MT / 8 / NW, BBLK = NT / 8 / NW;   // 1 KiB blocks per wave per stage
   constexpr int BPW = ABLK + BBLK;
   constexpr int STEPS = 8 / (2 * FC);
+  // 8-bit integers: their sums come first, are converted and scaled in the
+  // registers, and the pair's products are added to them there.
+  constexpr bool I8 = std::is_same<T, int8x_t>::value;
+  using TP = typename PairType<T, O>::type;
+  constexpr int ESZ2 = Op<TP>::esz, KT2 = 128 / ESZ2;
+  static_assert(Op<TP>::fc == FC, "the pair's stages have as many steps");
   constexpr int EPW = NB * 32 + 4;                         // floats of an epilogue row (padded: no bank conflicts)
   static_assert(MT % (8 * NW) == 0 && NT % (8 * NW) == 0, "a stage splits evenly over the waves");
   constexpr int RING = (2 * P + 1) * UNIT;
-  static_assert(NW * 32 * EPW * 4 <= RING, "the epilogue fits the ring");
+  static_assert((NW * 32 * EPW + (I8 ? NW * NB * 32 : 0)) * 4 <= RING && (!I8 || NB * 32 <= 64), "the epilogue fits the ring");
   static_assert(RING <= 160 * 1024, "gfx950 has 160 KiB of LDS");
   static_assert(STEPS % 2 == 0, "step s of every stage uses fragment set s & 1");
   extern __shared__ __align__(1024) char lds[];
@@ -419,11 +453,12 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   const int chunk = (lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7);   // of depth, in rows along it
   const Stream sa = make_stream<ESZ, MT, NW, AT>(g.a, g.lda, m0, g.M, lane, wave);
   const Stream sb = make_stream<ESZ, NT, NW, BT>(g.b, g.ldb, n0, g.N, lane, wave);
-  const Stream sa2 = make_stream<ESZ, MT, NW, false>(g.a2, g.lda2, m0, g.M, lane, wave);
-  const Stream sb2 = make_stream<ESZ, NT, NW, false>(g.b2, g.ldb2, n0, g.N, lane, wave);
-  // Stages: the low-rank pair's first, then the main depth's; this workgroup's
-  // part of them is [st0, st1).
-  const int n2 = PAIR ? (int)((g.K2 + KT - 1) / KT) : 0;
+  const Stream sa2 = make_stream<ESZ2, MT, NW, false>(g.a2, g.lda2, m0, g.M, lane, wave);
+  const Stream sb2 = make_stream<ESZ2, NT, NW, false>(g.b2, g.ldb2, n0, g.N, lane, wave);
+  // Stages: the low-rank pair's first, then the main depth's (8-bit integers:
+  // the other way round); this workgroup's part of them is [st0, st1).
+  const int n2 = PAIR ? (int)((g.K2 + KT2 - 1) / KT2) : 0;
+  const int n1 = I8 ? (int)((g.K + KT - 1) / KT) : 0;
   const int st0 = split * g.stages_per_split;
   const int st1 = st0 + g.stages_per_split < g.stages ? st0 + g.stages_per_split : g.stages;
 
@@ -441,9 +476,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       const uint32_t off = main.off + (uint32_t)b * main.step;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
     } else {
-      const bool pr = PAIR && i < n2;
-      const int k0 = (pr ? i : i - n2) * 128;   // bytes of depth before the stage
-      const int left = i < st1 ? (int)((pr ? g.K2 : g.K) * ESZ) - k0 : 0;
+      const bool pr = PAIR && (I8 ? i >= n1 : i < n2);
+      const int k0 = (I8 ? (pr ? i - n1 : i) : (pr ? i : i - n2)) * 128;   // bytes of depth before the stage
+      const int left = i < st1 ? (int)(pr ? g.K2 * ESZ2 : g.K * ESZ) - k0 : 0;
       const uint32_t at = pr ? pair.off + (uint32_t)b * pair.step : main.off + (uint32_t)b * main.step;
       const uint32_t off = chunk * 16 < left ? at : kOob;
       const __amdgpu_buffer_rsrc_t rs = pr ? pair.rsrc : main.rsrc;
@@ -461,7 +496,6 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   const int nv = (int)(g.N - n < 8 ? g.N - n : 8);
   float cs[8], bs[8];
   column_terms(g.ep, n, nv, cs, bs);
-
   f32x16 acc[MB][NB];
 #pragma unroll
   for (int a = 0; a < MB; ++a)
@@ -515,8 +549,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // source but not the matrix instructions between them.
   constexpr int RPM = (2 * ND + NM - 1) / NM;
   Frag F[2];
-  auto step = [&](Frag& cur, Frag& nxt, int ua, int ub, int s, int i, int ul, int um, int l0, int l1)
+  auto step = [&](Frag& cur, Frag& nxt, int ua, int ub, int s, int i, int ul, int um, int l0, int l1, auto pair)
       __attribute__((always_inline)) {
+    using TX = std::conditional_t<I8 && decltype(pair)::value, TP, T>;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
 #pragma unroll
@@ -530,7 +565,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
           else
             issue_a(i + P + 1, um, l - BBLK);
         }
-      acc[m / NB][m % NB] = Op<T>::run(cur.b[m % NB], cur.a[m / NB], acc[m / NB][m % NB]);   // (turned)
+      acc[m / NB][m % NB] = Op<TX>::run(cur.b[m % NB], cur.a[m / NB], acc[m / NB][m % NB]);   // (turned)
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -567,27 +602,64 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // Every matrix instruction stands in this one loop body: with the last
   // step's outside of it the compiler moved all accumulators between register
   // files around the loop.
-  auto stage = [&](int i) __attribute__((always_inline)) {
+  auto stage = [&](int i, auto pair) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s + 1 < STEPS; ++s)
       step(F[s & 1], F[(s + 1) & 1], unit(0), unit(1), s + 1, i - 1, unit(2 * P - 1), unit(2 * P),
-           BPW * (s + 1) / STEPS, BPW * (s + 2) / STEPS);
+           BPW * (s + 1) / STEPS, BPW * (s + 2) / STEPS, pair);
     // This wave has read all of stage i, and its loads of stage i + 1 have
     // landed; younger ones stay in flight. Past the barrier the units of stage
     // i take the next period's loads.
     wait_vm_lgkm0<LATER>();
     barrier_keep_loads();
-    step(F[1], F[0], unit(2), unit(3), 0, i, unit(0), unit(1), 0, L1);
+    step(F[1], F[0], unit(2), unit(3), 0, i, unit(0), unit(1), 0, L1, pair);
     u0 = unit(2);
   };
+  // Scales of the four columns that a lane holds in accumulators 4q to 4q + 3 of
+  // a block, row lane % 32 of it (past the last column zeros).
+  typedef float f32x4v __attribute__((ext_vector_type(4)));
+  const __amdgpu_buffer_rsrc_t ws_rsrc = make_rsrc(g.w_scale, I8 ? (uint32_t)(g.N * 4) : 0u);
+  auto w_scale4 = [&](int b, int q) __attribute__((always_inline)) {
+    const int at = (int)(n0 + (wn * NB + b) * 32 + 8 * q + 4 * fg) * 4;
+    return __builtin_bit_cast(f32x4v, __builtin_amdgcn_raw_buffer_load_b128(ws_rsrc, at, 0, 0));
+  };
   int i = st0;
-  if constexpr (PAIR) {
-    if (st0 < n2) {
-      for (; i < n2; ++i) stage(i);
+  if constexpr (I8) {
+    const int mid = st1 < n1 ? st1 : n1;
+    for (; i < mid; ++i) stage(i, Tag<false>{});
+    // (Without a pair the epilogue converts the sums.)
+    if constexpr (PAIR) {
+      float rs[MB];
+#pragma unroll
+      for (int a = 0; a < MB; ++a) {
+        const int64_t m = m0 + (wm * MB + a) * 32 + fr;
+        rs[a] = g.pair_rows[m < g.M ? m : g.M - 1];
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4v ws = w_scale4(b, q);
+#pragma unroll
+          for (int a = 0; a < MB; ++a)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float sum = (float)__float_as_int(acc[a][b][4 * q + v]);
+              acc[a][b][4 * q + v] = sum * rs[a] * ws[v] * g.inv_s;
+            }
+        }
+      for (; i < st1; ++i) stage(i, Tag<true>{});
       scale();
     }
+  } else {
+    if constexpr (PAIR) {
+      if (st0 < n2) {
+        for (; i < n2; ++i) stage(i, Tag<true>{});
+        scale();
+      }
+    }
+    for (; i < st1; ++i) stage(i, Tag<false>{});
   }
-  for (; i < st1; ++i) stage(i);
   wait_vm_lgkm0<0>();   // (the loads past the depth too: the ring is reused)
   barrier_keep_loads();
   // Epilogue: each wave turns its accumulators, 32 rows at a time, into rows
@@ -601,6 +673,13 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // accumulators are named by constants in a chain of uniform branches, since
   // registers cannot be indexed. The residual's rows are loaded one pass ahead.
   float* ew = reinterpret_cast<float*>(lds) + wave * 32 * EPW;
+  // 8-bit integers without a pair: the columns' scales, in LDS (there are no
+  // registers for them beside the accumulators of the 256-row tile)
+  float* wl = reinterpret_cast<float*>(lds) + NW * 32 * EPW + wave * NB * 32;
+  if constexpr (I8 && !PAIR) {
+    const int64_t c = n0 + wn * NB * 32 + lane;
+    if (lane < NB * 32) wl[lane] = g.w_scale[c < g.N ? c : g.N - 1];
+  }
   constexpr int IT = MB * PB / 2;
   const bool has_res = g.ep.residual != nullptr && g.splits == 1;
   const int64_t m_first = m0 + wm * MB * 32 + lane / LPR;   // this lane's first row; the others RPP apart
@@ -629,8 +708,8 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            typedef float f32x4v __attribute__((ext_vector_type(4)));
-            const f32x4v v = {acc[c][b][4 * q], acc[c][b][4 * q + 1], acc[c][b][4 * q + 2], acc[c][b][4 * q + 3]};
+            f32x4v v = {acc[c][b][4 * q], acc[c][b][4 * q + 1], acc[c][b][4 * q + 2], acc[c][b][4 * q + 3]};
+            if constexpr (I8 && !PAIR) v = __builtin_convertvector(__builtin_bit_cast(i32x4, v), f32x4v);
             *reinterpret_cast<f32x4v*>(ew + fr * EPW + b * 32 + 8 * q + 4 * fg) = v;
           }
       }
@@ -644,6 +723,10 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       const int row = ((it % (PB / 2)) * 2 + i) * RPP + lane / LPR;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[8 * i + e] = ew[row * EPW + col + e];
+      if constexpr (I8 && !PAIR) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[8 * i + e] *= wl[col + e];
+      }
       m[i] = m_first + (2 * it + i) * RPP;
       off[i] = at + i * pass;
       ok[i] = (2 * it + i) * RPP < rl;
@@ -725,11 +808,20 @@ struct Op16<e4m3_t> {
   }
 };
 
+template <>
+struct Op16<int8x_t> {   // integer sums, as in Op
+  static __device__ __forceinline__ f32x4 run(const u32x4* a, const u32x4* b, f32x4 c) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                         __builtin_bit_cast(i32x4, a[0]), __builtin_bit_cast(i32x4, b[0]),
+                                         __builtin_bit_cast(i32x4, c), 0, 0, 0));
+  }
+};
+
 constexpr int kFewWaves = 8;   // waves of a workgroup, each with its share of the depth
 
 template <typename T, int R, int TF, int BATCH>
 struct FewFrag {
-  static constexpr int CH = sizeof(T) == 1 ? 2 : 1;   // 16-byte chunks a lane feeds one instruction
+  static constexpr int CH = std::is_same<T, e4m3_t>::value ? 2 : 1;   // 16-byte chunks a lane feeds one instruction
   u32x4 w[BATCH][R][CH], x[BATCH][TF][CH];
 };
 
@@ -813,6 +905,9 @@ __device__ __forceinline__ void few_rows_depth(const char* const (&wp)[R], const
 template <typename T, typename O, int R, int TF, int BATCH>
 __global__ __launch_bounds__(kFewWaves * 64, TF <= 2 ? 2 : 1) void matmul_few_rows_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz;
+  constexpr bool I8 = std::is_same<T, int8x_t>::value;   // (sums first, then the pair; see the tile kernel)
+  using TP = typename PairType<T, O>::type;
+  constexpr int ESZ2 = Op<TP>::esz;
   __shared__ float red[kFewWaves * R * TF * 256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i8 = lane & 7, chunk = lane >> 3;
@@ -825,13 +920,13 @@ __global__ __launch_bounds__(kFewWaves * 64, TF <= 2 ? 2 : 1) void matmul_few_ro
   for (int r = 0; r < R; ++r) {
     const int64_t n = n0 + r * 8 + i8 < g.N ? n0 + r * 8 + i8 : g.N - 1;
     wp[r] = static_cast<const char*>(g.b) + n * g.ldb * ESZ;
-    bp[r] = static_cast<const char*>(g.b2) + n * g.ldb2 * ESZ;
+    bp[r] = static_cast<const char*>(g.b2) + n * g.ldb2 * ESZ2;
   }
 #pragma unroll
   for (int t = 0; t < TF; ++t) {
     const int64_t m = m0 + t * 8 + i8 < g.M ? m0 + t * 8 + i8 : g.M - 1;
     xp[t] = static_cast<const char*>(g.a) + m * g.lda * ESZ;
-    tp[t] = static_cast<const char*>(g.a2) + m * g.lda2 * ESZ;
+    tp[t] = static_cast<const char*>(g.a2) + m * g.lda2 * ESZ2;
   }
   f32x4 acc[R][TF];
 #pragma unroll
@@ -839,14 +934,47 @@ __global__ __launch_bounds__(kFewWaves * 64, TF <= 2 ? 2 : 1) void matmul_few_ro
 #pragma unroll
     for (int t = 0; t < TF; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int part = split * kFewWaves + wave, parts = g.splits * kFewWaves;
-  if (g.K2 > 0) {
-    few_rows_depth<T, R, TF, BATCH < 2 ? BATCH : 2>(bp, tp, g.K2 * ESZ, part, parts, chunk, acc);
+  if (!I8 && g.K2 > 0) {
+    few_rows_depth<TP, R, TF, BATCH < 2 ? BATCH : 2>(bp, tp, g.K2 * ESZ2, part, parts, chunk, acc);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int t = 0; t < TF; ++t) acc[r][t] *= g.s;
   }
   few_rows_depth<T, R, TF, BATCH>(wp, xp, g.K * ESZ, part, parts, chunk, acc);
+  if constexpr (I8) {
+    // Sum (i, j) of a 16 x 16 block is value i % 4 of lane 16 (i / 4) + j: columns
+    // 4 (lane / 16) + v mod 8 of the block's eight, and token lane % 8.
+    const bool pair = g.K2 > 0;
+    float rs[TF];
+#pragma unroll
+    for (int t = 0; t < TF; ++t) {
+      const int64_t m = m0 + t * 8 + i8;
+      rs[t] = pair ? g.pair_rows[m < g.M ? m : g.M - 1] : 1.f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float ws[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t n = n0 + r * 8 + 4 * ((lane >> 4) & 1) + v;
+        ws[v] = g.w_scale[n < g.N ? n : g.N - 1];
+      }
+#pragma unroll
+      for (int t = 0; t < TF; ++t) {
+        const i32x4 sum = __builtin_bit_cast(i32x4, acc[r][t]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[r][t][v] = (float)sum[v] * rs[t] * ws[v] * (pair ? g.inv_s : 1.f);
+      }
+    }
+    if (pair) {
+      few_rows_depth<TP, R, TF, BATCH < 2 ? BATCH : 2>(bp, tp, g.K2 * ESZ2, part, parts, chunk, acc);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TF; ++t) acc[r][t] *= g.s;
+    }
+  }
   // Sum (i, j) of a 16 x 16 block is value i % 4 of lane 16 (i / 4) + j.
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -947,7 +1075,7 @@ hipError_t launch_few_rows(GemmArgs g, hipStream_t st) {
   g.n_nt = (int)((g.N + 8 * R - 1) / (8 * R));
   g.n_mt = (int)((g.M + 8 * TF - 1) / (8 * TF));
   // (at most 128 registers, two workgroups a compute unit, where TF <= 2)
-  constexpr int BATCH = (TF == 1 ? 4 : 2) / (Op<T>::esz == 1 ? 2 : 1);
+  constexpr int BATCH = (TF == 1 ? 4 : 2) / (std::is_same<T, e4m3_t>::value ? 2 : 1);
   hipLaunchKernelGGL((matmul_few_rows_kernel<T, O, R, TF, BATCH>), dim3((unsigned)((int64_t)g.n_nt * g.n_mt * g.splits)),
                      dim3(kFewWaves * 64), 0, st, g);
   const hipError_t e = hipGetLastError();
@@ -955,25 +1083,26 @@ hipError_t launch_few_rows(GemmArgs g, hipStream_t st) {
 }
 
 // Stages of KT elements of the whole depth and of each of g.splits parts.
-void split_stages(GemmArgs& g, int KT) {
-  const int n2 = (int)((g.K2 + KT - 1) / KT);
+void split_stages(GemmArgs& g, int KT, int KT2) {
+  const int n2 = (int)((g.K2 + KT2 - 1) / KT2);
   g.stages = n2 + (int)((g.K + KT - 1) / KT);
   if (g.stages < 1) g.stages = 1;   // (no depth at all: one stage of zeros)
-  // The low-rank stages and their scaling belong to the first part alone.
+  // The low-rank stages and their scaling belong to the first part alone
+  // (8-bit integers, whose pair comes last: each part scales what it has).
   const int per = (g.stages + g.splits - 1) / g.splits;
-  g.stages_per_split = per > n2 ? per : n2;
+  g.stages_per_split = per > n2 || KT != KT2 ? per : n2;
   g.splits = (g.stages + g.stages_per_split - 1) / g.stages_per_split;
 }
 
 // Adds a copy of *src to the jobs and points *src at it.
-void add_pack(PackJobs& p, const void** src, int64_t rows, int64_t kb, int64_t lb, char* dst) {
+[[maybe_unused]] void add_pack(PackJobs& p, const void** src, int64_t rows, int64_t kb, int64_t lb, char* dst) {
   const int j = p.n++;
   p.src[j] = static_cast<const char*>(*src), p.dst[j] = dst, p.kb[j] = kb, p.lb[j] = lb;
   p.first[j + 1] = p.first[j] + rows * (lb / 16);
   *src = dst;
 }
 
-hipError_t launch_pack(const PackJobs& p, hipStream_t st) {
+[[maybe_unused]] hipError_t launch_pack(const PackJobs& p, hipStream_t st) {
   if (p.n == 0 || p.first[p.n] == 0) return hipSuccess;
   hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)((p.first[p.n] + 255) / 256)), dim3(256), 0, st, p);
   return hipGetLastError();

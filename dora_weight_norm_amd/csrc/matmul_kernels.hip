@@ -14,6 +14,7 @@
 // (87 us without); one token at 8192 x 8192 25 us, 5.6 TB/s (29 us); the
 // backward at 4096^3 254 us, 1.08 PFLOP/s (the vendor's two products 219 us).
 // On random operands the matrix cores sustain 1.73 PFLOP/s in bf16.
+#include "dora_rows.h"
 #include "matmul_device.h"
 
 namespace dora {
@@ -46,8 +47,16 @@ __global__ __launch_bounds__(256) void transpose_kernel(const U* src, int64_t ro
 // col_scale dz (rounded to the storage type: it is the operand of both
 // products, which the matrix cores take in 16 bits), and this row block's sums
 // of dz and dz u over its rows, in increasing order (u holds the row scale).
-template <typename T>
-__global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u, const float* row_scale,
+// U8: u is held as int8 rows (a strip of eight columns lies in one group).
+struct SavedU {
+  const uint8_t* q;
+  const float* scale;
+  int64_t groups;
+  int shift;
+};
+
+template <typename T, bool U8>
+__global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u, SavedU u8, const float* row_scale,
                                                          const float* col_scale, const float* bias, int act, int64_t M,
                                                          int64_t N, T* du, int64_t ldu, T* du2, float* sums) {
   __shared__ float lanes[16][256];
@@ -66,14 +75,21 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
   constexpr int U = 4;
   const int64_t step = (int64_t)gridDim.y * nl;
   for (int64_t m0 = (int64_t)blockIdx.y * nl + ly; nv > 0 && m0 < M; m0 += U * step) {
-    Raw8<T> ry[U], ru[U];
+    Raw8<T> ry[U], ru[U8 ? 1 : U];
+    uint32_t rq[U][2];
+    float us[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t m = m0 + i * step;
       if (m < M) {
         // (du, which the products read next, is to stay in the caches)
         ry[i] = load_raw8<T, true>(dy + m * N + n, nv);
-        ru[i] = load_raw8<T, true>(u + m * N + n, nv);
+        if constexpr (U8) {
+          load_row_bytes<8, true>(u8.q + m * N, n, N, rq[i]);
+          us[i] = u8.scale[m * u8.groups + (n >> u8.shift)];
+        } else {
+          ru[i] = load_raw8<T, true>(u + m * N + n, nv);
+        }
       }
     }
 #pragma unroll
@@ -83,7 +99,12 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
       const float rs = row_scale ? row_scale[m] : 1.f;
       float y[8], v[8], o[8];
       unpack8<T>(ry[i], y);
-      unpack8<T>(ru[i], v);
+      if constexpr (U8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(rq[i][e / 4] >> (8 * (e % 4))) * us[i];
+      } else {
+        unpack8<T>(ru[i], v);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = fmaf(cs[e], v[e], bs[e]);
       slope_all<8, std::is_same<T, float>::value>(o, act);
@@ -133,8 +154,10 @@ constexpr int kRowBlocks = 512;   // workgroups of the element-wise backward
 
 int tile_rows(int cfg) { return cfg == kTile256 ? 256 : (cfg == kTile128 ? 128 : 64); }
 // Elements of a stage's 128 bytes of depth.
-int stage_depth(int dtype) { return dtype == 1 ? 32 : (dtype == 3 ? 128 : 64); }
-int elem_size(int dtype) { return dtype == 1 ? 4 : (dtype == 3 ? 1 : 2); }
+int stage_depth(int dtype) { return dtype == 1 ? 32 : (dtype >= 3 ? 128 : 64); }
+int elem_size(int dtype) { return dtype == 1 ? 4 : (dtype >= 3 ? 1 : 2); }
+// Elements of the low-rank pair.
+int pair_size(int dtype) { return dtype == kInt8Operands ? 2 : elem_size(dtype); }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -230,7 +253,7 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* 
 // [k][row], and with AT `a` too.
 template <typename T, bool AT>
 hipError_t launch_gemm_tr(GemmArgs g, int cfg, hipStream_t st) {
-  split_stages(g, 64);
+  split_stages(g, 64, 64);
   hipError_t e = hipErrorInvalidValue;
   if (cfg == kTile256) e = launch_tile<T, T, 2, 4, 4, 2, 2, false, AT, true>(g, st);
   if (cfg == kTile128) e = launch_tile<T, T, 2, 2, 2, 2, 2, false, AT, true>(g, st);
@@ -243,7 +266,7 @@ hipError_t launch_gemm(GemmArgs g, int cfg, hipStream_t st) {
   if (cfg == kFew8) return launch_few_rows<T, O, 2, 1>(g, st);
   if (cfg == kFew16) return launch_few_rows<T, O, 2, 2>(g, st);
   if (cfg == kFew32) return launch_few_rows<T, O, 4, 4>(g, st);
-  split_stages(g, 128 / Op<T>::esz);
+  split_stages(g, 128 / Op<T>::esz, 128 / Op<T>::esz);
   hipError_t e = hipErrorInvalidValue;
   if (g.K2 > 0) {
     if constexpr (Op<T>::esz > 1) {   // (no pair in e4m3)
@@ -299,17 +322,18 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
   choose_tile(M, N, up(K, KT) / KT, dtype, K % epc == 0 ? kFewOnGrid : kFewOffGrid, &p.cfg, &p.splits);
-  auto operand = [&](int64_t rows, int64_t depth, int bit, bool* pack, int64_t* ld, size_t* at) {
+  auto operand = [&](int64_t rows, int64_t depth, int es, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
-    *pack = p.cfg < kFew8 && depth > 0 && (depth % epc != 0 || !(al & bit));
-    *ld = *pack ? up(depth, epc) : depth;
+    *pack = p.cfg < kFew8 && depth > 0 && (depth % (16 / es) != 0 || !(al & bit));
+    *ld = *pack ? up(depth, 16 / es) : depth;
     *at = off;
-    if (*pack) off = up256(off + (size_t)(rows * *ld) * esz);
+    if (*pack) off = up256(off + (size_t)(rows * *ld) * es);
   };
-  operand(M, K, 1, &p.pack_x, &p.ldx, &p.off_x);
-  operand(N, K, 2, &p.pack_w, &p.ldw, &p.off_w);
-  operand(M, r, 4, &p.pack_t, &p.ldt, &p.off_t);
-  operand(N, r, 8, &p.pack_b, &p.ldb, &p.off_b);
+  const int es2 = pair_size(dtype);
+  operand(M, K, esz, 1, &p.pack_x, &p.ldx, &p.off_x);
+  operand(N, K, esz, 2, &p.pack_w, &p.ldw, &p.off_w);
+  operand(M, r, es2, 4, &p.pack_t, &p.ldt, &p.off_t);
+  operand(N, r, es2, 8, &p.pack_b, &p.ldb, &p.off_b);
   p.off_part = off;
   if (p.splits > 1) off = up256(off + (size_t)(p.splits * M * N) * 4);
   p.ws_bytes = off;
@@ -318,13 +342,13 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
 
 hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int dtype, int64_t M, int64_t N,
                          int64_t K, const void* t, const void* b, int64_t r, float s, const Epilogue& ep,
-                         int out_dtype, char* ws, hipStream_t st) {
-  const int esz = elem_size(dtype);
+                         const float* w_scale, int out_dtype, char* ws, hipStream_t st) {
+  const int esz = elem_size(dtype), es2 = pair_size(dtype);
   PackJobs jobs{};
   if (p.pack_x) add_pack(jobs, &x, M, K * esz, p.ldx * esz, ws + p.off_x);
   if (p.pack_w) add_pack(jobs, &w, N, K * esz, p.ldw * esz, ws + p.off_w);
-  if (p.pack_t) add_pack(jobs, &t, M, r * esz, p.ldt * esz, ws + p.off_t);
-  if (p.pack_b) add_pack(jobs, &b, N, r * esz, p.ldb * esz, ws + p.off_b);
+  if (p.pack_t) add_pack(jobs, &t, M, r * es2, p.ldt * es2, ws + p.off_t);
+  if (p.pack_b) add_pack(jobs, &b, N, r * es2, p.ldb * es2, ws + p.off_b);
   const hipError_t e = launch_pack(jobs, st);
   if (e != hipSuccess) return e;
   GemmArgs g{};
@@ -333,12 +357,21 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
   g.s = s, g.M = M, g.N = N, g.splits = p.splits;
   g.part = reinterpret_cast<float*>(ws + p.off_part);
   g.ep = ep;
+  if (dtype == kInt8Operands) {
+    g.w_scale = w_scale;
+    if (r > 0) {   // (the pair's products are added to scaled sums, and s multiplies both)
+      g.pair_rows = ep.row_scale, g.ep.row_scale = nullptr;
+      g.inv_s = 1.f / s;
+    }
+    return gemm_int8(g, out_dtype, p.cfg, st);
+  }
   return gemm(g, dtype, out_dtype, p.cfg, st);
 }
 
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
-                                        bool need_sums, bool du_direct, bool aligned_xw) {
+                                        bool need_sums, bool du_direct, bool aligned_xw, bool x8, bool w8) {
   MatmulBackwardPlan p{};
+  p.x8 = x8 && need_dw, p.w8 = w8 && need_dx;
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   p.ldn = up(N, epc), p.ldm = up(M, epc);
   const int64_t strips = (N + 7) / 8, bx = (strips + 255) / 256;
@@ -360,9 +393,13 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.direct = dtype != 1;
   p.ldk = up(K, epc);
   p.copy = p.direct && (!aligned_xw || K % epc != 0);
-  p.off_wt = take(!need_dx ? 0 : (p.copy ? (size_t)(N * p.ldk) * esz : (p.direct ? 0 : (size_t)(K * p.ldn) * esz)));
+  // (int8 rows are brought back at the copies' stride, as whole chunks, whether or not others are copied)
+  const size_t w_bytes = (size_t)(N * p.ldk) * esz, x_bytes = (size_t)(M * p.ldk) * esz;
+  p.off_wt = take(!need_dx ? 0 : (p.copy || (p.direct && p.w8) ? w_bytes : (p.direct ? 0 : (size_t)(K * p.ldn) * esz)));
   p.off_dut = take(need_dw && !p.direct ? (size_t)(N * p.ldm) * esz : 0);
-  p.off_xt = take(!need_dw ? 0 : (p.copy ? (size_t)(M * p.ldk) * esz : (p.direct ? 0 : (size_t)(K * p.ldm) * esz)));
+  p.off_xt = take(!need_dw ? 0 : (p.copy || (p.direct && p.x8) ? x_bytes : (p.direct ? 0 : (size_t)(K * p.ldm) * esz)));
+  p.off_w8 = take(p.w8 && !p.direct ? w_bytes : 0);
+  p.off_x8 = take(p.x8 && !p.direct ? x_bytes : 0);
   size_t part = 0;
   if (need_dx) {
     choose_tile(M, K, up(N, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dx, &p.splits_dx);
@@ -381,7 +418,7 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
 hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, const void* u, const void* x,
                                   const void* w, int dtype, int64_t M, int64_t N, int64_t K, const float* row_scale,
                                   const float* col_scale, const float* bias, int act, void* du, void* dx, void* dw,
-                                  float* dbias, float* dcol, char* ws, hipStream_t st) {
+                                  float* dbias, float* dcol, const HeldInt8& held, char* ws, hipStream_t st) {
   const int esz = elem_size(dtype);
   hipError_t e = hipSuccess;
   // The element-wise pass writes du into the caller's array where that can be
@@ -398,16 +435,23 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     if (tx > 256) tx = 256;
     const dim3 block((unsigned)tx, (unsigned)(256 / tx));
     const dim3 grid((unsigned)((strips + tx - 1) / tx), (unsigned)p.rows);
-#define DORA_BWD(T)                                                                                             \
-  hipLaunchKernelGGL((matmul_bwd_kernel<T>), grid, block, 0, st, static_cast<const T*>(dy),                     \
-                     static_cast<const T*>(u), row_scale, col_scale, bias, act, M, N, reinterpret_cast<T*>(d),  \
+    const SavedU u8{held.u.q, held.u.scale, scales_of(N, held.u.group), group_shift(held.u.group)};
+#define DORA_BWD_U(T, U8)                                                                                           \
+  hipLaunchKernelGGL((matmul_bwd_kernel<T, U8>), grid, block, 0, st, static_cast<const T*>(dy),                     \
+                     static_cast<const T*>(u), u8, row_scale, col_scale, bias, act, M, N, reinterpret_cast<T*>(d),  \
                      p.ldn, static_cast<T*>(du2), sums)
+#define DORA_BWD(T)          \
+  if (u8.q != nullptr)       \
+    DORA_BWD_U(T, true);     \
+  else                       \
+    DORA_BWD_U(T, false)
     switch (dtype) {
       case 0: DORA_BWD(bf16_t); break;
       case 2: DORA_BWD(f16_t); break;
       default: DORA_BWD(float); break;
     }
 #undef DORA_BWD
+#undef DORA_BWD_U
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -417,31 +461,40 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   }
   GemmArgs g{};
   g.part = reinterpret_cast<float*>(ws + p.off_part);
+  // Int8 rows back to the storage type.
+  auto back = [&](const Int8Rows& r, int64_t rows, size_t off, const void** to) {
+    *to = ws + off;
+    if (rows > 0 && K > 0 && e == hipSuccess) e = launch_dequantize_rows(r, rows, K, p.ldk, dtype, ws + off, st);
+  };
+  if (p.w8) back(held.w, N, p.direct ? p.off_wt : p.off_w8, &w);
+  if (p.x8) back(held.x, M, p.direct ? p.off_xt : p.off_x8, &x);
+  if (e != hipSuccess) return e;
   if (p.direct) {
     if (p.copy) {
       PackJobs jobs{};
-      if (dx) add_pack(jobs, &w, N, K * esz, p.ldk * esz, ws + p.off_wt);
-      if (dw) add_pack(jobs, &x, M, K * esz, p.ldk * esz, ws + p.off_xt);
+      if (dx && !p.w8) add_pack(jobs, &w, N, K * esz, p.ldk * esz, ws + p.off_wt);
+      if (dw && !p.x8) add_pack(jobs, &x, M, K * esz, p.ldk * esz, ws + p.off_xt);
       e = launch_pack(jobs, st);
       if (e != hipSuccess) return e;
     }
-    const int64_t ldu = p.du_direct ? N : p.ldn, ldk = p.copy ? p.ldk : K;
+    const int64_t ldu = p.du_direct ? N : p.ldn;
+    const int64_t ldw = p.copy || p.w8 ? p.ldk : K, ldx = p.copy || p.x8 ? p.ldk : K;
     // dx: du along the depth, w across it; dw: both across it.
     if (dx && M > 0 && K > 0) {
-      g.a = d, g.b = w, g.lda = ldu, g.ldb = ldk, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
+      g.a = d, g.b = w, g.lda = ldu, g.ldb = ldw, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
       g.ep.y = dx;
       e = dtype == 0 ? launch_gemm_tr<bf16_t, false>(g, p.cfg_dx, st) : launch_gemm_tr<f16_t, false>(g, p.cfg_dx, st);
       if (e != hipSuccess) return e;
     }
     if (dw && N > 0 && K > 0) {
-      g.a = d, g.b = x, g.lda = ldu, g.ldb = ldk, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
+      g.a = d, g.b = x, g.lda = ldu, g.ldb = ldx, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
       g.ep.y = dw;
       e = dtype == 0 ? launch_gemm_tr<bf16_t, true>(g, p.cfg_dw, st) : launch_gemm_tr<f16_t, true>(g, p.cfg_dw, st);
     }
     return e;
   }
   if (dx && M > 0 && K > 0) {
-    if (N > 0) e = transpose(w, N, K, K, p.ldn, esz, ws + p.off_wt, st);
+    if (N > 0) e = transpose(w, N, K, p.w8 ? p.ldk : K, p.ldn, esz, ws + p.off_wt, st);
     if (e != hipSuccess) return e;
     g.a = d, g.b = ws + p.off_wt, g.lda = p.ldn, g.ldb = p.ldn, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
     g.ep.y = dx;
@@ -452,7 +505,7 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     if (M > 0) {
       e = transpose(d, M, N, p.ldn, p.ldm, esz, ws + p.off_dut, st);
       if (e != hipSuccess) return e;
-      e = transpose(x, M, K, K, p.ldm, esz, ws + p.off_xt, st);
+      e = transpose(x, M, K, p.x8 ? p.ldk : K, p.ldm, esz, ws + p.off_xt, st);
       if (e != hipSuccess) return e;
     }
     g.a = ws + p.off_dut, g.b = ws + p.off_xt, g.lda = p.ldm, g.ldb = p.ldm, g.K = M, g.M = N, g.N = K;

@@ -526,6 +526,159 @@ dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void*
                                       const float* bias, int act, void* du, void* dx, void* dw, float* dbias,
                                       float* dcol_scale, void* workspace, size_t workspace_bytes, void* stream);
 
+/* -------------------------------------------------------------------------
+ * Rows held in 8-bit integers: int8 values, each the nearest step of its
+ * scale, and fp32 scales, one a row or one for each group of columns of a
+ * row. The layer norm and dora_quantize_rows write them, dora_matmul_int8
+ * multiplies them, dora_matmul_backward_int8 reads them as checkpoints.
+ *
+ *   scale = max |x| / 127      q = x / scale to the nearest integer, ties to
+ *                              the even one
+ *
+ * with the maximum over the row or the group and the fp32 scale as it is
+ * held. Zeros have scale 1; a scale is at least 2^-100. A NaN or an infinity
+ * makes the scale NaN or infinite and q 0, so that every value of that row or
+ * group stands for NaN.
+ * ---------------------------------------------------------------------- */
+
+/* 8-bit integers, where an output's 8-bit type is chosen. */
+#define DORA_I8 4
+
+/*
+ * Layer norm with the residual's addition:
+ *
+ *   h = x + residual
+ *   mean[t] = mean_j h[t,j]
+ *   rstd[t] = 1 / sqrt(mean_j (h[t,j] - mean[t])^2 + eps)
+ *   n[t,j]  = (h[t,j] - mean[t]) * rstd[t] * weight[j] + bias[j]
+ *   y = n in the storage type
+ *   q, scale: n in 8 bits, by q_dtype DORA_E4M3 (scale = max_j |n| / 448, as
+ *   dora_rms_norm) or DORA_I8 (above)
+ *
+ * Arguments as dora_rms_norm, and bias: fp32 [d] or NULL (zeros); mean: fp32
+ * [T] or NULL. h (with a residual), y, q, mean and rstd may each be NULL to
+ * skip them, but not y and q both; scale comes with q. y and q may be written
+ * together. h may be x or residual itself. One launch, each input read once
+ * from memory (rows of more than 16384 elements are read again).
+ *
+ * The statistics are of the unrounded fp32 sum, the variance of the values
+ * about their mean. A NaN or an infinity in a row makes its statistics, n and
+ * scale NaN. T == 0 does nothing; d == 0 has no norm and is refused when
+ * scale, mean or rstd is asked for. T and d are below 2^31, T * d at most 2^33.
+ * Errors: as dora_rms_norm; an unknown q_dtype with q is
+ * DORA_ERR_UNSUPPORTED_DTYPE.
+ */
+dora_status dora_layer_norm(const void* x, const void* residual, const float* weight, const float* bias, float eps,
+                            int dtype, int64_t T, int64_t d, void* h, void* y, void* q, int q_dtype, float* scale,
+                            float* mean, float* rstd, void* stream);
+
+/* Workspace bytes dora_layer_norm_backward needs for dweight or dbias. Host only. */
+dora_status dora_layer_norm_backward_workspace_size(int64_t T, int64_t d, int dtype, size_t* ws_bytes);
+
+/*
+ * Backward of the layer norm, from the h, mean and rstd of the forward (h is x
+ * where there is no residual), with nh = (h - mean) * rstd and a = dy * weight:
+ *
+ *   dx[t,j]    = rstd[t] * (a[t,j] - mean_j(a[t,:]) - nh[t,j] * mean_j(a[t,:] nh[t,:])) + dh[t,j]
+ *   dweight[j] = sum_t dy[t,j] * nh[t,j]        dbias[j] = sum_t dy[t,j]
+ *
+ * dx is the gradient of x and of residual alike; dh is the gradient that
+ * reaches h directly, or NULL. dx may be dy or dh itself. dweight and dbias
+ * may each be NULL; they are summed in fp32 in a fixed order, and need the
+ * workspace (256-byte aligned).
+ * Errors: as dora_layer_norm, and DORA_ERR_WORKSPACE.
+ */
+dora_status dora_layer_norm_backward(const void* dy, const void* dh, const void* h, const float* mean,
+                                     const float* rstd, const float* weight, int dtype, int64_t T, int64_t d, void* dx,
+                                     float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * x [T, d] of `dtype` to int8 rows: q int8 [T, d], and scale fp32 [T] (group
+ * 0: one a row) or [T, ceil(d / group)] (group 32, 64, 128 or 256 columns, the
+ * last group what is left). One launch. T == 0 does nothing, and so does
+ * d == 0 with groups; without them it is refused.
+ * Errors: DORA_ERR_INVALID_ARG (sizes, group, missing, misaligned or
+ * overlapping pointers), DORA_ERR_UNSUPPORTED_DTYPE, DORA_ERR_HIP.
+ */
+dora_status dora_quantize_rows(const void* x, int dtype, int64_t T, int64_t d, int64_t group, int8_t* q, float* scale,
+                               void* stream);
+
+/* x = q * scale, rounded once to `dtype`: the values that int8 rows stand for. Arguments and errors alike. */
+dora_status dora_dequantize_rows(const int8_t* q, const float* scale, int64_t T, int64_t d, int64_t group, int dtype,
+                                 void* x, void* stream);
+
+/* Workspace and plan of dora_matmul_int8, as those of dora_matmul (x and w are int8, t and b of 16 bits). Host only. */
+dora_status dora_matmul_int8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int aligned_operands,
+                                            size_t* ws_bytes);
+dora_status dora_matmul_int8_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, int aligned_operands, int64_t* info,
+                                       int n_info);
+
+/*
+ * Matrix product in 8-bit integers with a scale for each token and channel:
+ *
+ *   u[m,n] = row_scale[m] * w_scale[n] * sum_k x[m,k] w[n,k] + s * sum_l t[m,l] b[n,l]
+ *   y[m,n] = act(col_scale[n] * u[m,n] + bias[n]) + residual[m,n]
+ *
+ * x int8 [M, K] with row_scale fp32 [M], w int8 [N, K] with w_scale fp32 [N]:
+ * int8 rows with one scale a row (any int8 value is taken, -128 too). y, u and
+ * residual are of `out_dtype` (bf16, fp16 or fp32); t [M, r] and b [N, r], the
+ * low-rank pair, are of `out_dtype`, bf16 or fp16 (none with r == 0, and none
+ * with fp32 outputs). With w an int8 copy of the frozen W, b = B, s the
+ * adapter's and col_scale = g, y is the whole DoRA layer on an 8-bit base. The
+ * other arguments are those of dora_matmul, and y may be residual itself.
+ *
+ * The sum over k is exact in int32 (K is at most 131071); it is converted to
+ * fp32 and multiplied by the scales there (parts of a split depth, and the
+ * eighths of a few rows' depth, each by themselves). With a pair that sum is
+ * divided by s and multiplied again, so |s| is between 2^-64 and 2^64, or s is
+ * 0 and the pair is not read.
+ * Errors: as dora_matmul, and DORA_ERR_INVALID_ARG for K past its limit, such
+ * an s, and a pair with fp32 outputs.
+ */
+dora_status dora_matmul_int8(const int8_t* x, const float* row_scale, const int8_t* w, const float* w_scale, int64_t M,
+                             int64_t N, int64_t K, const float* col_scale, const void* t, const void* b, int64_t r,
+                             float s, const float* bias, int act, const void* residual, int out_dtype, void* y, void* u,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* An operand held as int8 rows: scale [rows] with group 0, else [rows, ceil(columns / group)]. */
+typedef struct dora_int8_rows {
+  const int8_t* q;
+  const float* scale;
+  int64_t group;
+} dora_int8_rows;
+
+/* Operands of dora_matmul_backward_int8 held as int8 rows, as its workspace query names them. */
+#define DORA_HELD_X 1
+#define DORA_HELD_W 2
+
+/*
+ * Device workspace dora_matmul_backward_int8 needs: `outputs` as for
+ * dora_matmul_backward (DORA_GRAD_ALIGNED speaks of x and w where they are not
+ * held as int8 rows), `held` the DORA_HELD_ bits. Host only.
+ */
+dora_status dora_matmul_backward_int8_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
+                                                     size_t* ws_bytes);
+
+/*
+ * dora_matmul_backward_rows with any of u, x and w held as int8 rows: u8, x8
+ * and w8 stand in for u, x and w, of which each is given in one of the two
+ * forms (the other NULL). u8 [M, N] and x8 [M, K] are activations packed in
+ * the forward; w8 [N, K] is a frozen 8-bit base (the gradient dw of such a w,
+ * if asked for, is that of the values it stands for).
+ *
+ *   z = col_scale[n] * u + bias[n]   with u = u8.q * its scale in fp32
+ *   dx = du (w8.q * its scale)       dw = du^T (x8.q * its scale)
+ *
+ * The products' operands are of the storage type, so x8 and w8 are rounded to
+ * it, as du is. Everything else, the workspace and the errors are as there.
+ */
+dora_status dora_matmul_backward_int8(const void* dy, const void* u, const dora_int8_rows* u8, const void* x,
+                                      const dora_int8_rows* x8, const void* w, const dora_int8_rows* w8, int dtype,
+                                      int64_t M, int64_t N, int64_t K, const float* row_scale, const float* col_scale,
+                                      const float* bias, int act, void* du, void* dx, void* dw, float* dbias,
+                                      float* dcol_scale, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
