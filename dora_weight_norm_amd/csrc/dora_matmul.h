@@ -38,8 +38,8 @@ struct GemmArgs {
   int stages;              // stages of the whole depth
   int stages_per_split;
   float* part;             // [splits][M][N] fp32 partial sums (splits > 1)
-  // 8-bit integers: the columns' scales; with a pair also the rows' (the
-  // epilogue's otherwise) and 1 / s.
+  // 8-bit integers: the columns' scales; with a pair, and in the walking kernel,
+  // also the rows' (the epilogue's otherwise) and 1 / s.
   const float* w_scale;
   const float* pair_rows;
   float inv_s;
@@ -48,7 +48,10 @@ struct GemmArgs {
 
 // Kernels: tiles of 256, 128 or 64 rows and columns, or the few-rows kernel on
 // 8 rows by 16 columns, 16 by 16 or 32 by 32.
-enum MatmulTile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4, kFew32 = 5 };
+// 8-bit integers have a kernel of their own for up to 8 or 16 rows.
+enum MatmulTile : int {
+  kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4, kFew32 = 5, kWalk8 = 6, kWalk16 = 7
+};
 
 struct MatmulPlan {
   int cfg;

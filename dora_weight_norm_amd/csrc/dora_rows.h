@@ -180,11 +180,11 @@ __device__ __forceinline__ uint32_t row_max_bits(uint32_t v, uint32_t* lds) {
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-// scale = top / most (448 in e4m3, 127 in integers): 1 for a row of zeros, at
-// least kMinScale otherwise; NaN or infinite where top is.
-__device__ __forceinline__ float scale_of(uint32_t top_bits, float most = kE4m3Max) {
+// scale = top / 448: 1 for a row of zeros, at least kMinScale otherwise; NaN
+// or infinite where top is.
+__device__ __forceinline__ float scale_of(uint32_t top_bits) {
   const float top = __uint_as_float(top_bits);
-  const float s = top / most;
+  const float s = top / kE4m3Max;
   return top_bits == 0 ? 1.f : (s < kMinScale ? kMinScale : s);
 }
 
@@ -202,57 +202,81 @@ struct RowQuotient {
     const float q = n * inv;
     return fmaf(fmaf(-q, s, n), inv, q);
   }
-  // The integer nearest to n / scale (not to the rounded quotient), ties to the
-  // even one, as a float. A quotient that rounds to a tie comes from one side of
-  // it or from the tie itself, which the sign of the exact remainder tells: rows
-  // of few significant bits meet it often (half of the row's largest value is
-  // 63.5 steps). NaN, of rows with a NaN or an infinity, gives 0.
-  __device__ __forceinline__ float whole(float n) const {
-    const float q = (*this)(n);
-    const float k = rintf(q), d = q - k;
-    const float r = fmaf(-q, s, n);
-    const float w = fabsf(d) == 0.5f && r * d > 0.f ? k + 2.f * d : k;
-    return w == w ? w : 0.f;
+};
+
+// The scale of integers: 1 for a row of zeros, at least kMinScale otherwise, NaN
+// or infinite where the largest value is.
+__device__ __forceinline__ float int8_scale_of(uint32_t top_bits) {
+  const float s = __uint_as_float(top_bits) * (1.f / kInt8Max);
+  return top_bits == 0 ? 1.f : (s < kMinScale ? kMinScale : s);
+}
+
+// The integer nearest to n / scale (to the quotient itself, not to one rounded
+// in fp32), ties to the even one, in the low byte of the result: three 64-bit
+// operations a value. The reciprocal is good to 2^-45 and the quotient rounded
+// to steps of 2^-30, on which a tie lies and from which no other quotient of
+// two fp32 numbers is nearer to a tie than 2^-26; then to whole steps. NaN (of
+// rows with a NaN or an infinity) gives 0: its low bits are 0. Rows of few
+// significant bits meet ties often (half of the largest value is 63.5 steps),
+// and a quotient rounded in fp32 took them to either side. The same by an fp32
+// quotient, its remainder and a comparison took seventeen operations a value,
+// as long as the memory (8192 x 8192 bf16 in groups of 128).
+struct WholeSteps {
+  double inv;
+  __device__ __forceinline__ explicit WholeSteps(float scale) {
+    const double s = scale, r = __builtin_amdgcn_rcpf(scale);
+    inv = fma(r, fma(-s, r, 1.0), r);
+    if (!(scale <= 3.402823466e38f)) inv = __builtin_nan("");
+  }
+  __device__ __forceinline__ uint32_t operator()(float n) const {
+    constexpr double kFine = 0x1.8p22, kWhole = 0x1.8p52;
+    const double v = fma((double)n, inv, kFine) + (kWhole - kFine);
+    return (uint32_t)__builtin_bit_cast(uint64_t, v);
   }
 };
 
-// E values of |v| <= 127 that are whole, as bytes.
+// The low bytes of E words.
 template <int E>
-__device__ __forceinline__ void bytes_of(const float (&v)[E], uint32_t (&w)[E / 4]) {
+__device__ __forceinline__ void low_bytes(const uint32_t (&v)[E], uint32_t (&w)[E / 4]) {
 #pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
-    const uint32_t a = (uint32_t)(int)v[4 * i], b = (uint32_t)(int)v[4 * i + 1];
-    const uint32_t c = (uint32_t)(int)v[4 * i + 2], d = (uint32_t)(int)v[4 * i + 3];
-    // (bytes 0 of two words each, then the two halves)
-    w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u),
-                                 0x05040100u);
-  }
+  for (int i = 0; i < E / 4; ++i)   // (of two words each, then the two halves)
+    w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(v[4 * i + 3], v[4 * i + 2], 0x0c0c0400u),
+                                 __builtin_amdgcn_perm(v[4 * i + 1], v[4 * i], 0x0c0c0400u), 0x05040100u);
 }
 
 // E fp32 values of a row chunk as 8-bit integers.
 template <int E, bool STREAM = false>
 __device__ __forceinline__ void store_row_int8(uint8_t* row, int64_t k, int64_t d, const float (&f)[E],
-                                               const RowQuotient& quotient) {
-  float v[E];
+                                               const WholeSteps& steps) {
+  uint32_t v[E], w[E / 4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = quotient.whole(f[e]);
-  uint32_t w[E / 4];
-  bytes_of<E>(v, w);
+  for (int e = 0; e < E; ++e) v[e] = steps(f[e]);
+  low_bytes<E>(v, w);
   store_row_bytes<E, STREAM>(row, k, d, w);
 }
 
-// E fp32 values of a row chunk in the 8-bit type that `kind` names.
-template <int E, bool STREAM = false>
-__device__ __forceinline__ void store_row_8(uint8_t* row, int64_t k, int64_t d, const float (&f)[E],
-                                            const RowQuotient& quotient, int kind) {
+// C chunks of a row, NT threads apart, in the 8-bit type that `kind` names,
+// with the scale of the row's largest |value|, which it returns.
+template <int E, int NT, int C, bool STREAM>
+__device__ __forceinline__ float store_row_8(uint8_t* row, int lane, int64_t d, const float (&f)[C][E], uint32_t top,
+                                             int kind) {
   if (kind == kQInt8) {
-    store_row_int8<E, STREAM>(row, k, d, f, quotient);
-  } else {
+    const float s = int8_scale_of(top);
+    const WholeSteps steps(s);
+#pragma unroll
+    for (int c = 0; c < C; ++c) store_row_int8<E, STREAM>(row, (int64_t)(c * NT + lane) * E, d, f[c], steps);
+    return s;
+  }
+  const float s = scale_of(top);
+  const RowQuotient quotient(s);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
     float v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = quotient(f[e]);
-    store_row_q<E, STREAM>(row, k, d, v);
+    for (int e = 0; e < E; ++e) v[e] = quotient(f[c][e]);
+    store_row_q<E, STREAM>(row, (int64_t)(c * NT + lane) * E, d, v);
   }
+  return s;
 }
 
 // Threads and chunks a thread that hold a row of d elements; nt 0: too long.

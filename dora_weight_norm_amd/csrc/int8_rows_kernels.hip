@@ -69,11 +69,11 @@ __global__ __launch_bounds__(256) void quantize_groups_kernel(const T* x, RowSte
         const uint32_t o = (uint32_t)__shfl_xor((int)top, m, 64);
         top = o > top ? o : top;
       }
-      const float sc = scale_of(top, kInt8Max);
-      const RowQuotient quotient(sc);
+      const float sc = int8_scale_of(top);
+      const WholeSteps steps(sc);
       if (p[i].ok) {
         if (threadIdx.x % L == 0) scale[p[i].row * s.groups + (p[i].k >> s.shift)] = sc;
-        store_row_int8<E, STREAM>(q + p[i].row * s.d, p[i].k, s.d, f, quotient);
+        store_row_int8<E, STREAM>(q + p[i].row * s.d, p[i].k, s.d, f, steps);
       }
     }
   }

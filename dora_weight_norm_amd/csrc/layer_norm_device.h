@@ -167,12 +167,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
         }
       }
       top = row_max_bits<NT>(top, reinterpret_cast<uint32_t*>(red[par]) + 2 * (W - (NT == 64)));
-      const float s = scale_of(top, a.q8 == kQInt8 ? kInt8Max : kE4m3Max);
-      const RowQuotient quotient(s);
+      const float s = store_row_8<E, NT, C, STREAM>(static_cast<uint8_t*>(a.q) + t * a.d, lane, a.d, f, top, a.q8);
       if (lane == 0) a.scale[t] = s;
-      uint8_t* qr = static_cast<uint8_t*>(a.q) + t * a.d;
-#pragma unroll
-      for (int c = 0; c < C; ++c) store_row_8<E, STREAM>(qr, (int64_t)(c * NT + lane) * E, a.d, f[c], quotient, a.q8);
     }
   }
 }
@@ -229,9 +225,8 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs a) 
         for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mean) * rs, w[e], b[e]);
       }
     };
-    float s = 1.f;
+    uint32_t top = 0;
     if (a.q) {
-      uint32_t top = 0;
       for (int64_t k = (int64_t)threadIdx.x * E; k < a.d; k += NT * E) {
         float f[E];
         load(k, f);
@@ -243,17 +238,19 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs a) 
         }
       }
       top = row_max_bits<NT>(top, reinterpret_cast<uint32_t*>(red[par]) + 2 * W);
-      s = scale_of(top, a.q8 == kQInt8 ? kInt8Max : kE4m3Max);
-      if (threadIdx.x == 0) a.scale[t] = s;
+      if (threadIdx.x == 0) a.scale[t] = a.q8 == kQInt8 ? int8_scale_of(top) : scale_of(top);
     }
-    const RowQuotient quotient(s);
     for (int64_t k = (int64_t)threadIdx.x * E; k < a.d; k += NT * E) {
       float f[E];
       load(k, f);
       if (NORM && a.h) store_row_chunk<T>(static_cast<T*>(a.h) + t * a.d, k, a.d, f);
       normed(k, f);
       if (NORM && a.y) store_row_chunk<T>(static_cast<T*>(a.y) + t * a.d, k, a.d, f);
-      if (a.q) store_row_8<E>(static_cast<uint8_t*>(a.q) + t * a.d, k, a.d, f, quotient, a.q8);
+      // (one chunk of "lane" k / E)
+      if (a.q) {
+        const float(&one)[1][E] = reinterpret_cast<const float(&)[1][E]>(f);
+        store_row_8<E, NT, 1, false>(static_cast<uint8_t*>(a.q) + t * a.d, (int)(k / E), a.d, one, top, a.q8);
+      }
     }
   }
 }

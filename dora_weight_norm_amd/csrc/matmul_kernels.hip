@@ -71,39 +71,44 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
     bs[e] = (bias && e < nv) ? bias[n + e] : 0.f;
     sb[e] = sc[e] = 0.f;
   }
-  // Four rows' loads are in flight at a time.
+  // Four rows' loads are in flight at a time, and as int8 rows, which are fewer
+  // bytes of u, the next four's too.
   constexpr int U = 4;
+  struct Rows {
+    Raw8<T> y[U], u[U8 ? 1 : U];
+    uint32_t q[U8 ? U : 1][2];
+    float s[U8 ? U : 1];
+  };
   const int64_t step = (int64_t)gridDim.y * nl;
-  for (int64_t m0 = (int64_t)blockIdx.y * nl + ly; nv > 0 && m0 < M; m0 += U * step) {
-    Raw8<T> ry[U], ru[U8 ? 1 : U];
-    uint32_t rq[U][2];
-    float us[U];
+  auto load = [&](Rows& r, int64_t m0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t m = m0 + i * step;
       if (m < M) {
         // (du, which the products read next, is to stay in the caches)
-        ry[i] = load_raw8<T, true>(dy + m * N + n, nv);
+        r.y[i] = load_raw8<T, true>(dy + m * N + n, nv);
         if constexpr (U8) {
-          load_row_bytes<8, true>(u8.q + m * N, n, N, rq[i]);
-          us[i] = u8.scale[m * u8.groups + (n >> u8.shift)];
+          load_row_bytes<8, true>(u8.q + m * N, n, N, r.q[i]);
+          r.s[i] = u8.scale[m * u8.groups + (n >> u8.shift)];
         } else {
-          ru[i] = load_raw8<T, true>(u + m * N + n, nv);
+          r.u[i] = load_raw8<T, true>(u + m * N + n, nv);
         }
       }
     }
+  };
+  auto run = [&](const Rows& r, int64_t m0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t m = m0 + i * step;
       if (m >= M) continue;
       const float rs = row_scale ? row_scale[m] : 1.f;
       float y[8], v[8], o[8];
-      unpack8<T>(ry[i], y);
+      unpack8<T>(r.y[i], y);
       if constexpr (U8) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(rq[i][e / 4] >> (8 * (e % 4))) * us[i];
+        for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(r.q[i][e / 4] >> (8 * (e % 4))) * r.s[i];
       } else {
-        unpack8<T>(ru[i], v);
+        unpack8<T>(r.u[i], v);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = fmaf(cs[e], v[e], bs[e]);
@@ -125,6 +130,23 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
       } else {
         store8<T>(du + m * ldu + n, nv, o);
       }
+    }
+  };
+  const int64_t first = (int64_t)blockIdx.y * nl + ly;
+  if constexpr (U8) {
+    Rows a, b;
+    if (nv > 0) load(a, first);
+    for (int64_t m0 = first; nv > 0 && m0 < M; m0 += 2 * U * step) {
+      load(b, m0 + U * step);
+      run(a, m0);
+      load(a, m0 + 2 * U * step);
+      run(b, m0 + U * step);
+    }
+  } else {
+    for (int64_t m0 = first; nv > 0 && m0 < M; m0 += U * step) {
+      Rows r;
+      load(r, m0);
+      run(r, m0);
     }
   }
   if (sums == nullptr) return;   // uniform
@@ -249,6 +271,13 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* 
   }
 }
 
+// Whether the walking kernel takes a product of 8-bit integers: whole steps of
+// 128 bytes, eight a wave at most, a pair of one step a wave in whole chunks, and
+// two blocks of columns or more for a compute unit.
+bool int8_walks(int64_t M, int64_t N, int64_t K, int64_t r) {
+  return M <= 16 && K % 128 == 0 && K > 0 && K <= 8192 && r <= 512 && r % 8 == 0 && N >= 2 * 16 * kCUs;
+}
+
 // The backward's products on operands as they lie (16-bit types): `b` stored
 // [k][row], and with AT `a` too.
 template <typename T, bool AT>
@@ -322,6 +351,7 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
   choose_tile(M, N, up(K, KT) / KT, dtype, K % epc == 0 ? kFewOnGrid : kFewOffGrid, &p.cfg, &p.splits);
+  if (dtype == kInt8Operands && int8_walks(M, N, K, r)) p.cfg = M <= 8 ? kWalk8 : kWalk16, p.splits = 1;
   auto operand = [&](int64_t rows, int64_t depth, int es, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
     *pack = p.cfg < kFew8 && depth > 0 && (depth % (16 / es) != 0 || !(al & bit));
@@ -359,7 +389,7 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
   g.ep = ep;
   if (dtype == kInt8Operands) {
     g.w_scale = w_scale;
-    if (r > 0) {   // (the pair's products are added to scaled sums, and s multiplies both)
+    if (r > 0 || p.cfg >= kWalk8) {   // (the pair's products are added to scaled sums, and s multiplies both)
       g.pair_rows = ep.row_scale, g.ep.row_scale = nullptr;
       g.inv_s = 1.f / s;
     }

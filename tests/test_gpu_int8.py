@@ -550,3 +550,22 @@ def test_two_calls_at_once_on_two_streams():
     for pair in got:
         for g, w in zip(pair, want):
             assert torch.equal(g, w)
+
+
+# Up to 16 tokens, whole steps of 128 and two blocks of 16 columns for a compute unit: one workgroup a unit walks them.
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K,r", [(1, 8192, 128, 0), (1, 8193, 1152, 8), (7, 8200, 8192, 512), (8, 12300, 1024, 40),
+                                     (9, 8192, 8064, 0), (16, 28672, 256, 384), (13, 8207, 2048, 264), (2, 8192, 896, 64)])
+def test_walking_kernel(M, N, K, r, out):
+    o, rng = operands(M, N, K, 0 if out == "f32" else r, out, M + N + K)
+    check(o, rng, out, ACTS[(M + N + K) % 5], M % 2 == 0, True)
+    plain = {k: v for k, v in o.items() if k not in ("col_scale", "bias")}
+    check(plain, rng, out, "none", False, False)
+
+
+def test_products_beside_the_walking_kernel():
+    """What it does not take: a depth of no whole steps, one past 8192, a pair of no whole chunks or past a step a wave."""
+    for M, N, K, r in ((3, 8192, 1000, 16), (3, 8192, 8320, 16), (16, 8192, 1024, 20), (16, 8192, 1024, 520),
+                       (16, 8176, 1024, 16), (17, 8192, 1024, 16)):
+        o, rng = operands(M, N, K, r, "bf16", M + N + K)
+        check(o, rng, "bf16", "silu", True, False)
