@@ -158,6 +158,51 @@ __device__ __forceinline__ float row_sum(float v, float* lds) {
   return v;
 }
 
+// Sum over the wave, the same in every lane: over quads and rows of 16 by lane
+// permutes of the vector unit (a few cycles each, where a shuffle goes through
+// LDS), then over the four rows.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+__device__ __forceinline__ float row16_sum(float v) {   // over each row of 16 lanes
+  v += dpp<0xb1>(v);    // lane ^ 1
+  v += dpp<0x4e>(v);    // lane ^ 2
+  v += dpp<0x141>(v);   // mirror of eight
+  v += dpp<0x140>(v);   // mirror of sixteen
+  return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
+__device__ __forceinline__ uint32_t row16_max(uint32_t u) {
+  auto step = [&](uint32_t o) __attribute__((always_inline)) { u = o > u ? o : u; };
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0xb1, 0xf, 0xf, true));
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x4e, 0xf, 0xf, true));
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x141, 0xf, 0xf, true));
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x140, 0xf, 0xf, true));
+  return u;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t u) {
+  u = row16_max(u);
+  uint32_t m = (uint32_t)__builtin_amdgcn_readlane((int)u, 0);
+#pragma unroll
+  for (int i = 16; i < 64; i += 16) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)u, i);
+    m = o > m ? o : m;
+  }
+  return m;
+}
+
 // Largest |value| over the row, carried as its bits: among non-negative
 // floats the order of the bits is the order of the values, and a NaN's bits
 // are above infinity's, so a NaN anywhere comes out as a NaN.

@@ -17,8 +17,8 @@ namespace {
 // A workgroup of 256 threads is `bx` threads along a row by 256 / bx rows; an
 // item is one such step, `steps` of them along a row. kItems items' loads are
 // in flight at a time.
-constexpr int kItems = 4;
-constexpr int64_t kMostGroups = 2048;   // workgroups, eight a compute unit
+constexpr int kItems = 2;
+constexpr int64_t kMostGroups = 65536;   // workgroups
 
 struct RowSteps {
   int64_t T, d;
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void dequantize_rows_kernel(const uint8_t* q, 
     for (int i = 0; i < kItems; ++i) {
       p[i] = place_of<E>(s, it + i);
       if (p[i].ok) {
-        load_row_bytes<E, STREAM>(q + p[i].row * s.d, p[i].k, s.d, w[i]);
+        load_row_bytes<E>(q + p[i].row * s.d, p[i].k, s.d, w[i]);
         sc[i] = scale[p[i].row * s.groups + (p[i].k >> s.shift)];
       }
     }

@@ -6,10 +6,10 @@
 //   y = n, rounded once, or q = n / scale in e4m3 or int8, rounded once, with
 //   scale = max_j |n| / 448 or / 127
 //
-// The statistics are of the fp32 sum x + residual and in two passes over the
-// registers that hold the row: the variance is a sum of squares of v, which
-// loses nothing where the mean is far larger than the spread (a sum of h^2
-// would), at the price of one more reduction.
+// The statistics are of the fp32 sum x + residual. All of a row is taken relative
+// to its first value, and the variance is a sum of squares about means, so that
+// neither loses digits where the mean is far larger than the spread (a sum of
+// h^2 would lose them all).
 //
 // HBM bound, as the RMS norm, whose row loads, shapes and grids these kernels
 // share: a row is read once into the registers of one wave or one workgroup.
@@ -49,6 +49,13 @@ __device__ __forceinline__ void load_bias(const float* b, int64_t k, int64_t d, 
   }
 }
 
+// How many of a chunk's elements [k, k + E) lie in a row of d.
+template <int E>
+__device__ __forceinline__ int chunk_left(int64_t k, int64_t d) {
+  const int64_t left = d - k;
+  return (int)(left < E ? left : E);
+}
+
 // The same address, which the compiler takes for another: what is read there in
 // a loop stays in it.
 __device__ __forceinline__ const float* reread(const float* p) {
@@ -56,28 +63,70 @@ __device__ __forceinline__ const float* reread(const float* p) {
   return p;
 }
 
-// The row's statistics and n in place of h, from the C chunks that each of NT
-// threads holds; past d the values do not count.
+// The row's statistics, from the C chunks that each of NT threads holds; past d
+// the values do not count. Each wave takes the mean of its own values and their
+// squares about it; the waves' (count, mean, squares) join as those of any
+// parts do: the squares about the whole mean are the parts' own and count times
+// the square of each part's distance to it (Chan, Golub, LeVeque 1979). One
+// exchange between the waves serves both.
 template <int NT, int C, int E>
 __device__ __forceinline__ void row_stats(const float (&f)[C][E], int lane, int64_t d, float eps, float* red,
                                           float& mean, float& rstd) {
+  constexpr int W = NT / 64;
   float s = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int e = 0; e < E; ++e) s += f[c][e];
-  mean = row_sum<NT>(s, red) / (float)d;
+  // values of wave w
+  auto count = [&](int w) __attribute__((always_inline)) {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t left = d - (int64_t)(c * NT + w * 64) * E;
+      n += left < 0 ? 0 : (left < 64 * E ? (int)left : 64 * E);
+    }
+    return (float)n;
+  };
+  const int wave = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  const float own = count(wave);
+  const float mu = own > 0.f ? wave_sum(s) / own : 0.f;
   float q = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int64_t k = (int64_t)(c * NT + lane) * E;
+    const int n = chunk_left<E>((int64_t)(c * NT + lane) * E, d);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float v = k + e < d ? f[c][e] - mean : 0.f;
+      const float v = e < n ? f[c][e] - mu : 0.f;
       q = fmaf(v, v, q);
     }
   }
-  rstd = 1.f / sqrtf(row_sum<NT>(q, red + (NT > 64 ? NT / 64 : 0)) / (float)d + eps);
+  q = wave_sum(q);
+  mean = mu;
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) red[2 * wave] = mu, red[2 * wave + 1] = q;
+    __syncthreads();
+    // (lane w % 16 takes wave w's, so that each row of 16 lanes holds them all)
+    static_assert(W <= 16, "the waves of a workgroup are lanes of a row of 16");
+    const int w = threadIdx.x & 15;
+    const float n = w < W ? count(w) : 0.f, m = w < W ? red[2 * w] : 0.f;
+    mean = row16_sum(n * m) / (float)d;
+    q = row16_sum(fmaf(n * (m - mean), m - mean, w < W ? red[2 * w + 1] : 0.f));
+  }
+  rstd = 1.f / sqrtf(q / (float)d + eps);
+}
+
+// Largest |value| of the row, as its bits (see row_max_bits).
+template <int NT>
+__device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t* lds) {
+  v = wave_max(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    const int w = threadIdx.x & 15;
+    v = row16_max(w < NT / 64 ? lds[w] : 0u);
+  }
+  return v;
 }
 
 // NT threads and C chunks a thread to a row; workgroups of 256 threads hold
@@ -95,19 +144,23 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
   const int64_t t0 = (int64_t)blockIdx.x * RPW + (NT == 64 ? threadIdx.x >> 6 : 0);
   const bool has_res = NORM && a.residual != nullptr;
   u32x4 xv[C], rv[C];
+  T x0 = T(0), r0 = T(0);   // (NORM: the row's first values)
   auto load = [&](int64_t t) __attribute__((always_inline)) {
     const T* x = static_cast<const T*>(a.x) + t * a.d;
 #pragma unroll
     for (int c = 0; c < C; ++c) xv[c] = load_row_chunk<T, STREAM && LINES>(x, (int64_t)(c * NT + lane) * E, a.d);
+    if (NORM) x0 = x[0];
     if (has_res) {
       const T* res = static_cast<const T*>(a.residual) + t * a.d;
+      r0 = res[0];
 #pragma unroll
       for (int c = 0; c < C; ++c) rv[c] = load_row_chunk<T, STREAM && LINES>(res, (int64_t)(c * NT + lane) * E, a.d);
     }
   };
-  if (t0 < a.T) load(t0);
-  // (four chunks of 1024 threads, which have 128 registers each, read them anew for each row)
-  constexpr bool KEEP = NORM && NT * C < 4096;
+  // (Four chunks of 1024 threads, which have 128 registers each: no row ahead, and
+  // the weights are read anew for each row.)
+  constexpr bool AHEAD = NT * C < 4096, KEEP = NORM && AHEAD;
+  if (AHEAD && t0 < a.T) load(t0);
   float w[C][E], b[C][E];
   if constexpr (KEEP) {
 #pragma unroll
@@ -117,7 +170,9 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
     }
   }
   for (int64_t t = t0; t < a.T; t += (int64_t)gridDim.x * RPW, par ^= 1) {
+    if (!AHEAD) load(t);
     float f[C][E];
+    const float origin = to_f32(x0) + (has_res ? to_f32(r0) : 0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       unpack<T, E>(xv[c], f[c]);
@@ -129,7 +184,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
       }
     }
     // (h may be x or residual itself: other rows' loads are of other rows)
-    if (t + (int64_t)gridDim.x * RPW < a.T) load(t + (int64_t)gridDim.x * RPW);
+    if (AHEAD && t + (int64_t)gridDim.x * RPW < a.T) load(t + (int64_t)gridDim.x * RPW);
     if constexpr (NORM) {
       if (a.h) {
         T* h = static_cast<T*>(a.h) + t * a.d;
@@ -137,8 +192,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
         for (int c = 0; c < C; ++c) store_row_chunk<T, STREAM>(h, (int64_t)(c * NT + lane) * E, a.d, f[c]);
       }
       float mean, rs;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int n = chunk_left<E>((int64_t)(c * NT + lane) * E, a.d);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[c][e] = e < n ? f[c][e] - origin : 0.f;
+      }
       row_stats<NT, C, E>(f, lane, a.d, a.eps, red[par], mean, rs);
-      if (lane == 0 && a.mean) a.mean[t] = mean;
+      if (lane == 0 && a.mean) a.mean[t] = origin + mean;
       if (lane == 0 && a.rstd) a.rstd[t] = rs;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -159,14 +220,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
       uint32_t top = 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int64_t k = (int64_t)(c * NT + lane) * E;
+        const int n = chunk_left<E>((int64_t)(c * NT + lane) * E, a.d);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const uint32_t v = k + e < a.d ? abs_bits(f[c][e]) : 0u;
+          const uint32_t v = e < n ? abs_bits(f[c][e]) : 0u;
           top = v > top ? v : top;
         }
       }
-      top = row_max_bits<NT>(top, reinterpret_cast<uint32_t*>(red[par]) + 2 * (W - (NT == 64)));
+      top = row_top<NT>(top, reinterpret_cast<uint32_t*>(red[par]) + 2 * (W - (NT == 64)));
       const float s = store_row_8<E, NT, C, STREAM>(static_cast<uint8_t*>(a.q) + t * a.d, lane, a.d, f, top, a.q8);
       if (lane == 0) a.scale[t] = s;
     }

@@ -30,20 +30,15 @@ struct LayerNormBwdArgs {
 // Both sums over the NT threads that share a row, in a fixed order.
 template <int NT>
 __device__ __forceinline__ void row_sum2(float& u, float& v, float* lds) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    u += __shfl_xor(u, m, 64);
-    v += __shfl_xor(v, m, 64);
-  }
+  u = wave_sum(u), v = wave_sum(v);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) {
       lds[2 * (threadIdx.x >> 6)] = u;
       lds[2 * (threadIdx.x >> 6) + 1] = v;
     }
     __syncthreads();
-    u = lds[0], v = lds[1];
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) u += lds[2 * i], v += lds[2 * i + 1];
+    const int w = threadIdx.x & 15;
+    u = row16_sum(w < NT / 64 ? lds[2 * w] : 0.f), v = row16_sum(w < NT / 64 ? lds[2 * w + 1] : 0.f);
   }
 }
 

@@ -273,9 +273,18 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* 
 
 // Whether the walking kernel takes a product of 8-bit integers: whole steps of
 // 128 bytes, eight a wave at most, a pair of one step a wave in whole chunks, and
-// two blocks of columns or more for a compute unit.
+// two blocks of columns or more for a compute unit; up to 8 rows, for which the
+// few-rows kernel reads fewer tokens, three, and depths of 2048 and more, since
+// a block's bytes are all that a unit has on their way. Measured, the few-rows
+// kernel against this, us on the GPU:
+//    1, 8 and 16 x  8192 x 8192   13.1, 14.7; 15.2, 15.3; 19.5, 16.3
+//    1, 8 and 16 x 12288 x 8192   21.6, 19.6; 22.3, 20.2; 27.7, 20.9
+//    1, 8 and 16 x 28672 x 8192   43.0, 37.6; 48.1, 39.5; 59.0, 40.2
+//    1, 8 and 16 x 28672 x 2048   17.2, 16.2; 19.9, 16.0; 24.1, 16.5
+//    1, 8 and 16 x 16384 x 1024    7.8,  8.3;  8.7,  8.4; 10.4,  9.0
 bool int8_walks(int64_t M, int64_t N, int64_t K, int64_t r) {
-  return M <= 16 && K % 128 == 0 && K > 0 && K <= 8192 && r <= 512 && r % 8 == 0 && N >= 2 * 16 * kCUs;
+  if (M > 16 || K == 0 || K % 128 != 0 || K > 8192 || r > 512 || r % 8 != 0) return false;
+  return M > 8 ? N >= 2 * 16 * kCUs : N >= 3 * 16 * kCUs && K >= 2048;
 }
 
 // The backward's products on operands as they lie (16-bit types): `b` stored

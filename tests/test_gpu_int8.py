@@ -554,8 +554,8 @@ def test_two_calls_at_once_on_two_streams():
 
 # Up to 16 tokens, whole steps of 128 and two blocks of 16 columns for a compute unit: one workgroup a unit walks them.
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("M,N,K,r", [(1, 8192, 128, 0), (1, 8193, 1152, 8), (7, 8200, 8192, 512), (8, 12300, 1024, 40),
-                                     (9, 8192, 8064, 0), (16, 28672, 256, 384), (13, 8207, 2048, 264), (2, 8192, 896, 64)])
+@pytest.mark.parametrize("M,N,K,r", [(1, 12288, 2048, 0), (1, 12305, 2176, 8), (7, 12300, 8192, 512), (8, 16400, 2944, 40),
+                                     (9, 8192, 8064, 0), (16, 28672, 256, 384), (13, 8207, 2048, 264), (12, 8192, 128, 64)])
 def test_walking_kernel(M, N, K, r, out):
     o, rng = operands(M, N, K, 0 if out == "f32" else r, out, M + N + K)
     check(o, rng, out, ACTS[(M + N + K) % 5], M % 2 == 0, True)
