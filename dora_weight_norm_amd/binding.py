@@ -1038,8 +1038,9 @@ def dora_matmul_backward_int8(dy, u, x, w, col_scale=None, bias=None, act: str =
         pw = w8 = None
     if not need_dw:
         px = x8 = None
+    at = [p or 0 for p in (px, pw, x8 and x8.q, w8 and w8.q)]
     outputs = (GRAD_DX * need_dx + GRAD_DW * need_dw + GRAD_SUMS * (need_dbias or need_dcol_scale)
-               + GRAD_DU * (du.data_ptr() % 16 == 0) + GRAD_ALIGNED * ((px or 0) % 16 == 0 and (pw or 0) % 16 == 0))
+               + GRAD_DU * (du.data_ptr() % 16 == 0) + GRAD_ALIGNED * all(p % 16 == 0 for p in at))
     held = HELD_X * (x8 is not None) + HELD_W * (w8 is not None)
     need = _size_of("dora_matmul_backward_int8_workspace_size", M, N, K, code, outputs, held)
     workspace = _space(workspace, need, stream, dev)

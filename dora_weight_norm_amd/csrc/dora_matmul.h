@@ -43,6 +43,11 @@ struct GemmArgs {
   const float* w_scale;
   const float* pair_rows;
   float inv_s;
+  // b as int8 rows [k][column]: the scales, b_groups a k, of groups of
+  // 2^b_shift columns.
+  const float* b_scale;
+  int64_t b_groups;
+  int b_shift;
   Epilogue ep;
 };
 
@@ -65,6 +70,9 @@ struct MatmulPlan {
 // Operand type of the products in 8-bit integers, beside the C ABI's codes.
 constexpr int kInt8Operands = 4;
 hipError_t gemm_int8(const GemmArgs& g, int out_dtype, int cfg, hipStream_t st);
+// The backward's products whose b is int8 rows: tiles of 256 or 128 rows, `a`
+// stored [k][row] with a_across.
+hipError_t gemm_rows8(const GemmArgs& g, int dtype, bool a_across, int cfg, hipStream_t st);
 
 // The product's plan (dtype: a C ABI code or kInt8Operands, whose t and b are of
 // 16 bits); `al` is a bit mask of the operands whose pointers are
@@ -75,7 +83,8 @@ struct MatmulBackwardPlan {
   bool du_direct;                               // du is written into the caller's array alone
   bool direct;                                  // the products read x, w and du in their own layout,
   bool copy;                                    // x and w from copies with a row stride of ldk
-  bool x8, w8;                                  // x, w are int8 rows, brought back into such copies
+  bool x8, w8;                                  // x, w are int8 rows,
+  bool x8_tile, w8_tile;                        // read as such by the tile kernel, or brought back into such copies
   int64_t rows;                                 // row blocks of the element-wise pass
   int64_t ldn, ldm, ldk;                        // padded N, M and K
   int cfg_dx, cfg_dw, splits_dx, splits_dw;

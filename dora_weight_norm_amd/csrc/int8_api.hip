@@ -201,7 +201,9 @@ dora_status dora_matmul_backward_int8(const void* dy, const void* u, const dora_
                       {dcol_scale, N * 4, 4}};
   const unsigned same[] = {1u, 0u, 0u, 0u, 0u};   // du may be dy itself
   if (!buffers_ok(in, 13, out, 5, same)) return DORA_ERR_INVALID_ARG;
-  const bool al = (dw == nullptr || x8 != nullptr || aligned(x, 16)) && (dx == nullptr || w8 != nullptr || aligned(w, 16));
+  // (of each operand the form that is given; the other one is null)
+  const bool al = (dw == nullptr || (aligned(x, 16) && aligned(held.x.q, 16))) &&
+                  (dx == nullptr || (aligned(w, 16) && aligned(held.w.q, 16)));
   const MatmulBackwardPlan p =
       plan_matmul_backward(M, N, K, dtype, dx != nullptr, dw != nullptr, dbias != nullptr || dcol_scale != nullptr,
                            du != nullptr && aligned(du, 16), al, x8 != nullptr, w8 != nullptr);

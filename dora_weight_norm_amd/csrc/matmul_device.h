@@ -377,6 +377,21 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // direct load in flight and waits for them all.)
 __device__ __forceinline__ s16x4 tr_load(lds_s16x4* __restrict p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
 
+// Two values as 16-bit ones, round to nearest even.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {a, b};
+  if constexpr (std::is_same<T, bf16_t>::value) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
+// (likewise)
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+__device__ __forceinline__ void store_lds(lds_u32x4* __restrict p, u32x4 v) { *p = v; }
+
 template <int R>
 __device__ __forceinline__ u32x4 read_tr(const char* unit, int r0, int s, int lane) {
   const int g = lane >> 4, m = lane & 15;
@@ -410,12 +425,19 @@ __device__ __forceinline__ u32x4 read_tr(const char* unit, int r0, int s, int la
 // of fragments and reads the next step's while this step's matrix instructions
 // run.
 // ---------------------------------------------------------------------------
-template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT, bool BT>
+// B8: the columns are int8 rows [k][column] with a scale for each k and group of
+// columns, brought to the 16-bit type on their way to LDS. A lane takes 16
+// bytes of a k at a time, loaded one period ahead, and converts and stores them
+// element by element between the period's matrix instructions: each element of
+// the stage once a workgroup, where a conversion behind the transposing reads
+// would do it in every wave.
+template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT, bool BT, bool B8 = false>
 __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, KT = 128 / ESZ;
   constexpr int NW = WM * WN, MT = WM * MB * 32, NT = WN * NB * 32;
   constexpr int UNIT = (MT > NT ? MT : NT) * 128;           // bytes of a ring unit
-  constexpr int ABLK = MT / 8 / NW, BBLK = NT / 8 / NW;   // 1 KiB blocks per wave per stage
+  // 1 KiB blocks per wave per stage (B8: 16 bytes a lane, which become 32)
+  constexpr int ABLK = MT / 8 / NW, BBLK = NT / (B8 ? 16 : 8) / NW;
   constexpr int BPW = ABLK + BBLK;
   constexpr int STEPS = 8 / (2 * FC);
   // 8-bit integers: their sums come first, are converted and scaled in the
@@ -427,7 +449,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   constexpr int EPW = NB * 32 + 4;                         // floats of an epilogue row (padded: no bank conflicts)
   static_assert(MT % (8 * NW) == 0 && NT % (8 * NW) == 0, "a stage splits evenly over the waves");
   constexpr int RING = (2 * P + 1) * UNIT;
-  static_assert((NW * 32 * EPW + (I8 ? NW * NB * 32 : 0)) * 4 <= RING && (!I8 || NB * 32 <= 64), "the epilogue fits the ring");
+  static_assert((NW * 32 * EPW + (I8 ? NW * NB * 32 : 0)) * 4 <= RING, "the epilogue fits the ring");
   static_assert(RING <= 160 * 1024, "gfx950 has 160 KiB of LDS");
   static_assert(STEPS % 2 == 0, "step s of every stage uses fragment set s & 1");
   extern __shared__ __align__(1024) char lds[];
@@ -483,6 +505,47 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       const uint32_t off = chunk * 16 < left ? at : kOob;
       const __amdgpu_buffer_rsrc_t rs = pr ? pair.rsrc : main.rsrc;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, k0, 0, 0);
+    }
+  };
+  // B8: a lane's 16 bytes j are those of k (wave * 64 + lane) / CPK + j * KPJ and
+  // of column 16 ((lane) % CPK) of the tile.
+  constexpr int CPK = NT / 16, KPJ = NW * 64 / CPK, PER_STEP = BBLK * 16 / STEPS;
+  static_assert(!B8 || (BT && !PAIR && ESZ == 2 && P == 2 && BBLK * KPJ == 64 && (PER_STEP == 16 || PER_STEP == 8)),
+                "a step converts one or half of a lane's 16 bytes");
+  u32x4 qv[B8 ? BBLK : 1], qout = {0u, 0u, 0u, 0u};
+  float qs[B8 ? BBLK : 1];
+  const int qk = (int)threadIdx.x / CPK, qc = (int)threadIdx.x % CPK;
+  const bool q_in = n0 + qc * 16 < g.N;   // (rows are whole chunks)
+  const uint32_t q_off = q_in ? (uint32_t)(qk * g.ldb + n0 + qc * 16) : kOob;
+  const uint32_t s_off = (uint32_t)(qk * g.b_groups + ((n0 + qc * 16) >> g.b_shift)) * 4u;
+  auto load_q = [&](int i, int j) __attribute__((always_inline)) {
+    const int64_t left = i < st1 ? g.K - (int64_t)i * 64 : 0, ks = left < 0 ? 0 : left;
+    const int64_t qb = ks * g.ldb, sb8 = ks * g.b_groups * 4;
+    const __amdgpu_buffer_rsrc_t rq = make_rsrc(static_cast<const char*>(g.b) + (int64_t)i * 64 * g.ldb,
+                                                (uint32_t)(qb < 0x7fffffff ? qb : 0x7fffffff));
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(g.b_scale + (int64_t)i * 64 * g.b_groups,
+                                                (uint32_t)(sb8 < 0x7fffffff ? sb8 : 0x7fffffff));
+    const uint32_t qo = q_off + (uint32_t)(j * KPJ) * (uint32_t)g.ldb;
+    const uint32_t so = s_off + (uint32_t)(j * KPJ) * (uint32_t)g.b_groups * 4u;
+    qv[j] = __builtin_amdgcn_raw_buffer_load_b128(rq, qo, 0, 0);
+    qs[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, so, 0, 0));
+  };
+  // Element e of the stage's BBLK * 16 of this lane, into the unit; with the last
+  // of 16 bytes the next stage's take their registers.
+  float qf = 0.f;
+  auto convert = [&](int unit, int e, int next) __attribute__((always_inline)) {
+    if constexpr (B8) {
+      const int j = e / 16, b = e % 16;
+      const float f = (float)(int8_t)(qv[j][b / 4] >> (8 * (b % 4))) * qs[j];
+      if (b % 2)
+        qout[b % 8 / 2] = pack2<T>(qf, f);
+      else
+        qf = f;
+      if (b % 8 == 7) {
+        const int k = qk + j * KPJ, c = qc * 2 + b / 8;
+        store_lds((lds_u32x4*)(lds + unit + k * (NT * 2) + ((c ^ trswz<NT>(k)) * 16)), qout);
+      }
+      if (b == 15) load_q(next, j);
     }
   };
   auto issue_a = [&](int i, int unit, int b) __attribute__((always_inline)) { issue(sa, sa2, i, unit, b, Tag<AT>{}); };
@@ -549,7 +612,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // source but not the matrix instructions between them.
   constexpr int RPM = (2 * ND + NM - 1) / NM;
   Frag F[2];
-  auto step = [&](Frag& cur, Frag& nxt, int ua, int ub, int s, int i, int ul, int um, int l0, int l1, auto pair)
+  // (B8: an eighth or sixteenth of the period's conversions, part t of STEPS, and
+  // the rows' loads.)
+  auto step = [&](Frag& cur, Frag& nxt, int ua, int ub, int s, int i, int ul, int um, int l0, int l1, int t, auto pair)
       __attribute__((always_inline)) {
     using TX = std::conditional_t<I8 && decltype(pair)::value, TP, T>;
 #pragma unroll
@@ -557,14 +622,22 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 #pragma unroll
       for (int q = m * RPM; q < (m + 1) * RPM && q < ND; ++q)
         read(ua, ub, s, nxt, q);
+      if constexpr (B8) {
 #pragma unroll
-      for (int l = l0; l < l1; ++l)
-        if ((l - l0) * NM / (l1 - l0) == m) {
-          if (l < BBLK)
-            issue_b(i + P, ul, l);
-          else
-            issue_a(i + P + 1, um, l - BBLK);
-        }
+        for (int l = 0; l < ABLK / STEPS; ++l)
+          if (l * NM / (ABLK / STEPS) == m) issue_a(i + P + 1, um, t * (ABLK / STEPS) + l);
+#pragma unroll
+        for (int e = m * PER_STEP / NM; e < (m + 1) * PER_STEP / NM; ++e) convert(ul, t * PER_STEP + e, i + P + 1);
+      } else {
+#pragma unroll
+        for (int l = l0; l < l1; ++l)
+          if ((l - l0) * NM / (l1 - l0) == m) {
+            if (l < BBLK)
+              issue_b(i + P, ul, l);
+            else
+              issue_a(i + P + 1, um, l - BBLK);
+          }
+      }
       acc[m / NB][m % NB] = Op<TX>::run(cur.b[m % NB], cur.a[m / NB], acc[m / NB][m % NB]);   // (turned)
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -576,26 +649,48 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
     return at >= RING ? at - RING : at;
   };
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
+  for (int j = 0; j < (B8 ? 1 : P); ++j) {
 #pragma unroll
     for (int b = 0; b < ABLK; ++b) issue_a(st0 + j, 2 * j * UNIT, b);
-    if (j + 1 < P) {
+    if (!B8 && j + 1 < P) {
 #pragma unroll
       for (int b = 0; b < BBLK; ++b) issue_b(st0 + j, (2 * j + 1) * UNIT, b);
     }
   }
   // (the columns of stage P - 1 and the rows of stage P: one period's loads, of
   // which the first step's part goes out here)
-  constexpr int L1 = BPW / STEPS;
-  constexpr int LATER = (P - 1) * ABLK + (P - 2) * BBLK;   // loads younger than the next stage's
+  constexpr int L1 = B8 ? ABLK / STEPS : BPW / STEPS;
+  // Loads younger than the next stage's (B8: of the rows', after the last of which
+  // come a period's rows and two loads for each of a lane's 16 bytes).
+  constexpr int LATER = B8 ? ABLK + 2 * BBLK : (P - 1) * ABLK + (P - 2) * BBLK;
+  if constexpr (B8) {
+    // (In a period's order, so that the waits of the loop, which are those of its
+    // first round too, leave as many loads in flight as its other rounds could.)
 #pragma unroll
-  for (int l = 0; l < L1; ++l) {
-    if (l < BBLK)
-      issue_b(st0 + P - 1, (2 * P - 1) * UNIT, l);
-    else
-      issue_a(st0 + P, 2 * P * UNIT, l - BBLK);
+    for (int j = 0; j < BBLK; ++j) load_q(st0, j);
+#pragma unroll
+    for (int t = 0; t <= STEPS; ++t) {
+      const bool first = t < STEPS;
+#pragma unroll
+      for (int l = 0; l < L1; ++l)
+        issue_a(first ? st0 + 1 : st0 + 2, first ? 2 * UNIT : 4 * UNIT, (first ? t * L1 : 0) + l);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = 0; e < PER_STEP; ++e)
+        convert(first ? UNIT : 3 * UNIT, (first ? t * PER_STEP : 0) + e, first ? st0 + 1 : st0 + 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_vm_lgkm0<LATER + L1>();
+  } else {
+#pragma unroll
+    for (int l = 0; l < L1; ++l) {
+      if (l < BBLK)
+        issue_b(st0 + P - 1, (2 * P - 1) * UNIT, l);
+      else
+        issue_a(st0 + P, 2 * P * UNIT, l - BBLK);
+    }
+    wait_vm_lgkm0<LATER + L1>();
   }
-  wait_vm_lgkm0<LATER + L1>();
   barrier_keep_loads();
 #pragma unroll
   for (int q = 0; q < ND; ++q) read(0, UNIT, 0, F[0], q);
@@ -606,13 +701,13 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 #pragma unroll
     for (int s = 0; s + 1 < STEPS; ++s)
       step(F[s & 1], F[(s + 1) & 1], unit(0), unit(1), s + 1, i - 1, unit(2 * P - 1), unit(2 * P),
-           BPW * (s + 1) / STEPS, BPW * (s + 2) / STEPS, pair);
+           BPW * (s + 1) / STEPS, BPW * (s + 2) / STEPS, s + 1, pair);
     // This wave has read all of stage i, and its loads of stage i + 1 have
     // landed; younger ones stay in flight. Past the barrier the units of stage
     // i take the next period's loads.
     wait_vm_lgkm0<LATER>();
     barrier_keep_loads();
-    step(F[1], F[0], unit(2), unit(3), 0, i, unit(0), unit(1), 0, L1, pair);
+    step(F[1], F[0], unit(2), unit(3), 0, i, unit(0), unit(1), 0, L1, 0, pair);
     u0 = unit(2);
   };
   // Scales of the four columns that a lane holds in accumulators 4q to 4q + 3 of
@@ -677,8 +772,11 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // registers for them beside the accumulators of the 256-row tile)
   float* wl = reinterpret_cast<float*>(lds) + NW * 32 * EPW + wave * NB * 32;
   if constexpr (I8 && !PAIR) {
-    const int64_t c = n0 + wn * NB * 32 + lane;
-    if (lane < NB * 32) wl[lane] = g.w_scale[c < g.N ? c : g.N - 1];
+#pragma unroll
+    for (int i = lane; i < NB * 32; i += 64) {
+      const int64_t c = n0 + wn * NB * 32 + i;
+      wl[i] = g.w_scale[c < g.N ? c : g.N - 1];
+    }
   }
   constexpr int IT = MB * PB / 2;
   const bool has_res = g.ep.residual != nullptr && g.splits == 1;
@@ -1050,12 +1148,13 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(PackJobs p) {
   *reinterpret_cast<u32x4*>(dst + r * lb + c) = load_bounded(src + r * kb, c, kb);
 }
 
-template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT = false, bool BT = false>
+template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT = false, bool BT = false,
+          bool B8 = false>
 hipError_t launch_tile(GemmArgs g, hipStream_t st) {
   constexpr int MT = WM * MB * 32, NT = WN * NB * 32;
   g.n_mt = (int)((g.M + MT - 1) / MT);
   g.n_nt = (int)((g.N + NT - 1) / NT);
-  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB, P, PAIR, AT, BT>;
+  auto k = matmul_tile_kernel<T, O, WM, WN, MB, NB, P, PAIR, AT, BT, B8>;
   constexpr int lds = (2 * P + 1) * (MT > NT ? MT : NT) * 128;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;

@@ -432,20 +432,23 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.direct = dtype != 1;
   p.ldk = up(K, epc);
   p.copy = p.direct && (!aligned_xw || K % epc != 0);
+  if (need_dx) choose_tile(M, K, up(N, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dx, &p.splits_dx);
+  if (need_dw) choose_tile(N, K, up(M, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dw, &p.splits_dw);
+  const bool chunks = p.direct && aligned_xw && K % 16 == 0;
+  p.w8_tile = p.w8 && chunks && p.cfg_dx != kTile64, p.x8_tile = p.x8 && chunks && p.cfg_dw != kTile64;
   // (int8 rows are brought back at the copies' stride, as whole chunks, whether or not others are copied)
   const size_t w_bytes = (size_t)(N * p.ldk) * esz, x_bytes = (size_t)(M * p.ldk) * esz;
-  p.off_wt = take(!need_dx ? 0 : (p.copy || (p.direct && p.w8) ? w_bytes : (p.direct ? 0 : (size_t)(K * p.ldn) * esz)));
+  const bool w_copy = p.w8 ? !p.w8_tile : p.copy, x_copy = p.x8 ? !p.x8_tile : p.copy;
+  p.off_wt = take(!need_dx ? 0 : (p.direct ? (w_copy ? w_bytes : 0) : (size_t)(K * p.ldn) * esz));
   p.off_dut = take(need_dw && !p.direct ? (size_t)(N * p.ldm) * esz : 0);
-  p.off_xt = take(!need_dw ? 0 : (p.copy || (p.direct && p.x8) ? x_bytes : (p.direct ? 0 : (size_t)(K * p.ldm) * esz)));
+  p.off_xt = take(!need_dw ? 0 : (p.direct ? (x_copy ? x_bytes : 0) : (size_t)(K * p.ldm) * esz));
   p.off_w8 = take(p.w8 && !p.direct ? w_bytes : 0);
   p.off_x8 = take(p.x8 && !p.direct ? x_bytes : 0);
   size_t part = 0;
   if (need_dx) {
-    choose_tile(M, K, up(N, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dx, &p.splits_dx);
     if (p.splits_dx > 1) part = (size_t)(p.splits_dx * M * K) * 4;
   }
   if (need_dw) {
-    choose_tile(N, K, up(M, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dw, &p.splits_dw);
     const size_t q = p.splits_dw > 1 ? (size_t)(p.splits_dw * N * K) * 4 : 0;
     part = q > part ? q : part;
   }
@@ -505,8 +508,8 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     *to = ws + off;
     if (rows > 0 && K > 0 && e == hipSuccess) e = launch_dequantize_rows(r, rows, K, p.ldk, dtype, ws + off, st);
   };
-  if (p.w8) back(held.w, N, p.direct ? p.off_wt : p.off_w8, &w);
-  if (p.x8) back(held.x, M, p.direct ? p.off_xt : p.off_x8, &x);
+  if (p.w8 && !p.w8_tile) back(held.w, N, p.direct ? p.off_wt : p.off_w8, &w);
+  if (p.x8 && !p.x8_tile) back(held.x, M, p.direct ? p.off_xt : p.off_x8, &x);
   if (e != hipSuccess) return e;
   if (p.direct) {
     if (p.copy) {
@@ -518,17 +521,27 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     }
     const int64_t ldu = p.du_direct ? N : p.ldn;
     const int64_t ldw = p.copy || p.w8 ? p.ldk : K, ldx = p.copy || p.x8 ? p.ldk : K;
+    auto rows8 = [&](const Int8Rows& r, bool across, int cfg) {
+      g.b = r.q, g.ldb = K, g.b_scale = r.scale, g.b_groups = scales_of(K, r.group), g.b_shift = group_shift(r.group);
+      return gemm_rows8(g, dtype, across, cfg, st);
+    };
     // dx: du along the depth, w across it; dw: both across it.
     if (dx && M > 0 && K > 0) {
       g.a = d, g.b = w, g.lda = ldu, g.ldb = ldw, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
       g.ep.y = dx;
-      e = dtype == 0 ? launch_gemm_tr<bf16_t, false>(g, p.cfg_dx, st) : launch_gemm_tr<f16_t, false>(g, p.cfg_dx, st);
+      if (p.w8_tile)
+        e = rows8(held.w, false, p.cfg_dx);
+      else
+        e = dtype == 0 ? launch_gemm_tr<bf16_t, false>(g, p.cfg_dx, st) : launch_gemm_tr<f16_t, false>(g, p.cfg_dx, st);
       if (e != hipSuccess) return e;
     }
     if (dw && N > 0 && K > 0) {
       g.a = d, g.b = x, g.lda = ldu, g.ldb = ldx, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
       g.ep.y = dw;
-      e = dtype == 0 ? launch_gemm_tr<bf16_t, true>(g, p.cfg_dw, st) : launch_gemm_tr<f16_t, true>(g, p.cfg_dw, st);
+      if (p.x8_tile)
+        e = rows8(held.x, true, p.cfg_dw);
+      else
+        e = dtype == 0 ? launch_gemm_tr<bf16_t, true>(g, p.cfg_dw, st) : launch_gemm_tr<f16_t, true>(g, p.cfg_dw, st);
     }
     return e;
   }

@@ -655,8 +655,8 @@ typedef struct dora_int8_rows {
 
 /*
  * Device workspace dora_matmul_backward_int8 needs: `outputs` as for
- * dora_matmul_backward (DORA_GRAD_ALIGNED speaks of x and w where they are not
- * held as int8 rows), `held` the DORA_HELD_ bits. Host only.
+ * dora_matmul_backward (DORA_GRAD_ALIGNED speaks of x, or x8's q, and of w, or
+ * w8's q), `held` the DORA_HELD_ bits. Host only.
  */
 dora_status dora_matmul_backward_int8_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
                                                      size_t* ws_bytes);

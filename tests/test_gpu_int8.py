@@ -569,3 +569,63 @@ def test_products_beside_the_walking_kernel():
                        (16, 8176, 1024, 16), (17, 8192, 1024, 16)):
         o, rng = operands(M, N, K, r, "bf16", M + N + K)
         check(o, rng, "bf16", "silu", True, False)
+
+
+def aligned_rows(rng, shape, dtype, group):
+    v = draw(rng, shape, dtype)
+    return bnd.Int8Rows(*bnd.dora_quantize_rows(v, group=group), group)
+
+
+# (M, N, K) whose products take the tiles of 256 and 128 rows: rows in whole chunks of 16 bytes, which these kernels
+# read as they are held; odd row counts, ends inside a tile, a split depth, and depths of one stage and less.
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K,group", [(8200, 384, 4112, 128), (4100, 2056, 4112, 0), (2077, 1025, 2064, 64), (8192, 64, 2048, 32),
+                                         (1030, 4104, 4112, 256), (5000, 100, 8192, 0), (16384, 40, 1040, 128)])
+def test_products_that_read_int8_rows(M, N, K, group, dtype):
+    rng = np.random.default_rng(M + N)
+    dy, u = draw(rng, (M, N), dtype), draw(rng, (M, N), dtype)
+    x, w, c = aligned_rows(rng, (M, K), dtype, group), aligned_rows(rng, (N, K), dtype, group), vec(rng, N, 0.2)
+    got = bnd.dora_matmul_backward_int8(dy, u, x, w, col_scale=c)
+    check_backward(got, dy, u, x, w, c, torch.zeros(N, device="cuda"), "none", dtype)
+    again = bnd.dora_matmul_backward_int8(dy, u, x, w, col_scale=c)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("at", ["x", "w"])
+def test_int8_rows_off_the_grid(at):
+    """q one byte into its buffer: the same values from copies as from the rows themselves, but for how sums are ordered."""
+    rng = np.random.default_rng(31)
+    M, N, K = 2100, 520, 2064
+    dy, u = draw(rng, (M, N), "bf16"), draw(rng, (M, N), "bf16")
+    v = {"x": aligned_rows(rng, (M, K), "bf16", 128), "w": aligned_rows(rng, (N, K), "bf16", 0)}
+    v[at] = v[at]._replace(q=off(v[at].q))
+    got = bnd.dora_matmul_backward_int8(dy, u, v["x"], v["w"])
+    check_backward(got, dy, u, v["x"], v["w"], torch.ones(N, device="cuda"), torch.zeros(N, device="cuda"), "none", "bf16")
+
+
+def test_int8_rows_with_a_nan_scale_reach_their_own():
+    rng = np.random.default_rng(32)
+    M, N, K = 2100, 384, 4096
+    dy, u = draw(rng, (M, N), "bf16"), draw(rng, (M, N), "bf16")
+    x = aligned_rows(rng, (M, K), "bf16", 128)
+    clean = bnd.dora_matmul_backward_int8(dy, u, x, None, need_dx=False)[1]
+    x.scale[2099, 3] = float("nan")
+    x.q[2099, 3 * 128:4 * 128] = 0
+    dw = bnd.dora_matmul_backward_int8(dy, u, x, None, need_dx=False)[1]
+    assert torch.isnan(dw[:, 384:512]).all()
+    keep = [k for k in range(K) if not 384 <= k < 512]
+    assert torch.equal(dw[:, keep], clean[:, keep])
+
+
+def test_the_largest_values_that_int8_rows_stand_for():
+    x = torch.zeros(4, 4096, device="cuda", dtype=torch.bfloat16)
+    x[:, ::3], x[:, 1::3] = 3.38e38, -3.38e38
+    q, s = bnd.dora_quantize_rows(x, group=128)
+    back = bnd.dora_dequantize_rows(q, s, group=128)
+    assert torch.isfinite(back).all() and (back.float() / x.float().where(x != 0, back.float()) - 1)[:, ::3].abs().max() < 2.0 ** -7
+    dy = torch.zeros(4096, 384, device="cuda", dtype=torch.bfloat16)
+    dy[1] = 2.0 ** -20
+    rows = bnd.Int8Rows(q.repeat(1024, 1), s.repeat(1024, 1), 128)
+    dw = bnd.dora_matmul_backward_int8(dy, dy, rows, None, need_dx=False)[1]
+    assert torch.equal(dw, (back[1].float() * 2.0 ** -20).bfloat16().expand(384, 4096))
