@@ -518,13 +518,26 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   const bool q_in = n0 + qc * 16 < g.N;   // (rows are whole chunks)
   const uint32_t q_off = q_in ? (uint32_t)(qk * g.ldb + n0 + qc * 16) : kOob;
   const uint32_t s_off = (uint32_t)(qk * g.b_groups + ((n0 + qc * 16) >> g.b_shift)) * 4u;
-  auto load_q = [&](int i, int j) __attribute__((always_inline)) {
-    const int64_t left = i < st1 ? g.K - (int64_t)i * 64 : 0, ks = left < 0 ? 0 : left;
-    const int64_t qb = ks * g.ldb, sb8 = ks * g.b_groups * 4;
-    const __amdgpu_buffer_rsrc_t rq = make_rsrc(static_cast<const char*>(g.b) + (int64_t)i * 64 * g.ldb,
-                                                (uint32_t)(qb < 0x7fffffff ? qb : 0x7fffffff));
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(g.b_scale + (int64_t)i * 64 * g.b_groups,
-                                                (uint32_t)(sb8 < 0x7fffffff ? sb8 : 0x7fffffff));
+  // The stage that is being loaded, as addresses and bytes up to the end of this
+  // workgroup's depth, which advance by a stage at a time (computed anew for each
+  // load they were a third of the loop's instructions, of which one wave a SIMD
+  // issues one in four cycles).
+  const int64_t k_end = g.K < (int64_t)st1 * 64 ? g.K : (int64_t)st1 * 64, k_first = k_end - (int64_t)st0 * 64;
+  const char* q_at = static_cast<const char*>(g.b) + (int64_t)st0 * 64 * g.ldb;
+  const char* s_at = reinterpret_cast<const char*>(g.b_scale) + (int64_t)st0 * 256 * g.b_groups;
+  const char* a_at = sa.p + (int64_t)st0 * 64 * sa.kbytes;
+  int64_t q_left = k_first * g.ldb, s_left = k_first * g.b_groups * 4, a_left = k_first * sa.kbytes;
+  auto bytes = [](int64_t left) __attribute__((always_inline)) {
+    return (uint32_t)(left < 0 ? 0 : (left < 0x7fffffff ? left : 0x7fffffff));
+  };
+  uint32_t q_bytes = bytes(q_left), s_bytes = bytes(s_left), a_bytes = bytes(a_left);
+  auto advance = [&]() __attribute__((always_inline)) {
+    q_at += 64 * g.ldb, s_at += 256 * g.b_groups, a_at += 64 * sa.kbytes;
+    q_left -= 64 * g.ldb, s_left -= 256 * g.b_groups, a_left -= 64 * sa.kbytes;
+    q_bytes = bytes(q_left), s_bytes = bytes(s_left), a_bytes = bytes(a_left);
+  };
+  auto load_q = [&](int j) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t rq = make_rsrc(q_at, q_bytes), rs = make_rsrc(s_at, s_bytes);
     const uint32_t qo = q_off + (uint32_t)(j * KPJ) * (uint32_t)g.ldb;
     const uint32_t so = s_off + (uint32_t)(j * KPJ) * (uint32_t)g.b_groups * 4u;
     qv[j] = __builtin_amdgcn_raw_buffer_load_b128(rq, qo, 0, 0);
@@ -533,7 +546,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // Element e of the stage's BBLK * 16 of this lane, into the unit; with the last
   // of 16 bytes the next stage's take their registers.
   float qf = 0.f;
-  auto convert = [&](int unit, int e, int next) __attribute__((always_inline)) {
+  auto convert = [&](int unit, int e) __attribute__((always_inline)) {
     if constexpr (B8) {
       const int j = e / 16, b = e % 16;
       const float f = (float)(int8_t)(qv[j][b / 4] >> (8 * (b % 4))) * qs[j];
@@ -545,10 +558,21 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
         const int k = qk + j * KPJ, c = qc * 2 + b / 8;
         store_lds((lds_u32x4*)(lds + unit + k * (NT * 2) + ((c ^ trswz<NT>(k)) * 16)), qout);
       }
-      if (b == 15) load_q(next, j);
+      if (b == 15) load_q(j);
     }
   };
   auto issue_a = [&](int i, int unit, int b) __attribute__((always_inline)) { issue(sa, sa2, i, unit, b, Tag<AT>{}); };
+  // (B8: of the stage being loaded, whose number i is.)
+  auto issue_a8 = [&](int i, int unit, int b) __attribute__((always_inline)) {
+    if constexpr (AT) {
+      char* dst = lds + unit + (b * NW + wave) * 1024;
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(a_at, a_bytes);
+      const uint32_t off = sa.off + (uint32_t)b * sa.step;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
+    } else {
+      issue_a(i, unit, b);
+    }
+  };
   auto issue_b = [&](int i, int unit, int b) __attribute__((always_inline)) { issue(sb, sb2, i, unit, b, Tag<BT>{}); };
 
   // The epilogue's columns of this lane: their scales and biases are asked for
@@ -625,9 +649,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       if constexpr (B8) {
 #pragma unroll
         for (int l = 0; l < ABLK / STEPS; ++l)
-          if (l * NM / (ABLK / STEPS) == m) issue_a(i + P + 1, um, t * (ABLK / STEPS) + l);
+          if (l * NM / (ABLK / STEPS) == m) issue_a8(i + P + 1, um, t * (ABLK / STEPS) + l);
 #pragma unroll
-        for (int e = m * PER_STEP / NM; e < (m + 1) * PER_STEP / NM; ++e) convert(ul, t * PER_STEP + e, i + P + 1);
+        for (int e = m * PER_STEP / NM; e < (m + 1) * PER_STEP / NM; ++e) convert(ul, t * PER_STEP + e);
       } else {
 #pragma unroll
         for (int l = l0; l < l1; ++l)
@@ -651,7 +675,12 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 #pragma unroll
   for (int j = 0; j < (B8 ? 1 : P); ++j) {
 #pragma unroll
-    for (int b = 0; b < ABLK; ++b) issue_a(st0 + j, 2 * j * UNIT, b);
+    for (int b = 0; b < ABLK; ++b) {
+      if constexpr (B8)
+        issue_a8(st0, 0, b);
+      else
+        issue_a(st0 + j, 2 * j * UNIT, b);
+    }
     if (!B8 && j + 1 < P) {
 #pragma unroll
       for (int b = 0; b < BBLK; ++b) issue_b(st0 + j, (2 * j + 1) * UNIT, b);
@@ -667,17 +696,18 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
     // (In a period's order, so that the waits of the loop, which are those of its
     // first round too, leave as many loads in flight as its other rounds could.)
 #pragma unroll
-    for (int j = 0; j < BBLK; ++j) load_q(st0, j);
+    for (int j = 0; j < BBLK; ++j) load_q(j);
 #pragma unroll
     for (int t = 0; t <= STEPS; ++t) {
       const bool first = t < STEPS;
+      if (t == 0 || t == STEPS) advance();
 #pragma unroll
       for (int l = 0; l < L1; ++l)
-        issue_a(first ? st0 + 1 : st0 + 2, first ? 2 * UNIT : 4 * UNIT, (first ? t * L1 : 0) + l);
+        issue_a8(first ? st0 + 1 : st0 + 2, first ? 2 * UNIT : 4 * UNIT, (first ? t * L1 : 0) + l);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int e = 0; e < PER_STEP; ++e)
-        convert(first ? UNIT : 3 * UNIT, (first ? t * PER_STEP : 0) + e, first ? st0 + 1 : st0 + 2);
+        convert(first ? UNIT : 3 * UNIT, (first ? t * PER_STEP : 0) + e);
       __builtin_amdgcn_sched_barrier(0);
     }
     wait_vm_lgkm0<LATER + L1>();
@@ -707,6 +737,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
     // i take the next period's loads.
     wait_vm_lgkm0<LATER>();
     barrier_keep_loads();
+    if constexpr (B8) advance();
     step(F[1], F[0], unit(2), unit(3), 0, i, unit(0), unit(1), 0, L1, 0, pair);
     u0 = unit(2);
   };

@@ -579,8 +579,9 @@ def aligned_rows(rng, shape, dtype, group):
 # (M, N, K) whose products take the tiles of 256 and 128 rows: rows in whole chunks of 16 bytes, which these kernels
 # read as they are held; odd row counts, ends inside a tile, a split depth, and depths of one stage and less.
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("M,N,K,group", [(8200, 384, 4112, 128), (4100, 2056, 4112, 0), (2077, 1025, 2064, 64), (8192, 64, 2048, 32),
-                                         (1030, 4104, 4112, 256), (5000, 100, 8192, 0), (16384, 40, 1040, 128)])
+@pytest.mark.parametrize("M,N,K,group", [(8200, 384, 4112, 128), (4100, 2056, 4112, 0), (2077, 1021, 2064, 64), (8192, 64, 2048, 32),
+                                         (1021, 4104, 4112, 256), (5000, 100, 8192, 0), (16384, 40, 1040, 128),
+                                         (130, 1000, 8208, 32), (1000, 8200, 2048, 0), (600, 600, 28672, 64)])
 def test_products_that_read_int8_rows(M, N, K, group, dtype):
     rng = np.random.default_rng(M + N)
     dy, u = draw(rng, (M, N), dtype), draw(rng, (M, N), dtype)
