@@ -6,10 +6,9 @@
 //   y = n, rounded once, or q = n / scale in e4m3 or int8, rounded once, with
 //   scale = max_j |n| / 448 or / 127
 //
-// The statistics are of the fp32 sum x + residual. All of a row is taken relative
-// to its first value, and the variance is a sum of squares about means, so that
-// neither loses digits where the mean is far larger than the spread (a sum of
-// h^2 would lose them all).
+// The statistics are of the fp32 sum x + residual. The variance is a sum of
+// squares about means, which keeps its digits where the mean is far larger than
+// the spread (a sum of h^2 would lose them all).
 //
 // HBM bound, as the RMS norm, whose row loads, shapes and grids these kernels
 // share: a row is read once into the registers of one wave or one workgroup.
@@ -68,7 +67,8 @@ __device__ __forceinline__ const float* reread(const float* p) {
 // squares about it; the waves' (count, mean, squares) join as those of any
 // parts do: the squares about the whole mean are the parts' own and count times
 // the square of each part's distance to it (Chan, Golub, LeVeque 1979). One
-// exchange between the waves serves both.
+// exchange between the waves serves both; a part's mean is off by a few 2^-24 of
+// itself, which counts times its distance to the whole one.
 template <int NT, int C, int E>
 __device__ __forceinline__ void row_stats(const float (&f)[C][E], int lane, int64_t d, float eps, float* red,
                                           float& mean, float& rstd) {
@@ -144,15 +144,12 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
   const int64_t t0 = (int64_t)blockIdx.x * RPW + (NT == 64 ? threadIdx.x >> 6 : 0);
   const bool has_res = NORM && a.residual != nullptr;
   u32x4 xv[C], rv[C];
-  T x0 = T(0), r0 = T(0);   // (NORM: the row's first values)
   auto load = [&](int64_t t) __attribute__((always_inline)) {
     const T* x = static_cast<const T*>(a.x) + t * a.d;
 #pragma unroll
     for (int c = 0; c < C; ++c) xv[c] = load_row_chunk<T, STREAM && LINES>(x, (int64_t)(c * NT + lane) * E, a.d);
-    if (NORM) x0 = x[0];
     if (has_res) {
       const T* res = static_cast<const T*>(a.residual) + t * a.d;
-      r0 = res[0];
 #pragma unroll
       for (int c = 0; c < C; ++c) rv[c] = load_row_chunk<T, STREAM && LINES>(res, (int64_t)(c * NT + lane) * E, a.d);
     }
@@ -172,7 +169,6 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
   for (int64_t t = t0; t < a.T; t += (int64_t)gridDim.x * RPW, par ^= 1) {
     if (!AHEAD) load(t);
     float f[C][E];
-    const float origin = to_f32(x0) + (has_res ? to_f32(r0) : 0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       unpack<T, E>(xv[c], f[c]);
@@ -192,14 +188,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void layer_norm_kernel(LayerNo
         for (int c = 0; c < C; ++c) store_row_chunk<T, STREAM>(h, (int64_t)(c * NT + lane) * E, a.d, f[c]);
       }
       float mean, rs;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int n = chunk_left<E>((int64_t)(c * NT + lane) * E, a.d);
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[c][e] = e < n ? f[c][e] - origin : 0.f;
-      }
       row_stats<NT, C, E>(f, lane, a.d, a.eps, red[par], mean, rs);
-      if (lane == 0 && a.mean) a.mean[t] = origin + mean;
+      if (lane == 0 && a.mean) a.mean[t] = mean;
       if (lane == 0 && a.rstd) a.rstd[t] = rs;
 #pragma unroll
       for (int c = 0; c < C; ++c) {

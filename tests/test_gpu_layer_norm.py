@@ -1,14 +1,13 @@
 """The residual layer norm and its backward on the GPU against the fp64 reference.
 
-Tolerances. The fp32 sum of d values, each relative to the row's first, in any
-order is off by at most d 2^-24 of the mean of their sizes, which moves the
-mean; h itself, the sum of two, by 2^-24, as each subtraction of the first
-value and of the mean. The squares about that mean are off by (d + 4) 2^-24
-relative, by the square of the mean's error (their sum about the true mean is
-least), by what moves a value in its own subtractions, and, where parts of a row
-are joined by the squares of their means' distances, by twice the mean's error
-times such a distance, whose root mean square is at most the spread. n then has
-three roundings more. Each output adds half a step of its type.
+Tolerances. The fp32 sum of d values in any order is off by at most d 2^-24 of
+the mean of their sizes, which moves the mean; h itself, the sum of two, by
+2^-24. The squares about that mean are off by (d + 4) 2^-24 relative, by the
+square of the mean's error (their sum about the true mean is least), by what
+moves a value in its own subtraction, and, where parts of a row are joined by
+the squares of their means' distances, by twice the mean's error times such a
+distance, whose root mean square is at most the spread. n then has three
+roundings more. Each output adds half a step of its type.
 """
 
 import numpy as np
@@ -34,8 +33,8 @@ def bounds(n, h, mean, rstd, w, b):
     """(error of the mean [T], of rstd [T], of n [T, d]) of fp32 arithmetic in any order."""
     d = h.shape[1]
     ah, v = np.abs(h), np.abs(h - mean[:, None])
-    em = (d + 3) * EPS32 * (ah.mean(1) + ah[:, 0])
-    move = EPS32 * (2 * ah + ah[:, :1] + v)          # of one value in its sum and two subtractions
+    em = (d + 3) * EPS32 * ah.mean(1)
+    move = EPS32 * (ah + v)                          # of one value in its sum and its subtraction
     var = (v * v).mean(1)
     evar = (d + 4) * EPS32 * (var + em * em) + em * em + 2 * (v * move).mean(1) + 2 * em * move.mean(1) + (move * move).mean(1)
     evar = evar + 2 * em * np.sqrt(var)
