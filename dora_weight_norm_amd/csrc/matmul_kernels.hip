@@ -88,7 +88,8 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
         // (du, which the products read next, is to stay in the caches)
         r.y[i] = load_raw8<T, true>(dy + m * N + n, nv);
         if constexpr (U8) {
-          load_row_bytes<8, true>(u8.q + m * N, n, N, r.q[i]);
+          // (through the caches: 27.6 and 29.7 us at 4096 x 4096 with SiLU, sums included)
+          load_row_bytes<8>(u8.q + m * N, n, N, r.q[i]);
           r.s[i] = u8.scale[m * u8.groups + (n >> u8.shift)];
         } else {
           r.u[i] = load_raw8<T, true>(u + m * N + n, nv);
