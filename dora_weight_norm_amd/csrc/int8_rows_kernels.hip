@@ -79,22 +79,34 @@ __global__ __launch_bounds__(256) void quantize_groups_kernel(const T* x, RowSte
   }
 }
 
-// Rows of x lie ld >= d elements apart; those from d on, up to a whole chunk or
-// ld, are written as zeros.
+// One or two operands of rows of d columns, the second's rows numbered after the
+// first's; rows of x lie ld >= d elements apart, and those from d on, up to a
+// whole chunk or ld, are written as zeros.
+struct UnpackJob {
+  const uint8_t* q;
+  const float* scale;
+  int64_t groups, T;
+  int shift;
+  void* x;
+};
+
 template <typename T, bool STREAM>
-__global__ __launch_bounds__(256) void dequantize_rows_kernel(const uint8_t* q, const float* scale, RowSteps s, T* x,
-                                                              int64_t ld) {
+__global__ __launch_bounds__(256) void dequantize_rows_kernel(UnpackJob a, UnpackJob b, RowSteps s, int64_t ld) {
   constexpr int E = Elem<T>::epc;
   for (uint32_t it = blockIdx.x * kItems; it < s.items; it += gridDim.x * kItems) {
     uint32_t w[kItems][E / 4];
     float sc[kItems];
     Place p[kItems];
+    T* to[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       p[i] = place_of<E>(s, it + i);
+      const bool first = p[i].row < a.T;
+      const int64_t row = first ? p[i].row : p[i].row - a.T;
+      to[i] = static_cast<T*>(first ? a.x : b.x) + row * ld;
       if (p[i].ok) {
-        load_row_bytes<E>(q + p[i].row * s.d, p[i].k, s.d, w[i]);
-        sc[i] = scale[p[i].row * s.groups + (p[i].k >> s.shift)];
+        load_row_bytes<E>((first ? a.q : b.q) + row * s.d, p[i].k, s.d, w[i]);
+        sc[i] = (first ? a.scale : b.scale)[row * (first ? a.groups : b.groups) + (p[i].k >> (first ? a.shift : b.shift))];
       }
     }
 #pragma unroll
@@ -103,7 +115,7 @@ __global__ __launch_bounds__(256) void dequantize_rows_kernel(const uint8_t* q, 
       float f[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) f[e] = (float)(int8_t)(w[i][e / 4] >> (8 * (e % 4))) * sc[i];
-      store_row_chunk<T, STREAM>(x + p[i].row * ld, p[i].k, ld, f);
+      store_row_chunk<T, STREAM>(to[i], p[i].k, ld, f);
     }
   }
 }
@@ -163,17 +175,14 @@ hipError_t quantize_groups(const void* x, int64_t T_, int64_t d, int64_t group, 
 }
 
 template <typename T>
-hipError_t dequantize(const Int8Rows& r, int64_t T_, int64_t d, int64_t ld, void* x, hipStream_t st) {
-  constexpr int E = Elem<T>::epc;
+hipError_t dequantize(const UnpackJob& a, const UnpackJob& b, int64_t d, int64_t ld, hipStream_t st) {
   dim3 grid, block;
-  const RowSteps s = row_steps(T_, d, r.group, E, 1, &grid, &block);
-  const bool stream = T_ * d * (int64_t)sizeof(T) > kStreamBytes && d % 128 == 0;
+  const RowSteps s = row_steps(a.T + b.T, d, 0, Elem<T>::epc, 1, &grid, &block);
+  const bool stream = (a.T + b.T) * d * (int64_t)sizeof(T) > kStreamBytes && d % 128 == 0;
   if (stream)
-    hipLaunchKernelGGL((dequantize_rows_kernel<T, true>), grid, block, 0, st, r.q, r.scale, s, static_cast<T*>(x),
-                       ld);
+    hipLaunchKernelGGL((dequantize_rows_kernel<T, true>), grid, block, 0, st, a, b, s, ld);
   else
-    hipLaunchKernelGGL((dequantize_rows_kernel<T, false>), grid, block, 0, st, r.q, r.scale, s, static_cast<T*>(x),
-                       ld);
+    hipLaunchKernelGGL((dequantize_rows_kernel<T, false>), grid, block, 0, st, a, b, s, ld);
   return hipGetLastError();
 }
 
@@ -193,12 +202,14 @@ hipError_t launch_quantize_rows(const void* x, int dtype, int64_t T, int64_t d, 
   }
 }
 
-hipError_t launch_dequantize_rows(const Int8Rows& r, int64_t T, int64_t d, int64_t ld, int dtype, void* x,
-                                  hipStream_t st) {
+hipError_t launch_dequantize_rows(const Int8Rows& r, int64_t T, void* x, const Int8Rows& r2, int64_t T2, void* x2,
+                                  int64_t d, int64_t ld, int dtype, hipStream_t st) {
+  const UnpackJob a{r.q, r.scale, scales_of(d, r.group), T, group_shift(r.group), x};
+  const UnpackJob b{r2.q, r2.scale, scales_of(d, r2.group), T2, group_shift(r2.group), x2};
   switch (dtype) {
-    case 0: return dequantize<bf16_t>(r, T, d, ld, x, st);
-    case 2: return dequantize<f16_t>(r, T, d, ld, x, st);
-    default: return dequantize<float>(r, T, d, ld, x, st);
+    case 0: return dequantize<bf16_t>(a, b, d, ld, st);
+    case 2: return dequantize<f16_t>(a, b, d, ld, st);
+    default: return dequantize<float>(a, b, d, ld, st);
   }
 }
 

@@ -513,14 +513,16 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   }
   GemmArgs g{};
   g.part = reinterpret_cast<float*>(ws + p.off_part);
-  // Int8 rows back to the storage type.
-  auto back = [&](const Int8Rows& r, int64_t rows, size_t off, const void** to) {
-    *to = ws + off;
-    if (rows > 0 && K > 0 && e == hipSuccess) e = launch_dequantize_rows(r, rows, K, p.ldk, dtype, ws + off, st);
-  };
-  if (p.w8 && !p.w8_tile) back(held.w, N, p.direct ? p.off_wt : p.off_w8, &w);
-  if (p.x8 && !p.x8_tile) back(held.x, M, p.direct ? p.off_xt : p.off_x8, &x);
-  if (e != hipSuccess) return e;
+  // Int8 rows back to the storage type, both operands in one launch.
+  const bool w_back = p.w8 && !p.w8_tile, x_back = p.x8 && !p.x8_tile;
+  char* w16 = ws + (p.direct ? p.off_wt : p.off_w8);
+  char* x16 = ws + (p.direct ? p.off_xt : p.off_x8);
+  if (w_back) w = w16;
+  if (x_back) x = x16;
+  if (K > 0 && (w_back ? N : 0) + (x_back ? M : 0) > 0) {
+    e = launch_dequantize_rows(held.w, w_back ? N : 0, w16, held.x, x_back ? M : 0, x16, K, p.ldk, dtype, st);
+    if (e != hipSuccess) return e;
+  }
   if (p.direct) {
     if (p.copy) {
       PackJobs jobs{};
