@@ -50,12 +50,16 @@ class AdaptedLayer:
     bias: torch.Tensor | None = None
     eps: float = 1e-6
 
+    def weight(self, stream=None):
+        """W in A's dtype: itself, or the values that its int8 rows stand for."""
+        if isinstance(self.W, bnd.Int8Rows):
+            return bnd.dora_dequantize_rows(*self.W, dtype=self.A.dtype, stream=stream)
+        return self.W
+
     def magnitude(self, stream=None):
         """(wnorm, g) of the layer as it stands, float32 [d_out]."""
-        W = self.W
-        if isinstance(W, bnd.Int8Rows):
-            W = bnd.dora_dequantize_rows(W.q, W.scale, group=W.group, dtype=self.A.dtype, stream=stream)
-        return bnd.dora_factored_norm(W, self.A, self.B, self.s, m=self.m, eps=self.eps, stream=stream)
+        return bnd.dora_factored_norm(self.weight(stream), self.A, self.B, self.s, m=self.m, eps=self.eps,
+                                      stream=stream)
 
 
 @dataclass
@@ -200,8 +204,9 @@ class Frozen8Bit:
 def freeze_8bit(layer: AdaptedLayer, stream=None) -> Frozen8Bit:
     """Merges and quantises a layer once, when serving starts."""
     _, g = layer.magnitude(stream)
+    W = layer.weight(stream)
     with bnd._on(stream):
-        v = layer.W.float() + layer.s * (layer.B.float() @ layer.A.float())
+        v = W.float() + layer.s * (layer.B.float() @ layer.A.float())
         scale = (v.abs().amax(1) / 448.0).clamp(min=2.0 ** -100)
         return Frozen8Bit((v / scale[:, None]).to(torch.float8_e4m3fn), scale * g, layer.bias)
 

@@ -630,3 +630,63 @@ def test_the_largest_values_that_int8_rows_stand_for():
     rows = bnd.Int8Rows(q.repeat(1024, 1), s.repeat(1024, 1), 128)
     dw = bnd.dora_matmul_backward_int8(dy, dy, rows, None, need_dx=False)[1]
     assert torch.equal(dw, (back[1].float() * 2.0 ** -20).bfloat16().expand(384, 4096))
+
+
+def test_backward_offsets_past_32_bits():
+    """x8 of more than 2^32 bytes, read as it is held and (one byte off) from a copy, and u8 of as many."""
+    M, N, K, n = 2100000, 384, 2064, 70
+    rng = np.random.default_rng(33)
+    x = bnd.Int8Rows(torch.zeros(M, K, device="cuda", dtype=torch.int8), torch.ones(M, 17, device="cuda"), 128)
+    tail = aligned_rows(rng, (n, K), "bf16", 128)
+    x.q[-n:], x.scale[-n:] = tail.q, tail.scale
+    dy = torch.zeros(M, N, device="cuda", dtype=torch.bfloat16)
+    dy[-n:] = draw(rng, (n, N), "bf16")
+    got = bnd.dora_matmul_backward_int8(dy, dy, x, None, need_dx=False)
+    one, zero = torch.ones(N, device="cuda"), torch.zeros(N, device="cuda")
+    short = [got[0], got[1], got[2], got[3], got[4][-n:]]
+    check_backward(short, dy[-n:], dy[-n:], tail, tail.q.new_zeros(N, K).bfloat16(), one, zero, "none", "bf16")
+    assert not got[4][:-n].any()
+    moved = x._replace(q=off(x.q))
+    del x
+    again = bnd.dora_matmul_backward_int8(dy, dy, moved, None, need_dx=False)
+    check_backward([None, again[1], again[2], again[3], again[4][-n:]], dy[-n:], dy[-n:], tail,
+                   tail.q.new_zeros(N, K).bfloat16(), one, zero, "none", "bf16")
+    # u8: the same rows, of K columns
+    big = torch.zeros(M, K, device="cuda", dtype=torch.bfloat16)
+    big[-n:] = draw(rng, (n, K), "bf16")
+    _, _, db, dc, du = bnd.dora_matmul_backward_int8(big, moved, None, None, act="silu", need_dx=False, need_dw=False)
+    c1, c0 = torch.ones(K, device="cuda"), torch.zeros(K, device="cuda")
+    check_backward([None, None, db, dc, du[-n:]], big[-n:], tail, tail.q.new_zeros(n, 8).bfloat16(),
+                   tail.q.new_zeros(K, 8).bfloat16(), c1, c0, "silu", "bf16")
+    assert not du[:-n].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(0, 384, 4096), (8200, 0, 4096), (8200, 384, 0)])
+def test_empty_int8_backward(M, N, K):
+    dt, i8 = torch.bfloat16, torch.int8
+    rows = lambda a, b: bnd.Int8Rows(torch.ones(a, b, device="cuda", dtype=i8), torch.ones(a, device="cuda"))   # noqa: E731
+    dx, dw, db, dc, du = bnd.dora_matmul_backward_int8(torch.ones(M, N, device="cuda", dtype=dt), rows(M, N), rows(M, K),
+                                                       rows(N, K))
+    assert dx.shape == (M, K) and dw.shape == (N, K) and du.shape == (M, N)
+    assert (dx == 0).all() and (dw == 0).all()
+    if M == 0:
+        assert (db == 0).all() and (dc == 0).all()
+
+
+def test_du_in_the_place_of_dy():
+    """The C entry allows du to be dy itself (rows are asked for ahead of the ones being written)."""
+    rng = np.random.default_rng(34)
+    M, N = 1000, 520
+    dy = draw(rng, (M, N), "bf16")
+    u = aligned_rows(rng, (M, N), "bf16", 64)
+    want = bnd.dora_matmul_backward_int8(dy, u, None, None, act="gelu", need_dx=False, need_dw=False)
+    need = bnd.dora_matmul_backward_int8_workspace_size(M, N, 0, "bf16", bnd.GRAD_SUMS + bnd.GRAD_DU + bnd.GRAD_ALIGNED, 0)
+    ws = torch.empty(need, device="cuda", dtype=torch.uint8)
+    db, dc, into = torch.empty(N, device="cuda"), torch.empty(N, device="cuda"), dy.clone()
+    arg = bnd._Int8RowsArg(u.q.data_ptr(), u.scale.data_ptr(), 64)
+    import ctypes
+    bnd._call("dora_matmul_backward_int8", into.data_ptr(), None, ctypes.byref(arg), None, None, None, None, 0, M, N, 0,
+              None, None, None, 2, into.data_ptr(), None, None, db.data_ptr(), dc.data_ptr(), ws.data_ptr(), need,
+              torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(into, want[4]) and torch.equal(db, want[2]) and torch.equal(dc, want[3])

@@ -217,3 +217,10 @@ def test_int8_block_refusals():
         block.FeedForward(p.norm_weight, p.up, p.down, norm="batch")
     with pytest.raises(ValueError):
         block.FeedForward(p.norm_weight, p.up, p.down, norm_bias=p.norm_weight)
+
+
+def test_freezing_a_layer_on_an_8_bit_base():
+    p, rng = make("bf16", 256, 384, 16)
+    a, b = block.int8_base(p.up), thawed(block.int8_base(p.up))
+    x, y = block.freeze_8bit(a), block.freeze_8bit(b)
+    assert torch.equal(x.w.view(torch.uint8), y.w.view(torch.uint8)) and torch.equal(x.scale, y.scale)
