@@ -549,6 +549,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   auto convert = [&](int unit, int e) __attribute__((always_inline)) {
     if constexpr (B8) {
       const int j = e / 16, b = e % 16;
+      // (bytes that a later step takes are not to be picked out, and so waited for,
+      // when they were only just asked for)
+      if (b % 8 == 0) asm volatile("" : "+v"(qv[j]), "+v"(qs[j]));
       const float f = (float)(int8_t)(qv[j][b / 4] >> (8 * (b % 4))) * qs[j];
       if (b % 2)
         qout[b % 8 / 2] = pack2<T>(qf, f);
@@ -582,7 +585,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   const int64_t n = n0 + wn * NB * 32 + col;
   const int nv = (int)(g.N - n < 8 ? g.N - n : 8);
   float cs[8], bs[8];
-  column_terms(g.ep, n, nv, cs, bs);
+  if constexpr (!B8) column_terms(g.ep, n, nv, cs, bs);   // (B8: a product of the backward, stored as it is)
   f32x16 acc[MB][NB];
 #pragma unroll
   for (int a = 0; a < MB; ++a)
@@ -810,7 +813,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
     }
   }
   constexpr int IT = MB * PB / 2;
-  const bool has_res = g.ep.residual != nullptr && g.splits == 1;
+  const bool has_res = !B8 && g.ep.residual != nullptr && g.splits == 1;
   const int64_t m_first = m0 + wm * MB * 32 + lane / LPR;   // this lane's first row; the others RPP apart
   const int64_t rows_left = g.M - m_first;
   const int rl = nv <= 0 || rows_left <= 0 ? 0 : (int)(rows_left < MB * 32 ? rows_left : MB * 32);
@@ -867,6 +870,14 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = v[8 * i + e];
         if (ok[i]) store8<float>(g.part + (int64_t)split * g.M * g.N + off[i], nv, o);
+      }
+    } else if constexpr (B8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v[8 * i + e];
+        if (ok[i]) store8<O>(static_cast<O*>(g.ep.y) + off[i], nv, o);
       }
     } else {
       epilogue_rows<O, 2>(g.ep, v, cs, bs, m, off, ok, nv, res);

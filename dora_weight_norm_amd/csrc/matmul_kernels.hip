@@ -408,13 +408,21 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
   return gemm(g, dtype, out_dtype, p.cfg, st);
 }
 
-// Products of up to so many rows read int8 rows as they are held; of more, from
-// 16-bit copies: the conversion costs each row tile of such a product a tenth of
-// its time, the copies all of it the same. Measured, as held against copied, us
-// of the whole call without sums: dw of M x N x K 8192 x 384 x 8192 94, 119;
-// 8192 x 768 x 8192 135, 164; 8192 x 384 x 28672 224, 325; but 2048 x 2048 x 2048
-// 50, 44; 8192 x 8192 x 8192 1024, 936.
-constexpr int64_t kRows8 = 1024;
+// Whether a product of so many rows reads int8 rows [depth][K] as they are held,
+// or from 16-bit copies: the conversion makes its loop a tenth slower, the copies
+// cost a launch and three bytes an element of the rows whatever the product, which
+// is as much at 4096 rows. Measured, as held against copied, us of the whole call
+// without sums, dw of M x N x K (N rows) and dx (M rows):
+//    8192 x  384 x  8192    89, 116;   80,  90
+//    8192 x  768 x  8192   133, 153;  122, 125
+//    8192 x  384 x 28672   207, 315;  260, 302
+//    2048 x 2048 x  2048    41,  44;   42,  44
+//    4096 x 4096 x  4096   142, 142;  137, 139
+//    8192 x 4096 x  8192   494, 489;  486, 479
+//    8192 x 8192 x  8192   976, 927;  942, 899
+static bool reads_rows8(int64_t rows, int64_t depth, int64_t K) {
+  return rows <= 4096 || (double)(rows - 4096) * (double)depth * (double)K < 2.7e10;
+}
 
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
                                         bool need_sums, bool du_direct, bool aligned_xw, bool x8, bool w8) {
@@ -444,8 +452,8 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   if (need_dx) choose_tile(M, K, up(N, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dx, &p.splits_dx);
   if (need_dw) choose_tile(N, K, up(M, KT) / KT, dtype, p.direct ? 0 : kFewOnGrid, &p.cfg_dw, &p.splits_dw);
   const bool chunks = p.direct && aligned_xw && K % 16 == 0;
-  p.w8_tile = p.w8 && chunks && p.cfg_dx != kTile64 && M <= kRows8;
-  p.x8_tile = p.x8 && chunks && p.cfg_dw != kTile64 && N <= kRows8;
+  p.w8_tile = p.w8 && chunks && p.cfg_dx != kTile64 && reads_rows8(M, N, K);
+  p.x8_tile = p.x8 && chunks && p.cfg_dw != kTile64 && reads_rows8(N, M, K);
   // (int8 rows are brought back at the copies' stride, as whole chunks, whether or not others are copied)
   const size_t w_bytes = (size_t)(N * p.ldk) * esz, x_bytes = (size_t)(M * p.ldk) * esz;
   const bool w_copy = p.w8 ? !p.w8_tile : p.copy, x_copy = p.x8 ? !p.x8_tile : p.copy;
