@@ -272,6 +272,34 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* 
   }
 }
 
+// Whether a product of 8-bit integers with few rows goes to the tiles all the
+// same. They bring rows into shared memory in whole lines without a register,
+// which 32 rows of w in pieces of 16 bytes do not reach, and have more of w on
+// its way than blocks of 16 columns do, at shallow depths or where the walking
+// kernel ends; rows off the 16-byte grid would be copied first and stay.
+// Measured, the few-rows or walking kernel against the tiles, us on the GPU:
+//   17 and 32 x 28672 x 8192   76.6, 44.3 and 87.3, 46.2
+//   17 and 32 x  8192 x 8192   21.9, 19.0 and 24.5, 19.3
+//   17 and 32 x  8192 x 1024    8.6,  6.1 and  9.6,  6.2
+//   17 and 32 x  4096 x 4096   12.4, 12.7 and 13.8, 13.8
+//   17 and 32 x  2048 x 16384  18.5, 17.2 and 20.4, 17.8
+//   17 and 32 x  4096 x 32768  36.3, 48.2 and 41.0, 47.9 (rows 32 KB apart)
+//    1 and 16 x 28672 x 1024   13.1,  9.8 and 14.1,  9.9
+//    1 and 16 x 28672 x 2048   16.4, 14.8 and 16.8, 14.9
+//    1 and 16 x 28672 x 4096   23.1, 26.2 and 26.0, 26.3
+//    1 and 16 x 16384 x 2048   10.4,  9.7 and 11.3,  9.8
+//    1 and 16 x 12288 x 2048    8.7,  9.1 and  9.3,  9.2
+//    1 and 16 x  8192 x 512     4.8,  5.3 and  5.3,  5.3
+//    9 and 16 x  8192 x 16384  29.1, 35.7 and 33.5, 36.1 (8 rows for 9)
+//    9 and 16 x  8192 x 24576  41.2, 41.4 and 48.4, 41.9
+//    9 and 16 x 12288 x 12288  32.7, 37.5 and 37.8, 37.8
+//    9 and 16 x 28672 x 12288  69.1, 72.0 and 81.9, 74.4
+bool int8_tiles(int64_t M, int64_t N, int64_t K) {
+  if (M > 32 || K == 0 || K % 16 != 0) return false;
+  if (M > 16) return few_wide(M, N, up(K, 128) / 128, kInt8Operands, true);
+  return (N >= 4 * 16 * kCUs && K <= 2048) || (M > 12 && K > 8192 && N * K > (int64_t)1 << 27);
+}
+
 // Whether the walking kernel takes a product of 8-bit integers: whole steps of
 // 128 bytes, eight a wave at most, a pair of one step a wave in whole chunks, and
 // two blocks of columns or more for a compute unit; up to 8 rows, for which the
@@ -281,7 +309,6 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* 
 //    1, 8 and 16 x  8192 x 8192   13.1, 14.7; 15.2, 15.3; 19.5, 16.3
 //    1, 8 and 16 x 12288 x 8192   21.6, 19.6; 22.3, 20.2; 27.7, 20.9
 //    1, 8 and 16 x 28672 x 8192   43.0, 37.6; 48.1, 39.5; 59.0, 40.2
-//    1, 8 and 16 x 28672 x 2048   17.2, 16.2; 19.9, 16.0; 24.1, 16.5
 //    1, 8 and 16 x 16384 x 1024    7.8,  8.3;  8.7,  8.4; 10.4,  9.0
 bool int8_walks(int64_t M, int64_t N, int64_t K, int64_t r) {
   if (M > 16 || K == 0 || K % 128 != 0 || K > 8192 || r > 512 || r % 8 != 0) return false;
@@ -360,8 +387,9 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   MatmulPlan p{};
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   size_t off = 0;
-  choose_tile(M, N, up(K, KT) / KT, dtype, K % epc == 0 ? kFewOnGrid : kFewOffGrid, &p.cfg, &p.splits);
-  if (dtype == kInt8Operands && int8_walks(M, N, K, r)) p.cfg = M <= 8 ? kWalk8 : kWalk16, p.splits = 1;
+  const bool i8 = dtype == kInt8Operands, tiles = i8 && int8_tiles(M, N, K);
+  choose_tile(M, N, up(K, KT) / KT, dtype, tiles ? 0 : (K % epc == 0 ? kFewOnGrid : kFewOffGrid), &p.cfg, &p.splits);
+  if (i8 && !tiles && int8_walks(M, N, K, r)) p.cfg = M <= 8 ? kWalk8 : kWalk16, p.splits = 1;
   auto operand = [&](int64_t rows, int64_t depth, int es, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
     *pack = p.cfg < kFew8 && depth > 0 && (depth % (16 / es) != 0 || !(al & bit));

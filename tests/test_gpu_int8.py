@@ -555,7 +555,7 @@ def test_two_calls_at_once_on_two_streams():
 # Up to 16 tokens, whole steps of 128 and two blocks of 16 columns for a compute unit: one workgroup a unit walks them.
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("M,N,K,r", [(1, 12288, 2048, 0), (1, 12305, 2176, 8), (7, 12300, 8192, 512), (8, 16400, 2944, 40),
-                                     (9, 8192, 8064, 0), (16, 28672, 256, 384), (13, 8207, 2048, 264), (12, 8192, 128, 64)])
+                                     (9, 8192, 8064, 0), (16, 28672, 256, 384), (16, 17000, 2176, 384), (13, 8207, 2048, 264), (12, 8192, 128, 64)])
 def test_walking_kernel(M, N, K, r, out):
     o, rng = operands(M, N, K, 0 if out == "f32" else r, out, M + N + K)
     check(o, rng, out, ACTS[(M + N + K) % 5], M % 2 == 0, True)
@@ -569,6 +569,18 @@ def test_products_beside_the_walking_kernel():
                        (16, 8176, 1024, 16), (17, 8192, 1024, 16)):
         o, rng = operands(M, N, K, r, "bf16", M + N + K)
         check(o, rng, "bf16", "silu", True, False)
+
+
+# Up to 32 rows that go to the tiles: 17 and more over many columns, fewer over the most at shallow depths or past the
+# walking kernel's, with a split depth, a pair off the 16-byte grid, and one row.
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K,r", [(17, 8200, 1040, 20), (32, 12288, 4096, 384), (24, 4112, 8208, 0), (3, 16400, 2048, 16),
+                                     (1, 16384, 16, 0), (16, 20001, 272, 5), (14, 8208, 16400, 40)])
+def test_few_rows_in_tiles(M, N, K, r, out):
+    r = 0 if out == "f32" else r
+    assert bnd.dora_matmul_int8_plan_info(M, N, K, r)["tile_rows"] > 0
+    o, rng = operands(M, N, K, r, out, M + N + K)
+    check(o, rng, out, ACTS[(M + N + K) % 5], M % 2 == 0, True)
 
 
 def aligned_rows(rng, shape, dtype, group):

@@ -115,6 +115,9 @@ def test_int8_product_plans():
     assert plan(8192, 8192, 8192, 384) == (256, False, 0, -1)
     assert plan(1, 8192, 8192, 384)[0] == 0 and plan(1, 8192, 8192, 384)[3] == 8
     assert plan(16, 28672, 8192, 0)[3] == 16 and plan(300, 520, 264, 0)[0] == 64
+    assert plan(32, 28672, 8192, 0)[0] == 64 and plan(17, 8192, 8192, 384)[0] == 64 and plan(16, 28672, 1024, 0)[0] == 64
+    assert plan(16, 8192, 28672, 0)[0] == 64 and plan(12, 8192, 28672, 0)[3] == 16 and plan(16, 8192, 16384, 0)[3] == 16
+    assert plan(32, 28672, 8189, 0)[3] == 32 and plan(32, 1024, 4096, 0)[3] == 16 and plan(16, 8192, 1024, 0)[3] == 16
     # rows of no whole 16-byte chunks: x and w in bytes, the pair in 16 bits
     assert plan(333, 1001, 776, 24)[2] == 3 and plan(333, 1001, 784, 20)[2] == 12
     assert plan(333, 1001, 784, 24, aligned_operands=11)[2] == 4
@@ -125,7 +128,9 @@ def test_int8_product_plans():
     assert f(4, 4, 131072, 0, 15, ctypes.byref(sz)) == 1 and f(4, 4, 131071, 0, 15, ctypes.byref(sz)) == 0
     assert f(4, 4, 4, 0, 15, None) == 1
     # a call whose s is 0 needs no more than the query with the pair says
-    for M, N, K, r in ((40, 300, 63, 5), (300, 520, 4104, 700), (1000, 1000, 100, 64)):
+    for M, N, K, r in ((40, 300, 63, 5), (300, 520, 4104, 700), (1000, 1000, 100, 64),
+                       (32, 8192, 8192, 20), (17, 4096, 14336, 5), (1, 28672, 2048, 7), (32, 28672, 512, 600),
+                       (16, 8192, 24576, 9)):
         assert bnd.dora_matmul_int8_workspace_size(M, N, K, 0) <= bnd.dora_matmul_int8_workspace_size(M, N, K, r)
 
 
