@@ -9,6 +9,12 @@
 // fp16 like the outputs, then runs through the same accumulators, which hold
 // the main sums divided by s and are multiplied by it at the end, so that s
 // costs no rounding of an operand.
+//
+// Large products are bound by the power of the matrix cores: the bare product
+// takes 351 us at 8192^3 on zeros (3.1 POP/s) and 449 on normally distributed
+// rows (2.4; four waves of 128 x 128 sums 474). Measured: 8192 x 8192 x 8192 with
+// r = 384, a residual and two bf16 outputs 531 to 543 us (the vendor's bare int8
+// product 546); 8192 x 28672 x 8192 1.54 ms, 1.60 with GELU (2.4 POP/s).
 #include "matmul_device.h"
 
 namespace dora {
@@ -26,7 +32,8 @@ namespace {
 // the few-rows kernel: a load takes 128 bytes of each of eight rows, and the
 // two diagonal 8 x 8 blocks of a 16 x 16 product are wanted.
 // The waves' sums, the pair's apart, meet in LDS, in one of two buffers, so that
-// a block takes one barrier.
+// a block takes one barrier. Bound by w's bytes: 16 x 28672 x 8192 with r = 384
+// 45 us (258 MB, 5.7 TB/s), 66 in the few-rows kernel.
 // ---------------------------------------------------------------------------
 constexpr int kWalkSteps = 8;   // of 128 bytes, a wave's share of the depth
 

@@ -7,7 +7,8 @@
 //
 // HBM bound: 3.03 bytes an element of 16 bits in groups of 128. A thread takes
 // 16 bytes of a row, so a group is 4 to 64 lanes of one wave and its maximum a
-// few lane exchanges: no LDS, no barrier.
+// few lane exchanges: no LDS, no barrier. Measured, 8192 x 8192 bf16 in groups
+// of 128: packing 37 to 38 us (5.4 TB/s), back 34 us (5.9 TB/s).
 #include "layer_norm_device.h"
 
 namespace dora {

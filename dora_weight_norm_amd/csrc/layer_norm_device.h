@@ -12,6 +12,10 @@
 //
 // HBM bound, as the RMS norm, whose row loads, shapes and grids these kernels
 // share: a row is read once into the registers of one wave or one workgroup.
+// Measured: 8192 x 8192 bf16 with a residual to h and int8 rows 83 us, 5.7 TB/s
+// (the RMS norm to e4m3 79); one row of 8192 4.0 us on the GPU; whole rows of
+// 8192 x 8192 to int8 38 us. Rows of 1024 threads took 104 to 118 us where 512
+// took 84 to 92.
 #pragma once
 
 #include "dora_launch.h"

@@ -13,7 +13,9 @@ namespace {
 // workgroup walks rows blockIdx.x, + gridDim.x, ... with its columns' weights
 // and both sums in registers (rows in increasing order) and stores one partial
 // row [dweight | dbias] at its end; a second kernel adds the partials in a
-// fixed order.
+// fixed order. HBM bound: 8192 x 4096 bf16 with dh 53 us, 47 of them the rows
+// (268 MB, 5.7 TB/s) and 4.5 the sums; twice or four times the workgroups, or
+// stores past the caches, took 56 to 60.
 // ---------------------------------------------------------------------------
 struct LayerNormBwdArgs {
   const void* dy;
