@@ -26,7 +26,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["dora_api.hip", "block_api.hip", "norm_kernels.hip", "compose_kernels.hip", "rms_norm_kernels.hip",
            "matmul_kernels.hip", "layer_norm_kernels.hip", "int8_rows_kernels.hip", "int8_matmul_kernels.hip",
-           "int8_backward_kernels.hip", "int8_api.hip"]
+           "int8_backward_kernels.hip", "backward_sides_kernels.hip", "int8_api.hip"]
 
 COMMON_FLAGS = [
     "--offload-arch=gfx950",

@@ -66,10 +66,7 @@ hipError_t launch_layer_norm_bwd(const void* dy, const void* dh, const void* h, 
                                  float* dbias, void* ws, hipStream_t st);
 hipError_t launch_quantize_rows(const void* x, int dtype, int64_t T, int64_t d, int64_t group, void* q, float* scale,
                                 hipStream_t st);
-// x [T][d] and x2 [T2][d] (T2 may be 0) at a row stride of ld elements (zeros from
-// d on, up to a whole chunk).
-hipError_t launch_dequantize_rows(const Int8Rows& r, int64_t T, void* x, const Int8Rows& r2, int64_t T2, void* x2,
-                                  int64_t d, int64_t ld, int dtype, hipStream_t st);
+hipError_t launch_dequantize_rows(const Int8Rows& r, int64_t T, int64_t d, int dtype, void* x, hipStream_t st);
 size_t fast_kernel_lds_bytes(int cfg);
 size_t gen_kernel_lds_bytes(int cfg);
 

@@ -88,7 +88,7 @@ struct MatmulBackwardPlan {
   int64_t rows;                                 // row blocks of the element-wise pass
   int64_t ldn, ldm, ldk;                        // padded N, M and K
   int cfg_dx, cfg_dw, splits_dx, splits_dw;
-  size_t off_du, off_dut, off_wt, off_xt, off_w8, off_x8, off_sum, off_part;
+  size_t off_du, off_dut, off_wt, off_xt, off_sum, off_part;
   size_t ws_bytes;
 };
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
@@ -98,6 +98,34 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
 struct HeldInt8 {
   Int8Rows u, x, w;
 };
+
+// What a backward's products need beside du, in one launch: the element-wise
+// pass's partial sums added up (part may be null where there are none), int8 rows
+// of w and x in the storage type at a row stride of ldk elements (16 bits), and
+// transposed fp32 copies dst[c][r] of src [rows][cols], or of rows8, with zeros up to a row of ld.
+struct Turned {
+  const void* src;
+  Int8Rows rows8;
+  int64_t rows, cols, lsrc, ld;
+  void* dst;
+};
+struct BackwardSides {
+  bool want_sums;
+  const float* part;
+  int n_part;
+  float* dbias;
+  float* dcol;
+  Int8Rows w8, x8;
+  void* w16;
+  void* x16;
+  Turned turned[3];
+  int n_turned;
+  void turn(const void* src, const Int8Rows& r, int64_t rows, int64_t cols, int64_t lsrc, int64_t ld, void* dst) {
+    turned[n_turned++] = Turned{src, r, rows, cols, lsrc, ld, dst};
+  }
+};
+hipError_t launch_backward_sides(const BackwardSides& b, int64_t M, int64_t N, int64_t K, int64_t ldk, int dtype,
+                                 hipStream_t st);
 
 hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int dtype, int64_t M, int64_t N,
                          int64_t K, const void* t, const void* b, int64_t r, float s, const Epilogue& ep,

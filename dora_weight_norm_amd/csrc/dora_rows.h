@@ -324,6 +324,51 @@ __device__ __forceinline__ float store_row_8(uint8_t* row, int lane, int64_t d, 
   return s;
 }
 
+// out0[j] (j < n0) or out1[j - n0] = sum of column j over the n_part rows of
+// part [n_part][n]; either output may be null. One workgroup owns 64 columns;
+// its sixteen waves each add a contiguous sixteenth of the rows in increasing
+// order (loads kSumBatch at a time), then wave 0 adds those sums in order.
+constexpr int kSumCols = 64, kSumSplit = 16, kSumBatch = 16, kSumThreads = kSumCols * kSumSplit;
+struct ColumnSum {
+  const float* part;
+  int n_part;
+  int64_t n;
+  float* out0;
+  int64_t n0;
+  float* out1;
+};
+[[maybe_unused]] unsigned sum_groups(int64_t n) { return (unsigned)((n + kSumCols - 1) / kSumCols); }
+
+__device__ __forceinline__ void column_sum(const ColumnSum& s, unsigned block) {
+  __shared__ float red[kSumSplit][kSumCols];
+  const int c = threadIdx.x % kSumCols, q = threadIdx.x / kSumCols;
+  const int64_t j = (int64_t)block * kSumCols + c, n = s.n;
+  const int y0 = (int)((int64_t)s.n_part * q / kSumSplit), y1 = (int)((int64_t)s.n_part * (q + 1) / kSumSplit);
+  float acc = 0.f;
+  if (j < n) {
+    const float* col = s.part + j;
+    int y = y0;
+    for (; y + kSumBatch <= y1; y += kSumBatch) {
+      float v[kSumBatch];
+#pragma unroll
+      for (int u = 0; u < kSumBatch; ++u) v[u] = col[(int64_t)(y + u) * n];
+#pragma unroll
+      for (int u = 0; u < kSumBatch; ++u) acc += v[u];
+    }
+    for (; y < y1; ++y) acc += col[(int64_t)y * n];
+  }
+  red[q][c] = acc;
+  __syncthreads();
+  if (q != 0 || j >= n) return;
+#pragma unroll
+  for (int k = 1; k < kSumSplit; ++k) acc += red[k][c];
+  if (j < s.n0) {
+    if (s.out0) s.out0[j] = acc;
+  } else if (s.out1) {
+    s.out1[j - s.n0] = acc;
+  }
+}
+
 // Threads and chunks a thread that hold a row of d elements; nt 0: too long.
 struct RowShape {
   int nt, c;

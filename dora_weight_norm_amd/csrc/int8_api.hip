@@ -116,8 +116,8 @@ dora_status dora_dequantize_rows(const int8_t* q, const float* scale, int64_t T,
   const Span out[] = {{x, T * d * es, (size_t)es}};
   const unsigned same[] = {0u};
   if (!buffers_ok(in, 2, out, 1, same)) return DORA_ERR_INVALID_ARG;
-  return hip_status(launch_dequantize_rows(Int8Rows{reinterpret_cast<const uint8_t*>(q), scale, group}, T, x, Int8Rows{}, 0,
-                                           nullptr, d, d, dtype, static_cast<hipStream_t>(stream)));
+  return hip_status(launch_dequantize_rows(Int8Rows{reinterpret_cast<const uint8_t*>(q), scale, group}, T, d, dtype, x,
+                                           static_cast<hipStream_t>(stream)));
 }
 
 dora_status dora_matmul_int8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int aligned_operands,

@@ -21,28 +21,6 @@ namespace dora {
 
 namespace {
 
-// dst[c][r] = src[r][c] for src [rows][cols] at row stride lds_; dst rows of
-// stride ld >= rows, zeros from `rows` on. 64 x 64 tiles through LDS.
-template <typename U>
-__global__ __launch_bounds__(256) void transpose_kernel(const U* src, int64_t rows, int64_t cols, int64_t lsrc,
-                                                        int64_t ld, U* dst) {
-  __shared__ U tile[64][65];
-  const int64_t nr = (ld + 63) / 64;   // row tiles (of the destination's stride, so that its padding is written)
-  const int64_t r0 = blockIdx.x % nr * 64, c0 = blockIdx.x / nr * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t r = r0 + i * 4 + ty, c = c0 + tx;
-    tile[i * 4 + ty][tx] = (r < rows && c < cols) ? src[r * lsrc + c] : U(0);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t c = c0 + i * 4 + ty, r = r0 + tx;
-    if (c < cols && r < ld) dst[c * ld + r] = tile[tx][i * 4 + ty];
-  }
-}
-
 // Element-wise part of the backward: z from u, dz = dy act'(z), du = row_scale
 // col_scale dz (rounded to the storage type: it is the operand of both
 // products, which the matrix cores take in 16 bits), and this row block's sums
@@ -369,18 +347,6 @@ hipError_t gemm(const GemmArgs& g, int dtype, int out_dtype, int cfg, hipStream_
   }
 }
 
-hipError_t transpose(const void* src, int64_t rows, int64_t cols, int64_t lsrc, int64_t ld, int esz, void* dst,
-                     hipStream_t st) {
-  const dim3 grid((unsigned)((ld + 63) / 64 * ((cols + 63) / 64)));
-  if (esz == 2)
-    hipLaunchKernelGGL((transpose_kernel<uint16_t>), grid, dim3(256), 0, st, static_cast<const uint16_t*>(src), rows,
-                       cols, lsrc, ld, static_cast<uint16_t*>(dst));
-  else
-    hipLaunchKernelGGL((transpose_kernel<uint32_t>), grid, dim3(256), 0, st, static_cast<const uint32_t*>(src), rows,
-                       cols, lsrc, ld, static_cast<uint32_t*>(dst));
-  return hipGetLastError();
-}
-
 }  // namespace
 
 MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, int al) {
@@ -488,8 +454,6 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
   p.off_wt = take(!need_dx ? 0 : (p.direct ? (w_copy ? w_bytes : 0) : (size_t)(K * p.ldn) * esz));
   p.off_dut = take(need_dw && !p.direct ? (size_t)(N * p.ldm) * esz : 0);
   p.off_xt = take(!need_dw ? 0 : (p.direct ? (x_copy ? x_bytes : 0) : (size_t)(K * p.ldm) * esz));
-  p.off_w8 = take(p.w8 && !p.direct ? w_bytes : 0);
-  p.off_x8 = take(p.x8 && !p.direct ? x_bytes : 0);
   size_t part = 0;
   if (need_dx) {
     if (p.splits_dx > 1) part = (size_t)(p.splits_dx * M * K) * 4;
@@ -543,22 +507,23 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (want_sums && N > 0) {
-    e = launch_column_sum(sums, M > 0 ? (int)p.rows : 0, 2 * N, dbias, N, dcol, st);
-    if (e != hipSuccess) return e;
+  // The sums, and operands of the products that are not read as they lie: int8
+  // rows in the storage type, transposed copies.
+  BackwardSides side{};
+  side.want_sums = want_sums && N > 0;
+  side.part = sums, side.n_part = M > 0 ? (int)p.rows : 0, side.dbias = dbias, side.dcol = dcol;
+  const bool w_back = p.direct && p.w8 && !p.w8_tile, x_back = p.direct && p.x8 && !p.x8_tile;
+  if (w_back) side.w8 = held.w, w = side.w16 = ws + p.off_wt;
+  if (x_back) side.x8 = held.x, x = side.x16 = ws + p.off_xt;
+  if (!p.direct && M > 0 && K > 0 && N > 0) {
+    if (dx) side.turn(w, held.w, N, K, K, p.ldn, ws + p.off_wt);
+    if (dw) side.turn(d, Int8Rows{}, M, N, p.ldn, p.ldm, ws + p.off_dut);
+    if (dw) side.turn(x, held.x, M, K, K, p.ldm, ws + p.off_xt);
   }
+  e = launch_backward_sides(side, M, N, K, p.ldk, dtype, st);
+  if (e != hipSuccess) return e;
   GemmArgs g{};
   g.part = reinterpret_cast<float*>(ws + p.off_part);
-  // Int8 rows back to the storage type, both operands in one launch.
-  const bool w_back = p.w8 && !p.w8_tile, x_back = p.x8 && !p.x8_tile;
-  char* w16 = ws + (p.direct ? p.off_wt : p.off_w8);
-  char* x16 = ws + (p.direct ? p.off_xt : p.off_x8);
-  if (w_back) w = w16;
-  if (x_back) x = x16;
-  if (K > 0 && (w_back ? N : 0) + (x_back ? M : 0) > 0) {
-    e = launch_dequantize_rows(held.w, w_back ? N : 0, w16, held.x, x_back ? M : 0, x16, K, p.ldk, dtype, st);
-    if (e != hipSuccess) return e;
-  }
   if (p.direct) {
     if (p.copy) {
       PackJobs jobs{};
@@ -594,20 +559,12 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     return e;
   }
   if (dx && M > 0 && K > 0) {
-    if (N > 0) e = transpose(w, N, K, p.w8 ? p.ldk : K, p.ldn, esz, ws + p.off_wt, st);
-    if (e != hipSuccess) return e;
     g.a = d, g.b = ws + p.off_wt, g.lda = p.ldn, g.ldb = p.ldn, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
     g.ep.y = dx;
     e = gemm(g, dtype, dtype, p.cfg_dx, st);
     if (e != hipSuccess) return e;
   }
   if (dw && N > 0 && K > 0) {
-    if (M > 0) {
-      e = transpose(d, M, N, p.ldn, p.ldm, esz, ws + p.off_dut, st);
-      if (e != hipSuccess) return e;
-      e = transpose(x, M, K, p.x8 ? p.ldk : K, p.ldm, esz, ws + p.off_xt, st);
-      if (e != hipSuccess) return e;
-    }
     g.a = ws + p.off_dut, g.b = ws + p.off_xt, g.lda = p.ldm, g.ldb = p.ldm, g.K = M, g.M = N, g.N = K;
     g.splits = p.splits_dw;
     g.ep.y = dw;

@@ -347,42 +347,7 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_long_kernel(NormBwdArgs a) 
   }
 }
 
-// out0[j] (j < n0) or out1[j - n0] = sum of column j over the n_part rows of
-// part [n_part][n]; either output may be null. One workgroup owns 64 columns;
-// its sixteen waves each add a contiguous sixteenth of the rows in increasing
-// order (loads kSumBatch at a time), then wave 0 adds those sums in order.
-constexpr int kSumCols = 64, kSumSplit = 16, kSumBatch = 16;
-
-__global__ __launch_bounds__(kSumCols* kSumSplit) void column_sum_kernel(const float* part, int n_part, int64_t n,
-                                                                          float* out0, int64_t n0, float* out1) {
-  __shared__ float red[kSumSplit][kSumCols];
-  const int c = threadIdx.x % kSumCols, q = threadIdx.x / kSumCols;
-  const int64_t j = (int64_t)blockIdx.x * kSumCols + c;
-  const int y0 = (int)((int64_t)n_part * q / kSumSplit), y1 = (int)((int64_t)n_part * (q + 1) / kSumSplit);
-  float acc = 0.f;
-  if (j < n) {
-    const float* col = part + j;
-    int y = y0;
-    for (; y + kSumBatch <= y1; y += kSumBatch) {
-      float v[kSumBatch];
-#pragma unroll
-      for (int u = 0; u < kSumBatch; ++u) v[u] = col[(int64_t)(y + u) * n];
-#pragma unroll
-      for (int u = 0; u < kSumBatch; ++u) acc += v[u];
-    }
-    for (; y < y1; ++y) acc += col[(int64_t)y * n];
-  }
-  red[q][c] = acc;
-  __syncthreads();
-  if (q != 0 || j >= n) return;
-#pragma unroll
-  for (int k = 1; k < kSumSplit; ++k) acc += red[k][c];
-  if (j < n0) {
-    if (out0) out0[j] = acc;
-  } else if (out1) {
-    out1[j - n0] = acc;
-  }
-}
+__global__ __launch_bounds__(kSumThreads) void column_sum_kernel(ColumnSum s) { column_sum(s, blockIdx.x); }
 
 template <typename T>
 hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
@@ -448,8 +413,8 @@ hipError_t launch_bwd(NormBwdArgs a, float* dweight, hipStream_t st) {
 
 hipError_t launch_column_sum(const float* part, int n_part, int64_t n, float* out0, int64_t n0, float* out1,
                              hipStream_t st) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumSplit), 0,
-                     st, part, n_part, n, out0, n0, out1);
+  const ColumnSum s{part, n_part, n, out0, n0, out1};
+  hipLaunchKernelGGL(column_sum_kernel, dim3(sum_groups(n)), dim3(kSumThreads), 0, st, s);
   return hipGetLastError();
 }
 

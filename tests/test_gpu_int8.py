@@ -673,6 +673,23 @@ def test_backward_offsets_past_32_bits():
     assert not du[:-n].any()
 
 
+def test_transposed_copies_of_more_tiles_than_workgroups():
+    """Rows whose fp32 copies are more 64 x 64 tiles than one launch has workgroups for them."""
+    M, K, n = 2000070, 130, 150
+    rng = np.random.default_rng(35)
+    x = bnd.Int8Rows(torch.randint(-127, 128, (M, K), device="cuda", dtype=torch.int8), torch.full((M,), 0.25, device="cuda"))
+    u = bnd.Int8Rows(x.q[:, :1].contiguous(), x.scale)
+    at = torch.randint(0, M, (n,), device="cuda").unique()
+    dy = torch.zeros(M, 1, device="cuda")
+    dy[at] = torch.from_numpy(rng.integers(-4, 5, (len(at), 1)).astype(np.float32)).cuda()
+    w = bnd.Int8Rows(torch.randint(-127, 128, (1, K), device="cuda", dtype=torch.int8), torch.full((1,), 0.5, device="cuda"))
+    dx, dw, db, dc, du = bnd.dora_matmul_backward_int8(dy, u, x, w)
+    # (whole numbers times powers of two: every sum is exact)
+    want = (dy[at] * x.q[at].float() * 0.25).sum(0, keepdim=True)
+    assert torch.equal(du, dy) and torch.equal(dx, dy * (w.q.float() * 0.5))
+    assert torch.equal(dw, want) and dc.item() == want[0, 0].item() and db.item() == dy.sum().item()
+
+
 @pytest.mark.parametrize("M,N,K", [(0, 384, 4096), (8200, 0, 4096), (8200, 384, 0)])
 def test_empty_int8_backward(M, N, K):
     dt, i8 = torch.bfloat16, torch.int8
