@@ -72,7 +72,7 @@ inline bool backward_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t es) {
 
 // A product's plan as its query gives it.
 inline void plan_fields(const MatmulPlan& p, bool any, int64_t* info, int n_info) {
-  const int rows = p.cfg == kTile256 ? 256 : (p.cfg == kTile128 ? 128 : (p.cfg == kTile64 ? 64 : 0));
+  const int rows = p.cfg == kTile256 ? 256 : (p.cfg == kTile128 ? 128 : (p.cfg == kTile64 || p.cfg == kAny64 ? 64 : 0));
   const int copies = (p.pack_x ? 1 : 0) | (p.pack_w ? 2 : 0) | (p.pack_t ? 4 : 0) | (p.pack_b ? 8 : 0);
   const int few = p.cfg == kFew8 || p.cfg == kWalk8 ? 8
                   : (p.cfg == kFew16 || p.cfg == kWalk16 ? 16 : (p.cfg == kFew32 ? 32 : -1));

@@ -53,9 +53,11 @@ struct GemmArgs {
 
 // Kernels: tiles of 256, 128 or 64 rows and columns, or the few-rows kernel on
 // 8 rows by 16 columns, 16 by 16 or 32 by 32.
-// 8-bit integers have a kernel of their own for up to 8 or 16 rows.
+// 8-bit integers have kernels of their own for up to 8 or 16 rows, and for tiles of
+// 64 whose operands lie at any address.
 enum MatmulTile : int {
-  kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4, kFew32 = 5, kWalk8 = 6, kWalk16 = 7
+  kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4, kFew32 = 5, kWalk8 = 6, kWalk16 = 7,
+  kAny64 = 8
 };
 
 struct MatmulPlan {

@@ -158,8 +158,205 @@ hipError_t launch_walk_any(GemmArgs g, hipStream_t st) {
   return launch_walk<O, TF, false>(g, st);
 }
 
+// ---------------------------------------------------------------------------
+// 64 x 64 of a product whose rows lie at any address: four waves of 32 x 32 sums.
+// The tiles' direct loads take whole aligned chunks of 16 bytes, for which rows off
+// that grid are copied first; here they go through registers, two stages of 128
+// bytes ahead, the chunk at a row's end as its last 16 bytes, shifted (rows of at
+// least 16 bytes). Bound by a memory latency for every two stages, which several
+// workgroups a compute unit hide: four or eight stages ahead take the registers of
+// theirs (64 x 8192 x 8189 22.2 us with two, 23.5 with four, 28.8 with eight). 333 x
+// 1001 x 777 with r = 24: 9.7 us on the GPU, 10.7 behind copies, 11.4 and 16 with
+// the host's call. The sums are scaled and joined as in the other tiles, so that an
+// operand's address does not change a result.
+// ---------------------------------------------------------------------------
+// Sixteen bytes without the first `drop` of them, zeros behind.
+__device__ __forceinline__ u32x4 dropped(u32x4 v, int drop) {
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  if (drop >= 8) lo = hi, hi = 0, drop -= 8;
+  if (drop >= 8) lo = 0, drop = 0;
+  if (drop > 0) lo = lo >> (8 * drop) | hi << (64 - 8 * drop), hi >>= 8 * drop;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+template <typename O, bool PAIR>
+__global__ __launch_bounds__(256) void int8_any_kernel(GemmArgs g) {
+  using TP = typename PairType<int8x_t, O>::type;
+  constexpr int AHEAD = 2, BUF = 128 * 128, LD = 68;   // LD: floats of an epilogue row (padded)
+  __shared__ __align__(16) char lds[2 * BUF];          // [2][a's 64 rows, b's 64 rows][128]; then the sums
+  static_assert(64 * LD * 4 <= 2 * BUF, "the epilogue fits");
+  __shared__ __align__(16) float scales[2][64];        // with a pair: of the rows and the columns
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, fg = lane >> 5;
+  const int total = g.n_mt * g.n_nt, split = blockIdx.x / total, id = blockIdx.x - split * total;
+  const int64_t m0 = (int64_t)(id % g.n_mt) * 64, n0 = (int64_t)(id / g.n_mt) * 64;
+  // A thread takes chunk c of rows r and r + 32 of both operands. (Rows past the
+  // end read the last one's and are not stored.)
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+  const char *p[4], *p2[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t at = (i < 2 ? m0 : n0) + r + 32 * (i % 2), last = (i < 2 ? g.M : g.N) - 1, row = at < last ? at : last;
+    p[i] = static_cast<const char*>(i < 2 ? g.a : g.b) + row * (i < 2 ? g.lda : g.ldb);
+    p2[i] = static_cast<const char*>(i < 2 ? g.a2 : g.b2) + row * (i < 2 ? g.lda2 : g.ldb2) * 2;
+  }
+  const int n1 = (int)((g.K + 127) / 128), st0 = split * g.stages_per_split;
+  const int st1 = st0 + g.stages_per_split < g.stages ? st0 + g.stages_per_split : g.stages;
+  // Of the result a thread has eight columns of rows r and r + 32; what scales them
+  // is asked for here, a depth before it is needed.
+  const int64_t n = n0 + c * 8, m[2] = {m0 + r, m0 + r + 32}, off[2] = {m[0] * g.N + n, m[1] * g.N + n};
+  const int nv = (int)(g.N - n < 8 ? g.N - n : 8);
+  const bool ok[2] = {nv > 0 && m[0] < g.M, nv > 0 && m[1] < g.M};
+  float ws[8], cs[8], bs[8];
+  if constexpr (PAIR) {
+    if (threadIdx.x < 128) {
+      const bool cols = threadIdx.x >= 64;   // (uniform over a wave)
+      const int64_t at = (cols ? n0 : m0) + lane, end = cols ? g.N : g.M;
+      scales[cols][lane] = (cols ? g.w_scale : g.pair_rows)[at < end ? at : end - 1];
+    }
+  } else {
+    load8<float>(g.w_scale + n, nv, ws);
+  }
+  column_terms(g.ep, n, nv, cs, bs);
+  Raw8<O> res[2] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (ok[i] && g.ep.residual != nullptr && g.splits == 1)
+      res[i] = load_raw8<O>(static_cast<const O*>(g.ep.residual) + off[i], nv);
+  // Bytes of the depth before a stage, and of the whole: the main one's, or the pair's.
+  auto depth = [&](int st, int& k, int& len) __attribute__((always_inline)) {
+    const bool pair = PAIR && st >= n1;   // (uniform)
+    k = (pair ? st - n1 : st) * 128, len = (int)(pair ? g.K2 * 2 : g.K);
+    return pair;
+  };
+  // (Every stage issues four loads, those past the depth of its last bytes again:
+  // with a number that depends on the lane, a use would wait for them all.)
+  u32x4 v[AHEAD][4];
+  auto load = [&](int st, u32x4 (&to)[4]) __attribute__((always_inline)) {
+    int k, len;
+    const bool pair = depth(st < st1 ? st : st1 - 1, k, len);
+    k += c * 16;
+    const int at = k + 16 <= len ? k : len - 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = *reinterpret_cast<const u32x4_any*>((PAIR && pair ? p2[i] : p[i]) + at);
+  };
+  // (in the order of their uses, and so in the loop)
+#pragma unroll
+  for (int j = 0; j < AHEAD; ++j) {
+    load(st0 + j, v[j]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  f32x16 acc;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  // Values 4q to 4q + 3 of a lane are columns 8q + 4 fg and on of row fr. With a pair
+  // the sums are scaled before its products are added, as in the other tiles.
+  auto scaled = [&]() __attribute__((always_inline)) {
+    const float rs = scales[0][wm * 32 + fr];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x4 w4 = *reinterpret_cast<const f32x4*>(&scales[1][wn * 32 + 8 * q + 4 * fg]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[4 * q + e] = (float)__float_as_int(acc[4 * q + e]) * rs * w4[e] * g.inv_s;
+    }
+  };
+  auto stage = [&](int j, int st, auto more) __attribute__((always_inline)) {
+    char* buf = lds + (j & 1) * BUF;
+    int k, len;
+    const bool pair = depth(st, k, len);
+    if (k + 128 > len) {   // (uniform)
+      const int over = k + c * 16 + 16 - len;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = dropped(v[j][i], over < 0 ? 0 : (over < 16 ? over : 16));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = r + 32 * i;   // (b's rows behind a's)
+      *reinterpret_cast<u32x4*>(buf + row * 128 + (c ^ ((row >> 1) & 7)) * 16) = v[j][i];
+    }
+    if constexpr (decltype(more)::value) load(st + AHEAD, v[j]);
+    // (the waves a stage ahead write the other half, which all have read by now)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    barrier_keep_loads();
+    if (PAIR && pair && st == (n1 > st0 ? n1 : st0)) scaled();
+    u32x4 fa[4], fb[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int at = ((s * 2 + fg) ^ ((fr >> 1) & 7)) * 16;
+      fa[s] = *reinterpret_cast<const u32x4*>(buf + (wm * 32 + fr) * 128 + at);
+      fb[s] = *reinterpret_cast<const u32x4*>(buf + (64 + wn * 32 + fr) * 128 + at);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {   // (turned: a lane holds a row's columns)
+      if (PAIR && pair)
+        acc = Op<TP>::run(&fb[s], &fa[s], acc);
+      else
+        acc = Op<int8x_t>::run(&fb[s], &fa[s], acc);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int base = st0;
+  for (; base + AHEAD <= st1; base += AHEAD) {
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) stage(j, base + j, Tag<true>{});
+  }
+#pragma unroll
+  for (int j = 0; j + 1 < AHEAD; ++j)
+    if (base + j < st1) stage(j, base + j, Tag<false>{});   // (uniform)
+  __syncthreads();
+  if constexpr (PAIR) {
+    if (st1 <= n1) scaled();
+    acc *= g.s;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = (float)__float_as_int(acc[e]);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<f32x4*>(lds + ((wm * 32 + fr) * LD + wn * 32 + 8 * q + 4 * fg) * 4) =
+        f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+  __syncthreads();
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[8 * i + e] = reinterpret_cast<const float*>(lds)[(r + 32 * i) * LD + c * 8 + e];
+      if constexpr (!PAIR) f[8 * i + e] *= ws[e];
+    }
+  if (g.splits > 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = f[8 * i + e];
+      if (ok[i]) store8<float>(g.part + (int64_t)split * g.M * g.N + off[i], nv, o);
+    }
+  } else {
+    epilogue_rows<O, 2>(g.ep, f, cs, bs, m, off, ok, nv, res);
+  }
+}
+
+template <typename O>
+hipError_t launch_any(GemmArgs g, hipStream_t st) {
+  split_stages(g, 128, 64);
+  g.n_mt = (int)((g.M + 63) / 64), g.n_nt = (int)((g.N + 63) / 64);
+  const dim3 grid((unsigned)((int64_t)g.n_mt * g.n_nt * g.splits)), block(256);
+  if constexpr (sizeof(O) == 2) {
+    if (g.K2 > 0)
+      hipLaunchKernelGGL((int8_any_kernel<O, true>), grid, block, 0, st, g);
+    else
+      hipLaunchKernelGGL((int8_any_kernel<O, false>), grid, block, 0, st, g);
+  } else {
+    hipLaunchKernelGGL((int8_any_kernel<O, false>), grid, block, 0, st, g);
+  }
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || g.splits == 1 ? e : launch_join<O>(g, st);
+}
+
 template <typename O>
 hipError_t launch(GemmArgs g, int cfg, hipStream_t st) {
+  if (cfg == kAny64) return launch_any<O>(g, st);
   if (cfg == kWalk8) return launch_walk_any<O, 1>(g, st);
   if (cfg == kWalk16) return launch_walk_any<O, 2>(g, st);
   if (cfg == kFew8) return launch_few_rows<int8x_t, O, 2, 1>(g, st);

@@ -278,6 +278,28 @@ bool int8_tiles(int64_t M, int64_t N, int64_t K) {
   return (N >= 4 * 16 * kCUs && K <= 2048) || (M > 12 && K > 8192 && N * K > (int64_t)1 << 27);
 }
 
+// Whether 64-row tiles of 8-bit integers take rows off the 16-byte grid as they are
+// (int8_any_kernel), or behind copies: a copy costs a launch and its bytes, loads
+// through registers half as much again for each stage of each tile. A pair's
+// copies are small. (By sizes alone: a workspace for operands at any address serves
+// them at all.) Measured, behind copies against as they are, us of the whole call:
+//    333 x 1001 x  777, r = 24   16.5, 10.9      2304 stages of all tiles
+//     64 x 8192 x 8189           44.2, 22.2      8192
+//    128 x 8192 x 8189           48.2, 35.3     16384
+//    256 x 4096 x 8191           36.1, 35.1     16384
+//    500 x 4000 x 5001           39.9, 39.3     20160
+//   1000 x 1700 x 8190           40.6, 49.1     27648
+// the pair alone, by the stages of a workgroup,
+//    128 x 8192 x  512, r = 390  14.9, 11.0     11
+//   1000 x 1000 x 2000, r = 13   15.4, 13.7     17
+//     64 x 8192 x 8192, r = 13   22.9, 19.9     17
+//   1000 x 1000 x 4000, r = 13   18.7, 21.6     33
+bool int8_anywhere(int64_t M, int64_t N, int64_t K, int64_t r, int splits) {
+  if (K < 16 || (r > 0 && r < 8)) return false;
+  const int64_t tiles = up(M, 64) / 64 * (up(N, 64) / 64), stages = up(K, 128) / 128 + up(r, 64) / 64;
+  return tiles * stages <= 20000 && (K % 16 != 0 || stages <= 20 * splits);
+}
+
 // Whether the walking kernel takes a product of 8-bit integers: whole steps of
 // 128 bytes, eight a wave at most, a pair of one step a wave in whole chunks, and
 // two blocks of columns or more for a compute unit; up to 8 rows, for which the
@@ -355,6 +377,8 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   size_t off = 0;
   const bool i8 = dtype == kInt8Operands, tiles = i8 && int8_tiles(M, N, K);
   choose_tile(M, N, up(K, KT) / KT, dtype, tiles ? 0 : (K % epc == 0 ? kFewOnGrid : kFewOffGrid), &p.cfg, &p.splits);
+  const bool off_grid = K % 16 != 0 || (al & 3) != 3 || (r > 0 && (r % 8 != 0 || (al & 12) != 12));
+  if (i8 && p.cfg == kTile64 && off_grid && int8_anywhere(M, N, K, r, p.splits)) p.cfg = kAny64;
   if (i8 && !tiles && int8_walks(M, N, K, r)) p.cfg = M <= 8 ? kWalk8 : kWalk16, p.splits = 1;
   auto operand = [&](int64_t rows, int64_t depth, int es, int bit, bool* pack, int64_t* ld, size_t* at) {
     // (the few-rows kernel reads rows at any element address)
@@ -393,7 +417,7 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
   g.ep = ep;
   if (dtype == kInt8Operands) {
     g.w_scale = w_scale;
-    if (r > 0 || p.cfg >= kWalk8) {   // (the pair's products are added to scaled sums, and s multiplies both)
+    if (r > 0 || p.cfg == kWalk8 || p.cfg == kWalk16) {   // (the pair's products are added to scaled sums, and s multiplies both)
       g.pair_rows = ep.row_scale, g.ep.row_scale = nullptr;
       g.inv_s = 1.f / s;
     }

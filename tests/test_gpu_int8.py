@@ -316,7 +316,7 @@ def test_int8_refusals_of_the_binding():
     with pytest.raises(bnd.DoraError):
         bnd.dora_matmul_int8(x, w, xs, ws, s=float("inf"))
     with pytest.raises(ValueError):
-        bnd.dora_matmul_int8(torch.zeros(40, 63, device=dev, dtype=i8), w[:, :63].contiguous(), torch.ones(40, device=dev),
+        bnd.dora_matmul_int8(torch.zeros(40, 15, device=dev, dtype=i8), w[:, :15].contiguous(), torch.ones(40, device=dev),
                              ws, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
     for bad in (dict(group=48), dict(q=x.float()), dict(scale=ws)):
         with pytest.raises((ValueError, TypeError)):
@@ -581,6 +581,40 @@ def test_few_rows_in_tiles(M, N, K, r, out):
     assert bnd.dora_matmul_int8_plan_info(M, N, K, r)["tile_rows"] > 0
     o, rng = operands(M, N, K, r, out, M + N + K)
     check(o, rng, out, ACTS[(M + N + K) % 5], M % 2 == 0, True)
+
+
+# Small tiles on rows at any address: ends of every length in a row's last chunk, of x and w or the pair alone, one stage
+# and many, a split depth, the shortest rows, and results off 16 bytes.
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K,r", [(333, 1001, 777, 24), (65, 700, 16, 8), (70, 900, 17, 9), (300, 520, 8189, 0),
+                                     (64, 8192, 1025, 77), (40, 5000, 127, 63), (257, 321, 128, 13), (400, 300, 255, 130),
+                                     (33, 4111, 784, 500), (1000, 1000, 1001, 11), (129, 777, 31, 15)]
+                         + [(100, 1000, 256 + e, 0) for e in range(1, 16)])
+def test_tiles_on_rows_at_any_address(M, N, K, r, out):
+    r = 0 if out == "f32" else r
+    o, rng = operands(M, N, K, r, out, M + N + K)
+    check(o, rng, out, ACTS[(M + N + K) % 5], M % 2 == 0, True)
+
+
+def test_tiles_at_any_address_stay_in_their_rows():
+    """Operands off 16 bytes inside larger buffers whose other bytes would show; the same values from aligned ones."""
+    rng = np.random.default_rng(36)
+    M, N, K, r = 100, 333, 640, 16
+    o, _ = operands(M, N, K, r, "bf16", 36)
+
+    def inside(t, by):
+        buf = torch.full((t.numel() + 64,), 77, device="cuda", dtype=t.dtype)
+        buf[by:by + t.numel()] = t.flatten()
+        return buf[by:by + t.numel()].view(t.shape)
+
+    want, _ = bnd.dora_matmul_int8(**o)
+    moved = {k: inside(v, 3) if k in ("x", "w", "t", "b") else v for k, v in o.items()}
+    got, _ = bnd.dora_matmul_int8(**moved)
+    assert torch.equal(got, want)
+    x, w, xs, ws = (torch.ones(s, device="cuda", dtype=d) for s, d in (((100, 300), torch.int8), ((333, 300), torch.int8),
+                                                                     ((100,), torch.float32), ((333,), torch.float32)))
+    y, _ = bnd.dora_matmul_int8(inside(x, 5), inside(w, 9), xs, ws, out_dtype=torch.float32)
+    assert (y == 300).all()
 
 
 def aligned_rows(rng, shape, dtype, group):

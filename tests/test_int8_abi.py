@@ -102,8 +102,8 @@ def test_int8_product_refusals():
     assert _mm(**{**pair, "t": 0x6000001}) == 1 and _mm(bias=0x4000002) == 1 and _mm(w_scale=0x2900002) == 1
     assert _mm(y=0x1000000) == 1 and _mm(y=0x2000010) == 1 and _mm(y=0x2800000) == 1 and _mm(u=0x2900000) == 1
     assert _mm(residual=0x5000010) == 1 and _mm(u=0x5000000) == 1
-    assert _mm(M=40, K=63, ws_bytes=64) == 4 and _mm(M=40, K=63, ws=None) == 4 and _mm(M=40, K=63, ws=0x8000010) == 4
-    assert _mm(M=40, K=63, ws=0x2000000) == 1 and _mm(M=40, K=63, ws=0x2800000) == 1
+    assert _mm(M=40, K=15, ws_bytes=64) == 4 and _mm(M=40, K=15, ws=None) == 4 and _mm(M=40, K=15, ws=0x8000010) == 4
+    assert _mm(M=40, K=15, ws=0x2000000) == 1 and _mm(M=40, K=15, ws=0x2800000) == 1
     assert _mm(M=0) == 0 and _mm(N=0) == 0
 
 
@@ -119,18 +119,29 @@ def test_int8_product_plans():
     assert plan(16, 8192, 28672, 0)[0] == 64 and plan(12, 8192, 28672, 0)[3] == 16 and plan(16, 8192, 16384, 0)[3] == 16
     assert plan(32, 28672, 8189, 0)[3] == 32 and plan(32, 1024, 4096, 0)[3] == 16 and plan(16, 8192, 1024, 0)[3] == 16
     # rows of no whole 16-byte chunks: x and w in bytes, the pair in 16 bits
-    assert plan(333, 1001, 776, 24)[2] == 3 and plan(333, 1001, 784, 20)[2] == 12
-    assert plan(333, 1001, 784, 24, aligned_operands=11)[2] == 4
+    assert plan(3330, 2001, 776, 24)[2] == 3 and plan(3330, 2001, 784, 20)[2] == 12
+    assert plan(3330, 2001, 784, 24, aligned_operands=11)[2] == 4
+    # ... unless small tiles take them as they are
+    for a in ((333, 1001, 776, 24), (333, 1001, 784, 20), (64, 8192, 8189, 0), (128, 8192, 512, 390)):
+        assert plan(*a)[0] == 64 and plan(*a)[2] == 0
+    assert plan(333, 1001, 784, 24, aligned_operands=11)[2] == 0
+    assert plan(1000, 1700, 8190, 0)[2] == 3 and plan(1000, 1000, 4000, 13)[2] == 12
+    assert plan(333, 1001, 15, 0)[2] == 3 and plan(333, 1001, 784, 7)[2] == 12
     assert bnd.dora_matmul_int8_plan_info(0, 8, 8, 0)["tile_rows"] == -1
     assert bnd.dora_matmul_int8_workspace_size(4096, 4096, 4095, 0) >= 2 * 4096 * 4096
     sz = ctypes.c_size_t()
     f = bnd.load().dora_matmul_int8_workspace_size
     assert f(4, 4, 131072, 0, 15, ctypes.byref(sz)) == 1 and f(4, 4, 131071, 0, 15, ctypes.byref(sz)) == 0
     assert f(4, 4, 4, 0, 15, None) == 1
+    # a workspace for operands at any address serves them at all
+    for M, N, K, r in ((333, 1001, 776, 24), (1000, 1000, 4000, 13), (64, 8192, 8192, 13), (100, 2000, 3008, 16),
+                       (1000, 1700, 8190, 0), (1000, 1700, 8192, 5), (3330, 2001, 784, 20), (333, 1001, 15, 7)):
+        sizes = [bnd.dora_matmul_int8_workspace_size(M, N, K, r, al) for al in range(16)]
+        assert max(sizes) == sizes[0], (M, N, K, r)
     # a call whose s is 0 needs no more than the query with the pair says
     for M, N, K, r in ((40, 300, 63, 5), (300, 520, 4104, 700), (1000, 1000, 100, 64),
                        (32, 8192, 8192, 20), (17, 4096, 14336, 5), (1, 28672, 2048, 7), (32, 28672, 512, 600),
-                       (16, 8192, 24576, 9)):
+                       (16, 8192, 24576, 9), (64, 8192, 8192, 13), (1000, 1000, 4000, 13), (333, 1001, 777, 7)):
         assert bnd.dora_matmul_int8_workspace_size(M, N, K, 0) <= bnd.dora_matmul_int8_workspace_size(M, N, K, r)
 
 
