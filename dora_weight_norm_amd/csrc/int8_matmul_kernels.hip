@@ -13,8 +13,8 @@
 // Large products are bound by the power of the matrix cores: the bare product
 // takes 351 us at 8192^3 on zeros (3.1 POP/s) and 449 on normally distributed
 // rows (2.4; four waves of 128 x 128 sums 474). Measured: 8192 x 8192 x 8192 with
-// r = 384, a residual and two bf16 outputs 531 to 543 us (the vendor's bare int8
-// product 546); 8192 x 28672 x 8192 1.54 ms, 1.60 with GELU (2.4 POP/s).
+// r = 384, a residual and two bf16 outputs 528 to 547 us (the vendor's bare int8
+// product 546); 8192 x 28672 x 8192 1.54 ms, 1.57 to 1.63 with GELU (2.4 POP/s).
 #include "matmul_device.h"
 
 namespace dora {
