@@ -249,10 +249,16 @@ struct RowQuotient {
   }
 };
 
-// The scale of integers: 1 for a row of zeros, at least kMinScale otherwise, NaN
-// or infinite where the largest value is.
+// The scale of integers, max |x| / 127 correctly rounded in fp32: the product with
+// the rounded reciprocal and its exact remainder's share, as in RowQuotient (equal
+// to the division for every fp32 maximum from 2^-93 on; the product alone is a
+// step off for one in forty of them, among them six of the 128 significands of
+// bf16, where half of the maximum then came out as 64 instead of 63). 1 for a row
+// of zeros, at least kMinScale otherwise, NaN or infinite where the largest value is.
 __device__ __forceinline__ float int8_scale_of(uint32_t top_bits) {
-  const float s = __uint_as_float(top_bits) * (1.f / kInt8Max);
+  constexpr float kInv = 1.f / kInt8Max;
+  const float top = __uint_as_float(top_bits), q = top * kInv;
+  const float s = top_bits < 0x7f800000u ? fmaf(fmaf(-q, kInt8Max, top), kInv, q) : q;
   return top_bits == 0 ? 1.f : (s < kMinScale ? kMinScale : s);
 }
 

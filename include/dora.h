@@ -535,11 +535,11 @@ dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void*
  *   scale = max |x| / 127      q = x / scale to the nearest integer, ties to
  *                              the even one
  *
- * with the maximum over the row or the group. The scale is the fp32 product of
- * the maximum and 1 / 127 as fp32 has it; q is that of the exact quotient by
- * the scale so held. Zeros have scale 1; a scale is at least 2^-100. A NaN or an infinity
- * makes the scale NaN or infinite and q 0, so that every value of that row or
- * group stands for NaN.
+ * with the maximum over the row or the group. The scale is the quotient
+ * rounded once to fp32; q is that of the exact quotient by the scale so held.
+ * Zeros have scale 1; a scale is at least 2^-100. A NaN or an infinity makes
+ * the scale NaN or infinite and q 0, so that every value of that row or group
+ * stands for NaN.
  * ---------------------------------------------------------------------- */
 
 /* 8-bit integers, where an output's 8-bit type is chosen. */

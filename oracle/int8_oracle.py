@@ -51,8 +51,7 @@ def quantize_rows(x, group=0):
     n = -(-d // g)
     padded = np.concatenate([np.abs(x), np.zeros((T, n * g - d))], axis=1).reshape(T, n, g)
     top = padded.max(axis=2).astype(np.float32)
-    scale = np.where(top == 0, np.float32(1), np.maximum(top * (np.float32(1) / np.float32(INT8_MAX)),
-                                                          np.float32(2.0 ** -100)))
+    scale = np.where(top == 0, np.float32(1), np.maximum(top / np.float32(INT8_MAX), np.float32(2.0 ** -100)))
     q = np.rint(x / _columns(scale, d, group))
     return q, (scale if group else scale.reshape(T))
 
