@@ -66,6 +66,15 @@ __device__ __forceinline__ const float* reread(const float* p) {
   return p;
 }
 
+// The spread of a row whose squares about its mean add up to q. A NaN or an infinity
+// in the row, or a sum past fp32's range, leaves a q that is no finite number, and
+// both statistics are then NaN (1 / sqrt(inf) would be 0, and such a row its bias).
+__device__ __forceinline__ void finish_stats(float q, int64_t d, float eps, float& mean, float& rstd) {
+  const bool fine = q <= 3.402823466e38f;
+  rstd = fine ? 1.f / sqrtf(q / (float)d + eps) : __builtin_nanf("");
+  mean = fine ? mean : __builtin_nanf("");
+}
+
 // The row's statistics, from the C chunks that each of NT threads holds; past d
 // the values do not count. Each wave takes the mean of its own values and their
 // squares about it; the waves' (count, mean, squares) join as those of any
@@ -117,7 +126,7 @@ __device__ __forceinline__ void row_stats(const float (&f)[C][E], int lane, int6
     mean = row16_sum(n * m) / (float)d;
     q = row16_sum(fmaf(n * (m - mean), m - mean, w < W ? red[2 * w + 1] : 0.f));
   }
-  rstd = 1.f / sqrtf(q / (float)d + eps);
+  finish_stats(q, d, eps, mean, rstd);
 }
 
 // Largest |value| of the row, as its bits (see row_max_bits).
@@ -267,7 +276,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs a) 
           q = fmaf(v, v, q);
         }
       }
-      rs = 1.f / sqrtf(row_sum<NT>(q, red[par] + W) / (float)a.d + a.eps);
+      finish_stats(row_sum<NT>(q, red[par] + W), a.d, a.eps, mean, rs);
       if (threadIdx.x == 0 && a.mean) a.mean[t] = mean;
       if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rs;
     }

@@ -563,8 +563,9 @@ dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void*
  * from memory (rows of more than 16384 elements are read again).
  *
  * The statistics are of the unrounded fp32 sum, the variance of the values
- * about their mean. A NaN or an infinity in a row (or a sum past fp32's range)
- * makes its statistics, n and scale NaN. T == 0 does nothing; d == 0 has no norm and is refused when
+ * about their mean. A NaN or an infinity in a row (or a sum of its values or
+ * of their squares about the mean past fp32's range) makes its mean, rstd, n
+ * and scale NaN. T == 0 does nothing; d == 0 has no norm and is refused when
  * scale, mean or rstd is asked for. T and d are below 2^31, T * d at most 2^33.
  * Errors: as dora_rms_norm; an unknown q_dtype with q is
  * DORA_ERR_UNSUPPORTED_DTYPE.
