@@ -347,7 +347,16 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_long_kernel(NormBwdArgs a) 
   }
 }
 
-__global__ __launch_bounds__(kSumThreads) void column_sum_kernel(ColumnSum s) { column_sum(s, blockIdx.x); }
+// (A launch holds less than 2^32 threads, which 2 d columns pass from d = 2^27 on:
+// past kMostSums workgroups each takes several blocks of columns.)
+constexpr unsigned kMostSums = 1u << 21;
+
+__global__ __launch_bounds__(kSumThreads) void column_sum_kernel(ColumnSum s, unsigned groups) {
+  for (unsigned b = blockIdx.x; b < groups; b += gridDim.x) {   // (uniform)
+    column_sum(s, b);
+    __syncthreads();
+  }
+}
 
 template <typename T>
 hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
@@ -414,7 +423,9 @@ hipError_t launch_bwd(NormBwdArgs a, float* dweight, hipStream_t st) {
 hipError_t launch_column_sum(const float* part, int n_part, int64_t n, float* out0, int64_t n0, float* out1,
                              hipStream_t st) {
   const ColumnSum s{part, n_part, n, out0, n0, out1};
-  hipLaunchKernelGGL(column_sum_kernel, dim3(sum_groups(n)), dim3(kSumThreads), 0, st, s);
+  const unsigned groups = sum_groups(n);
+  hipLaunchKernelGGL(column_sum_kernel, dim3(groups < kMostSums ? groups : kMostSums), dim3(kSumThreads), 0, st, s,
+                     groups);
   return hipGetLastError();
 }
 
