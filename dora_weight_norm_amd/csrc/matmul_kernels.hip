@@ -254,7 +254,8 @@ void choose_tile(int64_t M, int64_t N, int64_t stages, int dtype, int few, int* 
 // same. They bring rows into shared memory in whole lines without a register,
 // which 32 rows of w in pieces of 16 bytes do not reach, and have more of w on
 // its way than blocks of 16 columns do, at shallow depths or where the walking
-// kernel ends; rows off the 16-byte grid would be copied first and stay.
+// kernel ends; rows whose length is off the 16-byte grid stay. (A w at an address
+// off it: int8_in_place.)
 // Measured, the few-rows or walking kernel against the tiles, us on the GPU:
 //   17 and 32 x 28672 x 8192   76.6, 44.3 and 87.3, 46.2
 //   17 and 32 x  8192 x 8192   21.9, 19.0 and 24.5, 19.3
@@ -299,6 +300,19 @@ bool int8_anywhere(int64_t M, int64_t N, int64_t K, int64_t r, int splits) {
   const int64_t tiles = up(M, 64) / 64 * (up(N, 64) / 64), stages = up(K, 128) / 128 + up(r, 64) / 64;
   return tiles * stages <= 20000 && (K % 16 != 0 || stages <= 20 * splits);
 }
+
+// Whether a product whose result is one row of 64-row tiles takes a w off the
+// 16-byte grid as it is: a copy writes and reads again what is read once here, in a
+// workspace as large as w. Measured, behind copies against as they are, us of the
+// whole call (w one byte off the grid, or rows of an odd length):
+//   17 and 32 x  28672 x 8192   127, 93 and 129, 93 (few-rows kernel 200, 244)
+//   17 and 32 x  28672 x 4096    60, 47 and  60, 48 (few-rows kernel 109, 132)
+//   14        x  28672 x 8320   132, 91             (few-rows kernel 191)
+//   33 and 64 x  28672 x 8189   132, 70 and 139, 81
+//   32 and 64 x  8192 x 28672   135, 86 and 142, 89
+//   64        x 100000 x 2000   144, 84
+//  128        x  28672 x 8192   153, 169 and x 2000 38, 35 (two rows of tiles)
+bool int8_in_place(int64_t M, int64_t K, int al) { return M <= 64 && K >= 16 && (K % 16 != 0 || !(al & 2)); }
 
 // Whether the walking kernel takes a product of 8-bit integers: whole steps of
 // 128 bytes, eight a wave at most, a pair of one step a wave in whole chunks, and
@@ -379,10 +393,16 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   choose_tile(M, N, up(K, KT) / KT, dtype, tiles ? 0 : (K % epc == 0 ? kFewOnGrid : kFewOffGrid), &p.cfg, &p.splits);
   const bool off_grid = K % 16 != 0 || (al & 3) != 3 || (r > 0 && (r % 8 != 0 || (al & 12) != 12));
   if (i8 && p.cfg == kTile64 && off_grid && int8_anywhere(M, N, K, r, p.splits)) p.cfg = kAny64;
+  size_t least = 0;
+  if (i8 && p.cfg < kFew8 && int8_in_place(M, K, al)) {
+    p.cfg = kAny64;
+    if (K % 16 == 0) least = plan_matmul(M, N, K, r, dtype, al | 2).ws_bytes;   // (a workspace for any address serves all)
+  }
   if (i8 && !tiles && int8_walks(M, N, K, r)) p.cfg = M <= 8 ? kWalk8 : kWalk16, p.splits = 1;
   auto operand = [&](int64_t rows, int64_t depth, int es, int bit, bool* pack, int64_t* ld, size_t* at) {
-    // (the few-rows kernel reads rows at any element address)
-    *pack = p.cfg < kFew8 && depth > 0 && (depth % (16 / es) != 0 || !(al & bit));
+    // (The few-rows kernel reads rows at any element address; the 64-row tile that
+    // does takes none shorter than 16 bytes, which a pair's may be.)
+    *pack = depth > 0 && (p.cfg < kFew8 ? depth % (16 / es) != 0 || !(al & bit) : p.cfg == kAny64 && depth < 16 / es);
     *ld = *pack ? up(depth, 16 / es) : depth;
     *at = off;
     if (*pack) off = up256(off + (size_t)(rows * *ld) * es);
@@ -394,7 +414,7 @@ MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K, int64_t r, int dtype, in
   operand(N, r, es2, 8, &p.pack_b, &p.ldb, &p.off_b);
   p.off_part = off;
   if (p.splits > 1) off = up256(off + (size_t)(p.splits * M * N) * 4);
-  p.ws_bytes = off;
+  p.ws_bytes = off > least ? off : least;
   return p;
 }
 
@@ -411,7 +431,8 @@ hipError_t launch_matmul(const MatmulPlan& p, const void* x, const void* w, int 
   if (e != hipSuccess) return e;
   GemmArgs g{};
   g.a = x, g.b = w, g.lda = p.ldx, g.ldb = p.ldw, g.K = K;
-  g.a2 = r > 0 ? t : nullptr, g.b2 = r > 0 ? b : nullptr, g.lda2 = p.ldt, g.ldb2 = p.ldb, g.K2 = r;
+  g.a2 = r > 0 ? t : nullptr, g.b2 = r > 0 ? b : nullptr, g.lda2 = p.ldt, g.ldb2 = p.ldb;
+  g.K2 = p.cfg == kAny64 && p.pack_t ? p.ldt : r;   // (with the zeros behind copies of such rows)
   g.s = s, g.M = M, g.N = N, g.splits = p.splits;
   g.part = reinterpret_cast<float*>(ws + p.off_part);
   g.ep = ep;

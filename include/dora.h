@@ -610,7 +610,13 @@ dora_status dora_quantize_rows(const void* x, int dtype, int64_t T, int64_t d, i
 dora_status dora_dequantize_rows(const int8_t* q, const float* scale, int64_t T, int64_t d, int64_t group, int dtype,
                                  void* x, void* stream);
 
-/* Workspace and plan of dora_matmul_int8, as those of dora_matmul (x and w are int8, t and b of 16 bits). Host only. */
+/*
+ * Workspace and plan of dora_matmul_int8, as those of dora_matmul (x and w are
+ * int8, t and b of 16 bits), but that small products, and products of up to 64
+ * rows as to w, read operands off the 16-byte grid as they are (K and r of
+ * less than 16 bytes apart). The workspace for operands at any address
+ * (aligned_operands 0) serves them at all. Host only.
+ */
 dora_status dora_matmul_int8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int aligned_operands,
                                             size_t* ws_bytes);
 dora_status dora_matmul_int8_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, int aligned_operands, int64_t* info,
