@@ -66,6 +66,7 @@ __all__ = [
     "dora_matmul_int8_plan_info",
     "dora_matmul_backward_int8",
     "dora_matmul_backward_int8_workspace_size",
+    "dora_matmul_backward_int8_plan_info",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdora.so")
@@ -157,6 +158,8 @@ def load():
                                     _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
         "dora_matmul_backward_int8_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, _c_i,
                                                             ctypes.POINTER(_c_sz)]),
+        "dora_matmul_backward_int8_plan_info": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, _c_i,
+                                                       ctypes.POINTER(_c_i64), _c_i]),
         "dora_matmul_backward_int8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64,
                                              _c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     }
@@ -835,15 +838,34 @@ def dora_matmul_int8_workspace_size(M: int, N: int, K: int, r: int, aligned_oper
     return _size_of("dora_matmul_int8_workspace_size", M, N, K, r, aligned_operands)
 
 
+INT8_KERNELS = ("tiles", "few_rows", "walk", "tiles_anywhere")
+HELD_READS = ("as_given", "copy", "int8_rows")
+
+
 def dora_matmul_int8_plan_info(M: int, N: int, K: int, r: int, aligned_operands: int = 15) -> dict:
-    buf = (_c_i64 * 5)()
-    _call("dora_matmul_int8_plan_info", M, N, K, r, aligned_operands, buf, 5)
-    return dict(zip(("tile_rows", "splits", "copies", "workspace_bytes", "few_rows"), list(buf)))
+    """`kernel`: one of INT8_KERNELS, or None where there is nothing to do."""
+    buf = (_c_i64 * 6)()
+    _call("dora_matmul_int8_plan_info", M, N, K, r, aligned_operands, buf, 6)
+    info = dict(zip(("tile_rows", "splits", "copies", "workspace_bytes", "few_rows"), list(buf)))
+    info["kernel"] = None if buf[5] < 0 else INT8_KERNELS[buf[5]]
+    return info
 
 
 def dora_matmul_backward_int8_workspace_size(M: int, N: int, K: int, dtype, outputs: int = 31, held: int = 3) -> int:
     """`outputs`: the sum of the GRAD_ constants that apply; `held`: of the HELD_ ones."""
     return _size_of("dora_matmul_backward_int8_workspace_size", M, N, K, _dtype_code(dtype), outputs, held)
+
+
+def dora_matmul_backward_int8_plan_info(M: int, N: int, K: int, dtype, outputs: int = 31, held: int = 3) -> dict:
+    """For dx and dw (None where there is none) the product's tile_rows, its splits, and how it `reads` w or x (one of
+    HELD_READS), and workspace_bytes. Arguments as the workspace query's."""
+    buf = (_c_i64 * 7)()
+    _call("dora_matmul_backward_int8_plan_info", M, N, K, _dtype_code(dtype), outputs, held, buf, 7)
+    info = {"workspace_bytes": buf[6]}
+    for name, at in (("dx", 0), ("dw", 3)):
+        info[name] = None if buf[at] < 0 else {"tile_rows": buf[at], "splits": buf[at + 1],
+                                               "reads": HELD_READS[buf[at + 2]]}
+    return info
 
 
 def _layer_norm(x, weight, bias, eps, residual, h, mean, rstd, want_stats, stream, y=None, q=None, scale=None,

@@ -69,7 +69,7 @@ dora_status dora_matmul_plan_info(int64_t M, int64_t N, int64_t K, int64_t r, in
   if (info == nullptr || n_info < 0 || !matmul_sizes_ok(M, N, K, r, operand_size(dtype))) return DORA_ERR_INVALID_ARG;
   const dora::MatmulPlan p = M > 0 && N > 0 ? dora::plan_matmul(M, N, K, r, dtype, aligned_operands)
                                             : dora::MatmulPlan{};
-  plan_fields(p, M > 0 && N > 0, info, n_info);
+  plan_fields(p, M > 0 && N > 0, false, info, n_info);
   return DORA_OK;
 }
 

@@ -70,14 +70,20 @@ inline bool backward_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t es) {
   return matmul_sizes_ok(M, N, K, 0, es) && M * es < kMaxRowBytes && N * es < kMaxRowBytes;
 }
 
+// Rows of a tile; 0 for the kernels of few rows.
+inline int plan_tile_rows(int cfg) {
+  return cfg == kTile256 ? 256 : (cfg == kTile128 ? 128 : (cfg == kTile64 || cfg == kAny64 ? 64 : 0));
+}
+
 // A product's plan as its query gives it.
-inline void plan_fields(const MatmulPlan& p, bool any, int64_t* info, int n_info) {
-  const int rows = p.cfg == kTile256 ? 256 : (p.cfg == kTile128 ? 128 : (p.cfg == kTile64 || p.cfg == kAny64 ? 64 : 0));
+inline void plan_fields(const MatmulPlan& p, bool any, bool int8, int64_t* info, int n_info) {
   const int copies = (p.pack_x ? 1 : 0) | (p.pack_w ? 2 : 0) | (p.pack_t ? 4 : 0) | (p.pack_b ? 8 : 0);
   const int few = p.cfg == kFew8 || p.cfg == kWalk8 ? 8
                   : (p.cfg == kFew16 || p.cfg == kWalk16 ? 16 : (p.cfg == kFew32 ? 32 : -1));
-  const int64_t vals[] = {any ? rows : -1, p.splits, copies, (int64_t)p.ws_bytes, few};
-  for (int i = 0; i < n_info; ++i) info[i] = i < 5 ? vals[i] : -1;
+  const int kernel = p.cfg < kFew8 ? 0 : (p.cfg == kAny64 ? 3 : (p.cfg == kWalk8 || p.cfg == kWalk16 ? 2 : 1));
+  const int64_t vals[] = {any ? plan_tile_rows(p.cfg) : -1, p.splits, copies, (int64_t)p.ws_bytes, few,
+                          any && int8 ? kernel : -1};
+  for (int i = 0; i < n_info; ++i) info[i] = i < 6 ? vals[i] : -1;
 }
 
 }  // namespace dora

@@ -131,7 +131,7 @@ dora_status dora_matmul_int8_plan_info(int64_t M, int64_t N, int64_t K, int64_t 
                                        int n_info) {
   if (info == nullptr || n_info < 0 || !int8_sizes_ok(M, N, K, r)) return DORA_ERR_INVALID_ARG;
   const bool any = M > 0 && N > 0;
-  plan_fields(any ? int8_plan(M, N, K, r, aligned_operands) : MatmulPlan{}, any, info, n_info);
+  plan_fields(any ? int8_plan(M, N, K, r, aligned_operands) : MatmulPlan{}, any, true, info, n_info);
   return DORA_OK;
 }
 
@@ -174,6 +174,23 @@ dora_status dora_matmul_backward_int8_workspace_size(int64_t M, int64_t N, int64
                                    outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU, outputs & DORA_GRAD_ALIGNED,
                                    held & DORA_HELD_X, held & DORA_HELD_W)
                   .ws_bytes;
+  return DORA_OK;
+}
+
+dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
+                                                int64_t* info, int n_info) {
+  size_t bytes;
+  const dora_status st = dora_matmul_backward_int8_workspace_size(M, N, K, dtype, outputs, held, &bytes);
+  if (st != DORA_OK) return st;
+  if (info == nullptr || n_info < 0) return DORA_ERR_INVALID_ARG;
+  const MatmulBackwardPlan p = plan_matmul_backward(
+      M, N, K, dtype, outputs & DORA_GRAD_DX, outputs & DORA_GRAD_DW, outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU,
+      outputs & DORA_GRAD_ALIGNED, held & DORA_HELD_X, held & DORA_HELD_W);
+  const bool dx = (outputs & DORA_GRAD_DX) && M > 0 && K > 0, dw = (outputs & DORA_GRAD_DW) && N > 0 && K > 0;
+  const int w = p.w8_tile ? 2 : (p.w8 || p.copy || !p.direct ? 1 : 0), x = p.x8_tile ? 2 : (p.x8 || p.copy || !p.direct ? 1 : 0);
+  const int64_t vals[] = {dx ? plan_tile_rows(p.cfg_dx) : -1, dx ? p.splits_dx : -1, dx ? w : -1,
+                          dw ? plan_tile_rows(p.cfg_dw) : -1, dw ? p.splits_dw : -1, dw ? x : -1, (int64_t)bytes};
+  for (int i = 0; i < n_info; ++i) info[i] = i < 7 ? vals[i] : -1;
   return DORA_OK;
 }
 

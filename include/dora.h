@@ -615,7 +615,10 @@ dora_status dora_dequantize_rows(const int8_t* q, const float* scale, int64_t T,
  * int8, t and b of 16 bits), but that small products, and products of up to 64
  * rows as to w, read operands off the 16-byte grid as they are (K and r of
  * less than 16 bytes apart). The workspace for operands at any address
- * (aligned_operands 0) serves them at all. Host only.
+ * (aligned_operands 0) serves them at all. The plan's sixth entry names the
+ * kernel: 0 tiles whose operands lie on the grid, 1 few rows, 2 few rows with
+ * the tokens in registers, which walks the columns, 3 tiles of 64 rows whose
+ * operands lie at any address (-1: nothing to do). Host only.
  */
 dora_status dora_matmul_int8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int aligned_operands,
                                             size_t* ws_bytes);
@@ -667,6 +670,18 @@ typedef struct dora_int8_rows {
  */
 dora_status dora_matmul_backward_int8_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
                                                      size_t* ws_bytes);
+
+/*
+ * The plan it would use, for diagnostics and tests: info[0 .. n_info-1] are, of
+ * dx and then of dw, the rows of the product's tile (0: the kernel for few rows
+ * and small products), the parts of its depth, and how it reads w (dx) or x
+ * (dw): 0 as it lies, 1 from a copy (of int8 rows in 16 bits, at whole chunks,
+ * transposed in fp32), 2 as the int8 rows that are held (-1 for a gradient that
+ * is not asked for or empty); then the workspace bytes; further entries are -1.
+ * Host only.
+ */
+dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
+                                                int64_t* info, int n_info);
 
 /*
  * dora_matmul_backward_rows with any of u, x and w held as int8 rows: u8, x8

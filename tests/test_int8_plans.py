@@ -1,5 +1,6 @@
 """Plans of the integer product for operands at any address (no GPU: queries alone)."""
 
+import ctypes
 import os
 
 import pytest
@@ -36,3 +37,42 @@ def test_a_workspace_for_few_rows_at_any_address_serves_them_at_all(M, N, K, r):
     assert max(sizes) == sizes[0] and max(sizes) < N * K // 2     # (no room for a copy of w)
     for al in range(16):                                           # s = 0 reads no pair
         assert bnd.dora_matmul_int8_workspace_size(M, N, K, 0, al) <= sizes[al]
+
+
+@pytest.mark.parametrize("kernel,shapes", [
+    ("walk", [(1, 12288, 2048, 0), (7, 12300, 8192, 512), (9, 8192, 8064, 0), (16, 16000, 256, 384), (12, 8192, 128, 64)]),
+    ("few_rows", [(1, 8192, 8192, 0), (16, 8192, 8320, 16), (16, 8192, 1024, 520), (32, 1024, 4096, 0), (100, 333, 640, 16)]),
+    ("tiles", [(16, 28672, 256, 384), (32, 28672, 8192, 0), (300, 333, 640, 16), (8192, 8192, 8192, 384)]),
+    ("tiles_anywhere", [(333, 1001, 777, 24), (40, 5000, 127, 63), (300, 333, 640, 13), (64, 28672, 8189, 0)]),
+    (None, [(0, 64, 64, 0), (64, 0, 64, 0)])])
+def test_kernels_of_shapes(kernel, shapes):
+    for a in shapes:
+        assert bnd.dora_matmul_int8_plan_info(*a)["kernel"] == kernel, a
+
+
+def test_the_plain_products_plan_names_no_kernel():
+    buf = (ctypes.c_int64 * 8)()
+    assert bnd.load().dora_matmul_plan_info(300, 333, 640, 16, 0, 15, buf, 8) == 0 and list(buf)[5:] == [-1] * 3
+    assert bnd.load().dora_matmul_int8_plan_info(300, 333, 640, 16, 15, buf, 8) == 0 and list(buf)[5:] == [0, -1, -1]
+
+
+def test_backward_plans():
+    plan = bnd.dora_matmul_backward_int8_plan_info
+    p = plan(8200, 384, 4112, "bf16")
+    assert p["dw"] == {"tile_rows": 128, "splits": 5, "reads": "int8_rows"} and p["dx"]["reads"] == "int8_rows"
+    assert plan(8192, 384, 8192, "f16")["dw"]["tile_rows"] == 256
+    assert plan(2100, 384, 4096, "bf16")["dw"] == {"tile_rows": 64, "splits": 1, "reads": "copy"}
+    for a in ((8192, 8192, 8192, "bf16"), (2100, 520, 2064, "bf16", 15), (64, 128, 256, "f32")):   # deep, off the grid, fp32
+        p = plan(*a)
+        assert p["dx"]["reads"] == p["dw"]["reads"] == "copy", a
+    p = plan(4096, 4096, 4096, "bf16", bnd.GRAD_DX + bnd.GRAD_DW + bnd.GRAD_ALIGNED, bnd.HELD_X)
+    assert p["dx"]["reads"] == "as_given" and p["dw"]["reads"] == "int8_rows"
+    p = plan(4096, 4096, 4096, "bf16", bnd.GRAD_DW, 0)
+    assert p["dx"] is None and p["dw"]["reads"] == "copy"
+    p = plan(0, 64, 64, "bf16")
+    assert p["dx"] is None and p["dw"] is not None
+    assert p["workspace_bytes"] == bnd.dora_matmul_backward_int8_workspace_size(0, 64, 64, "bf16")
+    f, buf = bnd.load().dora_matmul_backward_int8_plan_info, (ctypes.c_int64 * 9)()
+    assert f(64, 64, 64, 0, 31, 3, buf, 9) == 0 and list(buf)[7:] == [-1, -1]
+    assert f(64, 64, 64, 0, 31, 3, None, 7) == 1 and f(64, 64, 64, 0, 31, 3, buf, -1) == 1
+    assert f(64, 64, 64, 3, 31, 3, buf, 7) == 2 and f(64, 64, 64, 0, 32, 3, buf, 7) == 1 and f(-1, 1, 1, 0, 31, 3, buf, 7) == 1
