@@ -20,7 +20,9 @@ writes 8-bit rows.
 8-bit integers serve two ends, each by itself or both at once. `int8_base` holds
 a layer's frozen W as int8 rows: its product is then one of integers, with the
 input packed a scale a token, and the adapter beside it in 16 bits, in training
-and (`forward_int8`) in serving. And `forward(..., pack=128)` keeps the activations that the backward
+and (`forward_int8`) in serving (the row norm of such a base is that of its values in
+16 bits, and every training forward writes these for it, a layer at a time:
+`AdaptedLayer.magnitude`). And `forward(..., pack=128)` keeps the activations that the backward
 reads (the layers' inputs and their products before the magnitude) as int8 rows
 with a scale for each 128 columns, at half of their memory; the gradients are
 those of the values so kept.
@@ -51,13 +53,19 @@ class AdaptedLayer:
     eps: float = 1e-6
 
     def weight(self, stream=None):
-        """W in A's dtype: itself, or the values that its int8 rows stand for."""
+        """W in A's dtype: itself, or the values that its int8 rows stand for, rounded to it (a new tensor each time)."""
         if isinstance(self.W, bnd.Int8Rows):
             return bnd.dora_dequantize_rows(*self.W, dtype=self.A.dtype, stream=stream)
         return self.W
 
     def magnitude(self, stream=None):
-        """(wnorm, g) of the layer as it stands, float32 [d_out]."""
+        """(wnorm, g) of the layer as it stands, float32 [d_out].
+
+        On an 8-bit W the norm is of weight(): the call brings the whole W back to A's dtype first, in memory of its
+        own, and its values are rounded to 16 bits, which the integer product's are not. The two norms differ by less
+        than half a step of that type times the row norm of W: 2^-8 in bf16 and, of values from 2^-14 on, 2^-11 in
+        fp16 (with normally distributed W up to 1.2e-3 and 1.7e-4, for a row has 255 values at most, and equal ones
+        round alike). Training and serving take the same g."""
         return bnd.dora_factored_norm(self.weight(stream), self.A, self.B, self.s, m=self.m, eps=self.eps,
                                       stream=stream)
 
