@@ -24,8 +24,8 @@ and (`forward_int8`) in serving (the row norm of such a base is that of its valu
 16 bits, and every training forward writes these for it, a layer at a time:
 `AdaptedLayer.magnitude`). And `forward(..., pack=128)` keeps the activations that the backward
 reads (the layers' inputs and their products before the magnitude) as int8 rows
-with a scale for each 128 columns, at half of their memory; the gradients are
-those of the values so kept.
+with a scale for each 128 columns, at half of their memory (h and both t = x A^T
+stay as they are); the gradients are those of the values so kept.
 """
 
 from __future__ import annotations

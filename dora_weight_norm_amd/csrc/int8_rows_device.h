@@ -41,7 +41,9 @@ __device__ __forceinline__ Place place_of(const RowSteps& s, uint32_t item, uint
 
 // One or two operands of rows of d columns, the second's rows numbered after the
 // first's; rows of x lie ld >= d elements apart, and those from d on, up to a
-// whole chunk or ld, are written as zeros.
+// whole chunk or ld, are written as zeros. A value is the fp32 product of q and its
+// scale, rounded once to T (as the tile kernel rounds rows that it reads as they are
+// held: a product's operands have 16 bits).
 struct UnpackJob {
   const uint8_t* q;
   const float* scale;

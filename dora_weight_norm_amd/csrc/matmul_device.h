@@ -430,7 +430,11 @@ __device__ __forceinline__ u32x4 read_tr(const char* unit, int r0, int s, int la
 // bytes of a k at a time, loaded one period ahead, and converts and stores them
 // element by element between the period's matrix instructions: each element of
 // the stage once a workgroup, where a conversion behind the transposing reads
-// would do it in every wave.
+// would do it in every wave. A value q times its scale is rounded to 16 bits there,
+// half a step of 2^-8 (2^-11) of it: a scale of a group of columns differs from one
+// k to the next and from one column to another, so that no factor of a row, a column
+// or the result can take it (one a row could go into the other operand before that
+// is rounded, at the price of another copy of it).
 template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT, bool BT, bool B8 = false>
 __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, KT = 128 / ESZ;
