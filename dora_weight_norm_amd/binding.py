@@ -158,7 +158,9 @@ def load():
                                     _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
         "dora_matmul_backward_int8_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, _c_i,
                                                             ctypes.POINTER(_c_sz)]),
-        "dora_matmul_backward_int8_plan_info": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, _c_i,
+        "dora_matmul_backward_int8_scales_workspace_size": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, _c_i64, _c_i64,
+                                                                   ctypes.POINTER(_c_sz)]),
+        "dora_matmul_backward_int8_plan_info": (_c_i, [_c_i64, _c_i64, _c_i64, _c_i, _c_i, _c_i64, _c_i64,
                                                        ctypes.POINTER(_c_i64), _c_i]),
         "dora_matmul_backward_int8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64,
                                              _c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
@@ -856,11 +858,13 @@ def dora_matmul_backward_int8_workspace_size(M: int, N: int, K: int, dtype, outp
     return _size_of("dora_matmul_backward_int8_workspace_size", M, N, K, _dtype_code(dtype), outputs, held)
 
 
-def dora_matmul_backward_int8_plan_info(M: int, N: int, K: int, dtype, outputs: int = 31, held: int = 3) -> dict:
+def dora_matmul_backward_int8_plan_info(M: int, N: int, K: int, dtype, outputs: int = 31, x_scales: int = 1,
+                                        w_scales: int = 1) -> dict:
     """For dx and dw (None where there is none) the product's tile_rows, its splits, and how it `reads` w or x (one of
-    HELD_READS), and workspace_bytes. Arguments as the workspace query's."""
+    HELD_READS), and workspace_bytes. `outputs`: the sum of the GRAD_ constants that apply; `x_scales`, `w_scales`: how
+    many scales a row of x and w has, 0 where they are not Int8Rows."""
     buf = (_c_i64 * 7)()
-    _call("dora_matmul_backward_int8_plan_info", M, N, K, _dtype_code(dtype), outputs, held, buf, 7)
+    _call("dora_matmul_backward_int8_plan_info", M, N, K, _dtype_code(dtype), outputs, x_scales, w_scales, buf, 7)
     info = {"workspace_bytes": buf[6]}
     for name, at in (("dx", 0), ("dw", 3)):
         info[name] = None if buf[at] < 0 else {"tile_rows": buf[at], "splits": buf[at + 1],
@@ -1069,8 +1073,8 @@ def dora_matmul_backward_int8(dy, u, x, w, col_scale=None, bias=None, act: str =
     at = [p or 0 for p in (px, pw, x8 and x8.q, w8 and w8.q)]
     outputs = (GRAD_DX * need_dx + GRAD_DW * need_dw + GRAD_SUMS * (need_dbias or need_dcol_scale)
                + GRAD_DU * (du.data_ptr() % 16 == 0) + GRAD_ALIGNED * all(p % 16 == 0 for p in at))
-    held = HELD_X * (x8 is not None) + HELD_W * (w8 is not None)
-    need = _size_of("dora_matmul_backward_int8_workspace_size", M, N, K, code, outputs, held)
+    scales = [0 if v is None else (-(-K // v.group) or 1 if v.group else 1) for v in (x8, w8)]
+    need = _size_of("dora_matmul_backward_int8_scales_workspace_size", M, N, K, code, outputs, *scales)
     workspace = _space(workspace, need, stream, dev)
     ref = [None if v is None else ctypes.byref(v) for v in (u8, x8, w8)]
     _call_on(dev, "dora_matmul_backward_int8", dy.data_ptr(), pu, ref[0], px, ref[1], pw, ref[2], code, M, N, K, prow,

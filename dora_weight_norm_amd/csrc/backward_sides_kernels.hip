@@ -20,7 +20,7 @@ __global__ __launch_bounds__(kSumThreads) void rows_back_kernel(ColumnSum sum, u
                                                                 RowSteps s, int64_t ld) {
   if (blockIdx.x < sums) return column_sum(sum, blockIdx.x);
   const unsigned group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-  unpack_rows<T, STREAM>(a, b, s, ld, (blockIdx.x - sums) * 4 + group, (gridDim.x - sums) * 4, threadIdx.x & 255);
+  unpack_rows<T, STREAM, true>(a, b, s, ld, (blockIdx.x - sums) * 4 + group, (gridDim.x - sums) * 4, threadIdx.x & 255);
 }
 
 struct TurnJob {
@@ -78,7 +78,8 @@ __global__ __launch_bounds__(kSumThreads) void turn_kernel(ColumnSum sum, unsign
 template <typename T>
 void rows_back(const ColumnSum& sum, unsigned sums, const BackwardSides& b, int64_t M, int64_t N, int64_t K, int64_t ldk,
                hipStream_t st) {
-  const UnpackJob w = unpack_job(b.w8, b.w16 ? N : 0, K, b.w16), x = unpack_job(b.x8, b.x16 ? M : 0, K, b.x16);
+  const UnpackJob w = unpack_job(b.w8, b.w16 ? N : 0, K, b.w16, b.w_folded);
+  const UnpackJob x = unpack_job(b.x8, b.x16 ? M : 0, K, b.x16, b.x_folded);
   const int64_t rows = w.T + x.T;
   const RowSteps s = row_steps(rows, K, 0, Elem<T>::epc, 1);
   const dim3 grid(sums + (row_groups(s) + 3) / 4), block(kSumThreads);

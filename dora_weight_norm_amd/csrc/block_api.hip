@@ -109,7 +109,7 @@ dora_status dora_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K,
     return DORA_ERR_INVALID_ARG;
   *ws_bytes = dora::plan_matmul_backward(M, N, K, dtype, outputs & DORA_GRAD_DX, outputs & DORA_GRAD_DW,
                                          outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU, outputs & DORA_GRAD_ALIGNED,
-                                         false, false)
+                                         kNotHeld, kNotHeld)
                   .ws_bytes;
   return DORA_OK;
 }
@@ -143,7 +143,7 @@ dora_status dora_matmul_backward_rows(const void* dy, const void* u, const void*
   const dora::MatmulBackwardPlan p =
       dora::plan_matmul_backward(M, N, K, dtype, dx != nullptr, dw != nullptr, dbias != nullptr || dcol_scale != nullptr,
                                  du != nullptr && aligned(du, 16),
-                                 (dw == nullptr || aligned(x, 16)) && (dx == nullptr || aligned(w, 16)), false, false);
+                                 (dw == nullptr || aligned(x, 16)) && (dx == nullptr || aligned(w, 16)), kNotHeld, kNotHeld);
   const dora_status st = workspace_ok(workspace, workspace_bytes, p.ws_bytes, in, 7, out, 5);
   if (st != DORA_OK) return st;
   return hip_status(dora::launch_matmul_backward(p, dy, u, x, w, dtype, M, N, K, row_scale, col_scale, bias, act, du,

@@ -48,6 +48,7 @@ struct GemmArgs {
   const float* b_scale;
   int64_t b_groups;
   int b_shift;
+  bool b_folded;           // only the scales' powers of two (fold_exp): `a` holds the rest
   Epilogue ep;
 };
 
@@ -87,14 +88,19 @@ struct MatmulBackwardPlan {
   bool copy;                                    // x and w from copies with a row stride of ldk
   bool x8, w8;                                  // x, w are int8 rows,
   bool x8_tile, w8_tile;                        // read as such by the tile kernel, or brought back into such copies
+  bool fold_x, fold_w;                          // their scales, one a row, are in operands of dw and of dx of their own
+  bool plain;                                   // du itself is an operand
   int64_t rows;                                 // row blocks of the element-wise pass
   int64_t ldn, ldm, ldk;                        // padded N, M and K
   int cfg_dx, cfg_dw, splits_dx, splits_dw;
-  size_t off_du, off_dut, off_wt, off_xt, off_sum, off_part;
+  size_t off_du, off_dun, off_dum, off_dut, off_wt, off_xt, off_sum, off_part;
   size_t ws_bytes;
 };
+// How an operand is held: in the storage type, or as int8 rows with several scales a
+// row or one.
+enum HeldForm : int { kNotHeld = 0, kHeldGroups = 1, kHeldRows = 2 };
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
-                                        bool need_sums, bool du_direct, bool aligned_xw, bool x8, bool w8);
+                                        bool need_sums, bool du_direct, bool aligned_xw, HeldForm x8, HeldForm w8);
 
 // Operands of the backward that are held as int8 rows (q null: they are not).
 struct HeldInt8 {
@@ -120,6 +126,7 @@ struct BackwardSides {
   Int8Rows w8, x8;
   void* w16;
   void* x16;
+  bool w_folded, x_folded;   // by their scales' powers of two alone
   Turned turned[3];
   int n_turned;
   void turn(const void* src, const Int8Rows& r, int64_t rows, int64_t cols, int64_t lsrc, int64_t ld, void* dst) {

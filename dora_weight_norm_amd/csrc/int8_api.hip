@@ -31,6 +31,12 @@ bool held_ok(const void* v, const dora_int8_rows* r, bool read, bool empty) {
   return v == nullptr && group_ok(r->group) && (empty || (r->q != nullptr && r->scale != nullptr));
 }
 
+// An operand's form, by how many scales a row of it has (0: it is not held so).
+HeldForm form_of(int64_t scales) { return scales == 0 ? kNotHeld : (scales > 1 ? kHeldGroups : kHeldRows); }
+HeldForm form_of(const dora_int8_rows* r, int64_t columns) {
+  return r == nullptr ? kNotHeld : (scales_of(columns, r->group) > 1 ? kHeldGroups : kHeldRows);
+}
+
 Int8Rows rows_of(const dora_int8_rows* r, bool read) {
   return r != nullptr && read ? Int8Rows{reinterpret_cast<const uint8_t*>(r->q), r->scale, r->group} : Int8Rows{};
 }
@@ -166,30 +172,33 @@ dora_status dora_matmul_int8(const int8_t* x, const float* row_scale, const int8
 
 dora_status dora_matmul_backward_int8_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
                                                      size_t* ws_bytes) {
-  if (!valid_dtype(dtype)) return DORA_ERR_UNSUPPORTED_DTYPE;
-  if (ws_bytes == nullptr || outputs < 0 || outputs >= 2 * DORA_GRAD_ALIGNED || held < 0 ||
-      held >= 2 * DORA_HELD_W || !backward_sizes_ok(M, N, K, esize(dtype)))
-    return DORA_ERR_INVALID_ARG;
-  *ws_bytes = plan_matmul_backward(M, N, K, dtype, outputs & DORA_GRAD_DX, outputs & DORA_GRAD_DW,
-                                   outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU, outputs & DORA_GRAD_ALIGNED,
-                                   held & DORA_HELD_X, held & DORA_HELD_W)
-                  .ws_bytes;
-  return DORA_OK;
+  if (held < 0 || held >= 2 * DORA_HELD_W) return DORA_ERR_INVALID_ARG;
+  return dora_matmul_backward_int8_scales_workspace_size(M, N, K, dtype, outputs, held & DORA_HELD_X ? 1 : 0,
+                                                         held & DORA_HELD_W ? 1 : 0, ws_bytes);
 }
 
-dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
-                                                int64_t* info, int n_info) {
-  size_t bytes;
-  const dora_status st = dora_matmul_backward_int8_workspace_size(M, N, K, dtype, outputs, held, &bytes);
-  if (st != DORA_OK) return st;
-  if (info == nullptr || n_info < 0) return DORA_ERR_INVALID_ARG;
+dora_status dora_matmul_backward_int8_scales_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs,
+                                                            int64_t x_scales, int64_t w_scales, size_t* ws_bytes) {
+  if (ws_bytes == nullptr) return DORA_ERR_INVALID_ARG;
+  int64_t info[7];
+  const dora_status st = dora_matmul_backward_int8_plan_info(M, N, K, dtype, outputs, x_scales, w_scales, info, 7);
+  if (st == DORA_OK) *ws_bytes = (size_t)info[6];
+  return st;
+}
+
+dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K, int dtype, int outputs,
+                                                int64_t x_scales, int64_t w_scales, int64_t* info, int n_info) {
+  if (!valid_dtype(dtype)) return DORA_ERR_UNSUPPORTED_DTYPE;
+  if (info == nullptr || n_info < 0 || outputs < 0 || outputs >= 2 * DORA_GRAD_ALIGNED || x_scales < 0 ||
+      w_scales < 0 || !backward_sizes_ok(M, N, K, esize(dtype)))
+    return DORA_ERR_INVALID_ARG;
   const MatmulBackwardPlan p = plan_matmul_backward(
       M, N, K, dtype, outputs & DORA_GRAD_DX, outputs & DORA_GRAD_DW, outputs & DORA_GRAD_SUMS, outputs & DORA_GRAD_DU,
-      outputs & DORA_GRAD_ALIGNED, held & DORA_HELD_X, held & DORA_HELD_W);
+      outputs & DORA_GRAD_ALIGNED, form_of(x_scales), form_of(w_scales));
   const bool dx = (outputs & DORA_GRAD_DX) && M > 0 && K > 0, dw = (outputs & DORA_GRAD_DW) && N > 0 && K > 0;
   const int w = p.w8_tile ? 2 : (p.w8 || p.copy || !p.direct ? 1 : 0), x = p.x8_tile ? 2 : (p.x8 || p.copy || !p.direct ? 1 : 0);
   const int64_t vals[] = {dx ? plan_tile_rows(p.cfg_dx) : -1, dx ? p.splits_dx : -1, dx ? w : -1,
-                          dw ? plan_tile_rows(p.cfg_dw) : -1, dw ? p.splits_dw : -1, dw ? x : -1, (int64_t)bytes};
+                          dw ? plan_tile_rows(p.cfg_dw) : -1, dw ? p.splits_dw : -1, dw ? x : -1, (int64_t)p.ws_bytes};
   for (int i = 0; i < n_info; ++i) info[i] = i < 7 ? vals[i] : -1;
   return DORA_OK;
 }
@@ -223,7 +232,7 @@ dora_status dora_matmul_backward_int8(const void* dy, const void* u, const dora_
                   (dx == nullptr || (aligned(w, 16) && aligned(held.w.q, 16)));
   const MatmulBackwardPlan p =
       plan_matmul_backward(M, N, K, dtype, dx != nullptr, dw != nullptr, dbias != nullptr || dcol_scale != nullptr,
-                           du != nullptr && aligned(du, 16), al, x8 != nullptr, w8 != nullptr);
+                           du != nullptr && aligned(du, 16), al, form_of(x8, K), form_of(w8, K));
   const dora_status st = workspace_ok(workspace, workspace_bytes, p.ws_bytes, in, 13, out, 5);
   if (st != DORA_OK) return st;
   return hip_status(launch_matmul_backward(p, dy, u, x, w, dtype, M, N, K, row_scale, col_scale, bias, act, du, dx, dw,

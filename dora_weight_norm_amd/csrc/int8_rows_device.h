@@ -4,6 +4,7 @@
 
 #include "dora_launch.h"
 #include "dora_rows.h"
+#include "scale_parts.h"
 
 namespace dora {
 
@@ -43,17 +44,19 @@ __device__ __forceinline__ Place place_of(const RowSteps& s, uint32_t item, uint
 // first's; rows of x lie ld >= d elements apart, and those from d on, up to a
 // whole chunk or ld, are written as zeros. A value is the fp32 product of q and its
 // scale, rounded once to T (as the tile kernel rounds rows that it reads as they are
-// held: a product's operands have 16 bits).
+// held: a product's operands have 16 bits), or with its power of two alone where FOLD
+// and the job say so, which is exact.
 struct UnpackJob {
   const uint8_t* q;
   const float* scale;
   int64_t groups, T;
   int shift;
   void* x;
+  bool folded;
 };
 
 // Thread t of the 256 that are number `group` of `groups`.
-template <typename T, bool STREAM>
+template <typename T, bool STREAM, bool FOLD>
 __device__ __forceinline__ void unpack_rows(const UnpackJob& a, const UnpackJob& b, const RowSteps& s, int64_t ld,
                                             uint32_t group, uint32_t groups, uint32_t t) {
   constexpr int E = Elem<T>::epc;
@@ -76,6 +79,7 @@ __device__ __forceinline__ void unpack_rows(const UnpackJob& a, const UnpackJob&
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       if (!p[i].ok) continue;
+      if (FOLD && (p[i].row < a.T ? a.folded : b.folded)) sc[i] = fold_power<T>(sc[i]);
       float f[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) f[e] = (float)(int8_t)(w[i][e / 4] >> (8 * (e % 4))) * sc[i];
@@ -104,8 +108,8 @@ __device__ __forceinline__ void unpack_rows(const UnpackJob& a, const UnpackJob&
   return (unsigned)(groups < kMostGroups ? groups : kMostGroups);
 }
 
-[[maybe_unused]] UnpackJob unpack_job(const Int8Rows& r, int64_t T, int64_t d, void* x) {
-  return UnpackJob{r.q, r.scale, scales_of(d, r.group), T, group_shift(r.group), x};
+[[maybe_unused]] UnpackJob unpack_job(const Int8Rows& r, int64_t T, int64_t d, void* x, bool folded) {
+  return UnpackJob{r.q, r.scale, scales_of(d, r.group), T, group_shift(r.group), x, folded};
 }
 
 }  // namespace

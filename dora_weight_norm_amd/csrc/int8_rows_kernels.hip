@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void quantize_groups_kernel(const T* x, RowSte
 
 template <typename T, bool STREAM>
 __global__ __launch_bounds__(256) void dequantize_rows_kernel(UnpackJob a, RowSteps s) {
-  unpack_rows<T, STREAM>(a, UnpackJob{}, s, s.d, blockIdx.x, gridDim.x, threadIdx.x);
+  unpack_rows<T, STREAM, false>(a, UnpackJob{}, s, s.d, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
 template <typename T>
@@ -116,7 +116,7 @@ hipError_t launch_quantize_rows(const void* x, int dtype, int64_t T, int64_t d, 
 }
 
 hipError_t launch_dequantize_rows(const Int8Rows& r, int64_t T, int64_t d, int dtype, void* x, hipStream_t st) {
-  const UnpackJob a = unpack_job(r, T, d, x);
+  const UnpackJob a = unpack_job(r, T, d, x, false);
   switch (dtype) {
     case 0: return dequantize<bf16_t>(a, d, st);
     case 2: return dequantize<f16_t>(a, d, st);

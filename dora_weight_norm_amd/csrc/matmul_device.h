@@ -4,6 +4,7 @@
 #include "dora_device.h"
 #include "dora_launch.h"
 #include "dora_matmul.h"
+#include "scale_parts.h"
 
 namespace dora {
 
@@ -433,8 +434,8 @@ __device__ __forceinline__ u32x4 read_tr(const char* unit, int r0, int s, int la
 // would do it in every wave. A value q times its scale is rounded to 16 bits there,
 // half a step of 2^-8 (2^-11) of it: a scale of a group of columns differs from one
 // k to the next and from one column to another, so that no factor of a row, a column
-// or the result can take it (one a row could go into the other operand before that
-// is rounded, at the price of another copy of it).
+// or the result can take it. Of one scale a row the other operand holds the
+// significand (b_folded), and the integer times a power of two is exact.
 template <typename T, typename O, int WM, int WN, int MB, int NB, int P, bool PAIR, bool AT, bool BT, bool B8 = false>
 __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g) {
   constexpr int ESZ = Op<T>::esz, FC = Op<T>::fc, KT = 128 / ESZ;
@@ -556,6 +557,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
       // (bytes that a later step takes are not to be picked out, and so waited for,
       // when they were only just asked for)
       if (b % 8 == 0) asm volatile("" : "+v"(qv[j]), "+v"(qs[j]));
+      if (b == 0 && g.b_folded) qs[j] = fold_power<T>(qs[j]);
       const float f = (float)(int8_t)(qv[j][b / 4] >> (8 * (b % 4))) * qs[j];
       if (b % 2)
         qout[b % 8 / 2] = pack2<T>(qf, f);

@@ -33,21 +33,35 @@ struct SavedU {
   int shift;
 };
 
-template <typename T, bool U8>
+// FOLD: beside du, or in its place, the operands of products whose other one is int8
+// rows with one scale a row: du times the scales' significands (fold_exp), of w's rows
+// for dx (du_n) and of x's for dw (du_m), rounded once, from which the rows' integers
+// then take no rounding of their own. Either may be null, and du too.
+template <typename T>
+struct Folded {
+  const float* n_scale;
+  T* du_n;
+  const float* m_scale;
+  T* du_m;
+};
+
+template <typename T, bool U8, bool FOLD>
 __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u, SavedU u8, const float* row_scale,
                                                          const float* col_scale, const float* bias, int act, int64_t M,
-                                                         int64_t N, T* du, int64_t ldu, T* du2, float* sums) {
+                                                         int64_t N, T* du, int64_t ldu, T* du2, Folded<T> fold,
+                                                         float* sums) {
   __shared__ float lanes[16][256];
   const int64_t strip = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t n = strip * 8;
   const int ly = threadIdx.y, nl = blockDim.y;
   const int nv = (int)(N - n < 8 ? (N - n < 0 ? 0 : N - n) : 8);
-  float cs[8], bs[8], sb[8], sc[8];
+  float cs[8], bs[8], sb[8], sc[8], fn[FOLD ? 8 : 1];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     cs[e] = (col_scale && e < nv) ? col_scale[n + e] : 1.f;
     bs[e] = (bias && e < nv) ? bias[n + e] : 0.f;
     sb[e] = sc[e] = 0.f;
+    if constexpr (FOLD) fn[e] = fold.du_n && e < nv ? fold_factor<T>(fold.n_scale[n + e]) : 0.f;
   }
   // Four rows' loads are in flight at a time, and as int8 rows, which are fewer
   // bytes of u, the next four's too.
@@ -101,13 +115,33 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
       }
       if (du2) store8<T>(du2 + m * N + n, nv, o);
       // (a padded row's tail, up to the next strip of eight, is written as zeros)
-      if (nv < 8 && ldu > N) {
+      auto put = [&](T* to, float (&v)[8]) __attribute__((always_inline)) {
+        if (nv < 8 && ldu > N) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e >= nv) o[e] = 0.f;
-        store8<T>(du + m * ldu + n, (int)(ldu - n < 8 ? ldu - n : 8), o);
+          for (int e = 0; e < 8; ++e)
+            if (e >= nv) v[e] = 0.f;
+          store8<T>(to + m * ldu + n, (int)(ldu - n < 8 ? ldu - n : 8), v);
+        } else {
+          store8<T>(to + m * ldu + n, nv, v);
+        }
+      };
+      if constexpr (FOLD) {
+        if (fold.du_n) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = o[e] * fn[e];
+          put(fold.du_n, f);
+        }
+        if (fold.du_m) {
+          const float fm = fold_factor<T>(fold.m_scale[m]);
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = o[e] * fm;
+          put(fold.du_m, f);
+        }
+        if (du) put(du, o);
       } else {
-        store8<T>(du + m * ldu + n, nv, o);
+        put(du, o);
       }
     }
   };
@@ -464,9 +498,13 @@ static bool reads_rows8(int64_t rows, int64_t depth, int64_t K) {
 }
 
 MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dtype, bool need_dx, bool need_dw,
-                                        bool need_sums, bool du_direct, bool aligned_xw, bool x8, bool w8) {
+                                        bool need_sums, bool du_direct, bool aligned_xw, HeldForm x8, HeldForm w8) {
   MatmulBackwardPlan p{};
-  p.x8 = x8 && need_dw, p.w8 = w8 && need_dx;
+  p.x8 = x8 != kNotHeld && need_dw, p.w8 = w8 != kNotHeld && need_dx;
+  p.fold_x = x8 == kHeldRows && need_dw && dtype != 1 && K > 0;
+  p.fold_w = w8 == kHeldRows && need_dx && dtype != 1 && K > 0;
+  // (where both products have operands of their own, du is the caller's alone)
+  p.plain = !(p.fold_x || p.fold_w) || (need_dx && !p.fold_w) || (need_dw && !p.fold_x);
   const int esz = elem_size(dtype), epc = 16 / esz, KT = stage_depth(dtype);
   p.ldn = up(N, epc), p.ldm = up(M, epc);
   const int64_t strips = (N + 7) / 8, bx = (strips + 255) / 256;
@@ -480,7 +518,9 @@ MatmulBackwardPlan plan_matmul_backward(int64_t M, int64_t N, int64_t K, int dty
     return at;
   };
   p.du_direct = du_direct && N % epc == 0;
-  p.off_du = take(p.du_direct ? 0 : (size_t)(M * p.ldn) * esz);
+  p.off_du = take(p.du_direct || !p.plain ? 0 : (size_t)(M * p.ldn) * esz);
+  p.off_dun = take(p.fold_w ? (size_t)(M * p.ldn) * esz : 0);
+  p.off_dum = take(p.fold_x ? (size_t)(M * p.ldn) * esz : 0);
   p.off_sum = take(need_sums ? (size_t)(p.rows * 2 * N) * 4 : 0);
   // 16-bit products read du, w and x as they lie, copied to whole chunks where
   // their rows are none; fp32 ones (whose elements no transposing read takes)
@@ -521,8 +561,8 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   // The element-wise pass writes du into the caller's array where that can be
   // the products' operand, else at a padded row stride into the workspace
   // (and into the caller's array beside it).
-  char* d = p.du_direct ? static_cast<char*>(du) : ws + p.off_du;
-  void* du2 = p.du_direct ? nullptr : du;
+  char* d = !p.plain ? nullptr : (p.du_direct ? static_cast<char*>(du) : ws + p.off_du);
+  void* du2 = p.plain && p.du_direct ? nullptr : du;
   // (without rows the workspace may be null: whether sums are wanted is not read off their address)
   const bool want_sums = dbias || dcol;
   float* sums = want_sums ? reinterpret_cast<float*>(ws + p.off_sum) : nullptr;
@@ -533,22 +573,32 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     const dim3 block((unsigned)tx, (unsigned)(256 / tx));
     const dim3 grid((unsigned)((strips + tx - 1) / tx), (unsigned)p.rows);
     const SavedU u8{held.u.q, held.u.scale, scales_of(N, held.u.group), group_shift(held.u.group)};
-#define DORA_BWD_U(T, U8)                                                                                           \
-  hipLaunchKernelGGL((matmul_bwd_kernel<T, U8>), grid, block, 0, st, static_cast<const T*>(dy),                     \
-                     static_cast<const T*>(u), u8, row_scale, col_scale, bias, act, M, N, reinterpret_cast<T*>(d),  \
-                     p.ldn, static_cast<T*>(du2), sums)
-#define DORA_BWD(T)          \
-  if (u8.q != nullptr)       \
-    DORA_BWD_U(T, true);     \
-  else                       \
-    DORA_BWD_U(T, false)
+#define DORA_BWD_F(T, U8, FOLD)                                                                                      \
+  hipLaunchKernelGGL((matmul_bwd_kernel<T, U8, FOLD>), grid, block, 0, st, static_cast<const T*>(dy),                \
+                     static_cast<const T*>(u), u8, row_scale, col_scale, bias, act, M, N, reinterpret_cast<T*>(d),   \
+                     p.ldn, static_cast<T*>(du2),                                                                    \
+                     (Folded<T>{held.w.scale, p.fold_w ? reinterpret_cast<T*>(ws + p.off_dun) : nullptr,             \
+                                held.x.scale, p.fold_x ? reinterpret_cast<T*>(ws + p.off_dum) : nullptr}),           \
+                     sums)
+#define DORA_BWD_U(T, FOLD)          \
+  if (u8.q != nullptr)               \
+    DORA_BWD_F(T, true, FOLD);       \
+  else                               \
+    DORA_BWD_F(T, false, FOLD)
+#define DORA_BWD(T)                  \
+  if (p.fold_w || p.fold_x) {        \
+    DORA_BWD_U(T, true);             \
+  } else {                           \
+    DORA_BWD_U(T, false);            \
+  }
     switch (dtype) {
-      case 0: DORA_BWD(bf16_t); break;
-      case 2: DORA_BWD(f16_t); break;
-      default: DORA_BWD(float); break;
+      case 0: DORA_BWD(bf16_t) break;
+      case 2: DORA_BWD(f16_t) break;
+      default: DORA_BWD_U(float, false); break;
     }
 #undef DORA_BWD
 #undef DORA_BWD_U
+#undef DORA_BWD_F
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -558,8 +608,8 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   side.want_sums = want_sums && N > 0;
   side.part = sums, side.n_part = M > 0 ? (int)p.rows : 0, side.dbias = dbias, side.dcol = dcol;
   const bool w_back = p.direct && p.w8 && !p.w8_tile, x_back = p.direct && p.x8 && !p.x8_tile;
-  if (w_back) side.w8 = held.w, w = side.w16 = ws + p.off_wt;
-  if (x_back) side.x8 = held.x, x = side.x16 = ws + p.off_xt;
+  if (w_back) side.w8 = held.w, w = side.w16 = ws + p.off_wt, side.w_folded = p.fold_w;
+  if (x_back) side.x8 = held.x, x = side.x16 = ws + p.off_xt, side.x_folded = p.fold_x;
   if (!p.direct && M > 0 && K > 0 && N > 0) {
     if (dx) side.turn(w, held.w, N, K, K, p.ldn, ws + p.off_wt);
     if (dw) side.turn(d, Int8Rows{}, M, N, p.ldn, p.ldm, ws + p.off_dut);
@@ -579,25 +629,28 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     }
     const int64_t ldu = p.du_direct ? N : p.ldn;
     const int64_t ldw = p.copy || p.w8 ? p.ldk : K, ldx = p.copy || p.x8 ? p.ldk : K;
-    auto rows8 = [&](const Int8Rows& r, bool across, int cfg) {
+    auto rows8 = [&](const Int8Rows& r, bool folded, bool across, int cfg) {
       g.b = r.q, g.ldb = K, g.b_scale = r.scale, g.b_groups = scales_of(K, r.group), g.b_shift = group_shift(r.group);
+      g.b_folded = folded;
       return gemm_rows8(g, dtype, across, cfg, st);
     };
     // dx: du along the depth, w across it; dw: both across it.
     if (dx && M > 0 && K > 0) {
-      g.a = d, g.b = w, g.lda = ldu, g.ldb = ldw, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
+      g.a = p.fold_w ? ws + p.off_dun : d, g.lda = p.fold_w ? p.ldn : ldu;
+      g.b = w, g.ldb = ldw, g.K = N, g.M = M, g.N = K, g.splits = p.splits_dx;
       g.ep.y = dx;
       if (p.w8_tile)
-        e = rows8(held.w, false, p.cfg_dx);
+        e = rows8(held.w, p.fold_w, false, p.cfg_dx);
       else
         e = dtype == 0 ? launch_gemm_tr<bf16_t, false>(g, p.cfg_dx, st) : launch_gemm_tr<f16_t, false>(g, p.cfg_dx, st);
       if (e != hipSuccess) return e;
     }
     if (dw && N > 0 && K > 0) {
-      g.a = d, g.b = x, g.lda = ldu, g.ldb = ldx, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
+      g.a = p.fold_x ? ws + p.off_dum : d, g.lda = p.fold_x ? p.ldn : ldu;
+      g.b = x, g.ldb = ldx, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
       g.ep.y = dw;
       if (p.x8_tile)
-        e = rows8(held.x, true, p.cfg_dw);
+        e = rows8(held.x, p.fold_x, true, p.cfg_dw);
       else
         e = dtype == 0 ? launch_gemm_tr<bf16_t, true>(g, p.cfg_dw, st) : launch_gemm_tr<f16_t, true>(g, p.cfg_dw, st);
     }

@@ -666,10 +666,14 @@ typedef struct dora_int8_rows {
 /*
  * Device workspace dora_matmul_backward_int8 needs: `outputs` as for
  * dora_matmul_backward (DORA_GRAD_ALIGNED speaks of x, or x8's q, and of w, or
- * w8's q), `held` the DORA_HELD_ bits. Host only.
+ * w8's q), `held` the DORA_HELD_ bits. Rows of several scales may need less
+ * than this: the second query, with how many scales a row of x8 and of w8 has
+ * (0: x or w is not held so), says how much. Host only.
  */
 dora_status dora_matmul_backward_int8_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
                                                      size_t* ws_bytes);
+dora_status dora_matmul_backward_int8_scales_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int outputs,
+                                                            int64_t x_scales, int64_t w_scales, size_t* ws_bytes);
 
 /*
  * The plan it would use, for diagnostics and tests: info[0 .. n_info-1] are, of
@@ -680,8 +684,8 @@ dora_status dora_matmul_backward_int8_workspace_size(int64_t M, int64_t N, int64
  * is not asked for or empty); then the workspace bytes; further entries are -1.
  * Host only.
  */
-dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K, int dtype, int outputs, int held,
-                                                int64_t* info, int n_info);
+dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K, int dtype, int outputs,
+                                                int64_t x_scales, int64_t w_scales, int64_t* info, int n_info);
 
 /*
  * dora_matmul_backward_rows with any of u, x and w held as int8 rows: u8, x8
@@ -693,8 +697,11 @@ dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K,
  *   z = col_scale[n] * u + bias[n]   with u = u8.q * its scale in fp32
  *   dx = du (w8.q * its scale)       dw = du^T (x8.q * its scale)
  *
- * The products' operands are of the storage type, so x8 and w8 are rounded to
- * it, as du is. Everything else, the workspace and the errors are as there.
+ * The products' operands are of the storage type, so the values of x8 and w8
+ * are rounded to it, as du is. Those of rows with one scale are not: in 16 bits
+ * such a product's other operand is du times the scale's significand, rounded
+ * once, and the integers times the scale's power of two are exact. Everything
+ * else, the workspace and the errors are as there.
  */
 dora_status dora_matmul_backward_int8(const void* dy, const void* u, const dora_int8_rows* u8, const void* x,
                                       const dora_int8_rows* x8, const void* w, const dora_int8_rows* w8, int dtype,

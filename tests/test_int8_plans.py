@@ -65,14 +65,38 @@ def test_backward_plans():
     for a in ((8192, 8192, 8192, "bf16"), (2100, 520, 2064, "bf16", 15), (64, 128, 256, "f32")):   # deep, off the grid, fp32
         p = plan(*a)
         assert p["dx"]["reads"] == p["dw"]["reads"] == "copy", a
-    p = plan(4096, 4096, 4096, "bf16", bnd.GRAD_DX + bnd.GRAD_DW + bnd.GRAD_ALIGNED, bnd.HELD_X)
+    p = plan(4096, 4096, 4096, "bf16", bnd.GRAD_DX + bnd.GRAD_DW + bnd.GRAD_ALIGNED, 32, 0)
     assert p["dx"]["reads"] == "as_given" and p["dw"]["reads"] == "int8_rows"
-    p = plan(4096, 4096, 4096, "bf16", bnd.GRAD_DW, 0)
+    p = plan(4096, 4096, 4096, "bf16", bnd.GRAD_DW, 0, 0)
     assert p["dx"] is None and p["dw"]["reads"] == "copy"
     p = plan(0, 64, 64, "bf16")
     assert p["dx"] is None and p["dw"] is not None
     assert p["workspace_bytes"] == bnd.dora_matmul_backward_int8_workspace_size(0, 64, 64, "bf16")
     f, buf = bnd.load().dora_matmul_backward_int8_plan_info, (ctypes.c_int64 * 9)()
-    assert f(64, 64, 64, 0, 31, 3, buf, 9) == 0 and list(buf)[7:] == [-1, -1]
-    assert f(64, 64, 64, 0, 31, 3, None, 7) == 1 and f(64, 64, 64, 0, 31, 3, buf, -1) == 1
-    assert f(64, 64, 64, 3, 31, 3, buf, 7) == 2 and f(64, 64, 64, 0, 32, 3, buf, 7) == 1 and f(-1, 1, 1, 0, 31, 3, buf, 7) == 1
+    assert f(64, 64, 64, 0, 31, 1, 1, buf, 9) == 0 and list(buf)[7:] == [-1, -1]
+    assert f(64, 64, 64, 0, 31, 1, 1, None, 7) == 1 and f(64, 64, 64, 0, 31, 1, 1, buf, -1) == 1
+    assert f(64, 64, 64, 3, 31, 1, 1, buf, 7) == 2 and f(64, 64, 64, 0, 32, 1, 1, buf, 7) == 1
+    assert f(-1, 1, 1, 0, 31, 1, 1, buf, 7) == 1 and f(64, 64, 64, 0, 31, -1, 1, buf, 7) == 1
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 128, 256), (8192, 8192, 4096), (333, 1001, 777), (8200, 384, 4112), (1, 1, 1), (64, 64, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_backward_workspaces(M, N, K, dtype):
+    """Of one scale a row at least those of several and of none beside the copies that these take; an operand of its own
+    for each product of 16-bit types with one scale a row."""
+    def need(outputs, x, w):
+        return bnd._size_of("dora_matmul_backward_int8_scales_workspace_size", M, N, K, bnd._dtype_code(dtype), outputs, x, w)
+
+    for outputs in range(32):
+        whole = bnd.dora_matmul_backward_int8_workspace_size(M, N, K, dtype, outputs, bnd.HELD_X + bnd.HELD_W)
+        assert whole == need(outputs, 1, 1) == max(need(outputs, x, w) for x in (1, 5) for w in (1, 5))
+        for held in range(4):
+            x, w = held & 1, held >> 1
+            assert bnd.dora_matmul_backward_int8_workspace_size(M, N, K, dtype, outputs, held) == need(outputs, x, w)
+    du = M * N * 2
+    alone = bnd.GRAD_DX + bnd.GRAD_DU + bnd.GRAD_ALIGNED
+    if dtype != "f32" and N % 8 == 0 and K > 0:
+        assert need(alone, 0, 1) - need(alone, 0, 5) >= du
+    sz = ctypes.c_size_t()
+    f = bnd.load().dora_matmul_backward_int8_scales_workspace_size
+    assert f(M, N, K, 0, 31, 1, 1, None) == 1 and f(M, N, K, 0, 31, 1, -1, ctypes.byref(sz)) == 1
