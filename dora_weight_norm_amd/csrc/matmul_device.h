@@ -591,7 +591,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   const int64_t n = n0 + wn * NB * 32 + col;
   const int nv = (int)(g.N - n < 8 ? g.N - n : 8);
   float cs[8], bs[8];
-  if constexpr (!B8) column_terms(g.ep, n, nv, cs, bs);   // (B8: a product of the backward, stored as it is)
+  if constexpr (!B8) column_terms(g.ep, n, nv, cs, bs);   // (B8: a product of the backward, stored as it is or times a row's scale)
   f32x16 acc[MB][NB];
 #pragma unroll
   for (int a = 0; a < MB; ++a)
@@ -883,6 +883,11 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = v[8 * i + e];
+        if (g.ep.row_scale) {   // (uniform)
+          const float rs = ok[i] ? g.ep.row_scale[m[i]] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] *= rs;
+        }
         if (ok[i]) store8<O>(static_cast<O*>(g.ep.y) + off[i], nv, o);
       }
     } else {

@@ -647,6 +647,13 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     }
     if (dw && N > 0 && K > 0) {
       g.a = p.fold_x ? ws + p.off_dum : d, g.lda = p.fold_x ? p.ldn : ldu;
+      // Without an activation or a row scale du is dy times a column's scale, which is a
+      // row's of dw: dy itself is the operand then, and the scale multiplies the sums,
+      // so that x's rounding is the only one of an operand. (Where dy has the layout,
+      // and is not du's place.)
+      if (p.x8 && !p.fold_x && act == 0 && row_scale == nullptr && col_scale != nullptr && dy != du && p.ldn == N &&
+          reinterpret_cast<uintptr_t>(dy) % 16 == 0)
+        g.a = dy, g.lda = N, g.ep.row_scale = col_scale;
       g.b = x, g.ldb = ldx, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
       g.ep.y = dw;
       if (p.x8_tile)

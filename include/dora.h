@@ -700,8 +700,10 @@ dora_status dora_matmul_backward_int8_plan_info(int64_t M, int64_t N, int64_t K,
  * The products' operands are of the storage type, so the values of x8 and w8
  * are rounded to it, as du is. Those of rows with one scale are not: in 16 bits
  * such a product's other operand is du times the scale's significand, rounded
- * once, and the integers times the scale's power of two are exact. Everything
- * else, the workspace and the errors are as there.
+ * once, and the integers times the scale's power of two are exact. And of x8 in
+ * groups with act none and no row_scale dw is col_scale times dy^T x, without
+ * du's rounding, where dy lies on a 16-byte boundary (and is not du), and N is a
+ * multiple of 8. Everything else, the workspace and the errors are as there.
  */
 dora_status dora_matmul_backward_int8(const void* dy, const void* u, const dora_int8_rows* u8, const void* x,
                                       const dora_int8_rows* x8, const void* w, const dora_int8_rows* w8, int dtype,

@@ -199,3 +199,56 @@ def test_rows_of_one_scale_off_the_grid_on_a_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(eager, want):
             assert torch.equal(a, b)
+
+
+# Rows in groups beside a dy that is an operand as it is: brought back, and read by tiles of 128 (in parts) and 256 rows.
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K,reads", [(8200, 384, 4112, "int8_rows"), (4096, 2048, 4096, "int8_rows"), (600, 504, 1000, "copy"),
+                                         (64, 1000, 128, "copy")])
+def test_without_an_activation_dy_is_the_operand(M, N, K, reads, dtype):
+    assert bnd.dora_matmul_backward_int8_plan_info(M, N, K, dtype, x_scales=9, w_scales=0)["dw"]["reads"] == reads
+    rng = np.random.default_rng(10)
+    dy, u, w = draw(rng, (M, N), dtype), rows_of(rng, (M, N), dtype, group=32), draw(rng, (N, K), dtype, K ** -0.5)
+    x, c, bias = rows_of(rng, (M, K), dtype, group=64), vec(rng, N, 0.2), vec(rng, N, 0.3, 0.0)
+    got = bnd.dora_matmul_backward_int8(dy, u, x, w, col_scale=c, bias=bias)
+    dw = (host(dy) * host(c)[None, :]).T @ values(x)
+    assert np.linalg.norm(host(got[1]) - dw) / np.linalg.norm(dw) <= 0.65 * HALF[dtype]
+    size = np.abs(host(dy) * host(c)[None, :]).T @ np.abs(values(x))
+    close(got[1], dw, rounded(dtype, dw, (HALF[dtype] * 1.01 + (M + 4) * EPS32) * size + TINY[dtype] * np.abs(host(c)).max()
+                              * np.abs(host(dy)).sum(0)[:, None]), "dw")
+    # off the boundary, and in du's place, du is the operand
+    for other in (off(dy), dy):
+        again = bnd.dora_matmul_backward_int8(other, u, x, w, col_scale=c, bias=bias)
+        assert torch.equal(again[0], got[0]) and torch.equal(again[4], got[4])
+        close(again[1], dw, rounded(dtype, dw, (HALF[dtype] * 2.02 + (M + 4) * EPS32) * size + 3 * TINY[dtype]
+                                    * (np.abs(host(dy)).sum(0)[:, None] + np.abs(values(x)).sum(0)[None, :])), "dw")
+    y, x8 = dy.clone(), bnd._Int8RowsArg(x.q.data_ptr(), x.scale.data_ptr(), 64)
+    need = bnd._size_of("dora_matmul_backward_int8_scales_workspace_size", M, N, K, bnd._dtype_code(dtype),
+                        bnd.GRAD_DW + bnd.GRAD_DU + bnd.GRAD_ALIGNED, -(-K // 64), 0)
+    ws, into = torch.empty(need + 16, device="cuda", dtype=torch.uint8), torch.empty_like(got[1])
+    back = host(bnd.dora_dequantize_rows(*u, dtype=torch.float32))
+    uu = torch.from_numpy(back).cuda().to(dy.dtype)
+    bnd._call("dora_matmul_backward_int8", y.data_ptr(), uu.data_ptr(), None, None, ctypes.byref(x8), None, None,
+              bnd._dtype_code(dtype), M, N, K, None, c.data_ptr(), None, 0, y.data_ptr(), None, into.data_ptr(), None, None,
+              ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(y, got[4])
+    close(into, dw, rounded(dtype, dw, (HALF[dtype] * 2.02 + (M + 4) * EPS32) * size + 3 * TINY[dtype]
+                            * (np.abs(host(dy)).sum(0)[:, None] + np.abs(values(x)).sum(0)[None, :])), "dw")
+
+
+@pytest.mark.parametrize("kw", [dict(act="relu"), dict(rows=True), dict()])
+def test_du_is_the_operand_elsewhere(kw):
+    """With an activation, a row scale, or no column scale (du is dy then)."""
+    rng = np.random.default_rng(11)
+    M, N, K = 300, 264, 520
+    dy, u, w = draw(rng, (M, N), "bf16"), draw(rng, (M, N), "bf16"), draw(rng, (N, K), "bf16")
+    x = rows_of(rng, (M, K), "bf16", group=64)
+    c = vec(rng, N, 0.2) if kw else None
+    rows = vec(rng, M, 0.4) if "rows" in kw else None
+    got = bnd.dora_matmul_backward_int8(dy, u, x, w, col_scale=c, act=kw.get("act", "none"), row_scale=rows)
+    if c is None:
+        assert torch.equal(got[4], dy)
+    du, xv = host(got[4]), values(x)
+    ref, size = du.T @ xv, np.abs(du).T @ np.abs(xv)
+    close(got[1], ref, rounded("bf16", ref, (HALF["bf16"] * 1.01 + (M + 4) * EPS32) * size), "dw")
