@@ -48,7 +48,7 @@ struct GemmArgs {
   const float* b_scale;
   int64_t b_groups;
   int b_shift;
-  bool b_folded;           // only the scales' powers of two (fold_exp): `a` holds the rest
+  bool b_folded;           // only the scales' powers of two (scale_parts.h): `a` holds the rest
   Epilogue ep;
 };
 

@@ -79,7 +79,7 @@ __device__ __forceinline__ void unpack_rows(const UnpackJob& a, const UnpackJob&
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       if (!p[i].ok) continue;
-      if (FOLD && (p[i].row < a.T ? a.folded : b.folded)) sc[i] = fold_power<T>(sc[i]);
+      if constexpr (FOLD) sc[i] = FoldBits<T>(p[i].row < a.T ? a.folded : b.folded)(sc[i]);
       float f[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) f[e] = (float)(int8_t)(w[i][e / 4] >> (8 * (e % 4))) * sc[i];

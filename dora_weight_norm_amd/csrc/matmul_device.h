@@ -551,13 +551,14 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void matmul_tile_kernel(GemmArgs g)
   // Element e of the stage's BBLK * 16 of this lane, into the unit; with the last
   // of 16 bytes the next stage's take their registers.
   float qf = 0.f;
+  const FoldBits<T> fold(B8 && g.b_folded);
   auto convert = [&](int unit, int e) __attribute__((always_inline)) {
     if constexpr (B8) {
       const int j = e / 16, b = e % 16;
       // (bytes that a later step takes are not to be picked out, and so waited for,
       // when they were only just asked for)
       if (b % 8 == 0) asm volatile("" : "+v"(qv[j]), "+v"(qs[j]));
-      if (b == 0 && g.b_folded) qs[j] = fold_power<T>(qs[j]);
+      if (b == 0) qs[j] = fold(qs[j]);
       const float f = (float)(int8_t)(qv[j][b / 4] >> (8 * (b % 4))) * qs[j];
       if (b % 2)
         qout[b % 8 / 2] = pack2<T>(qf, f);

@@ -34,7 +34,7 @@ struct SavedU {
 };
 
 // FOLD: beside du, or in its place, the operands of products whose other one is int8
-// rows with one scale a row: du times the scales' significands (fold_exp), of w's rows
+// rows with one scale a row: du times the scales' significands (scale_parts.h), of w's rows
 // for dx (du_n) and of x's for dw (du_m), rounded once, from which the rows' integers
 // then take no rounding of their own. Either may be null, and du too.
 template <typename T>
@@ -45,7 +45,7 @@ struct Folded {
   T* du_m;
 };
 
-template <typename T, bool U8, bool FOLD>
+template <typename T, bool U8, bool FOLD, bool KEEP>
 __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u, SavedU u8, const float* row_scale,
                                                          const float* col_scale, const float* bias, int act, int64_t M,
                                                          int64_t N, T* du, int64_t ldu, T* du2, Folded<T> fold,
@@ -77,8 +77,8 @@ __global__ __launch_bounds__(256) void matmul_bwd_kernel(const T* dy, const T* u
     for (int i = 0; i < U; ++i) {
       const int64_t m = m0 + i * step;
       if (m < M) {
-        // (du, which the products read next, is to stay in the caches)
-        r.y[i] = load_raw8<T, true>(dy + m * N + n, nv);
+        // (what the products read next, du or with KEEP dy, is to stay in the caches)
+        r.y[i] = load_raw8<T, !KEEP>(dy + m * N + n, nv);
         if constexpr (U8) {
           // (through the caches: 27.6 and 29.7 us at 4096 x 4096 with SiLU, sums included)
           load_row_bytes<8>(u8.q + m * N, n, N, r.q[i]);
@@ -566,6 +566,12 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
   // (without rows the workspace may be null: whether sums are wanted is not read off their address)
   const bool want_sums = dbias || dcol;
   float* sums = want_sums ? reinterpret_cast<float*>(ws + p.off_sum) : nullptr;
+  // Without an activation or a row scale du is dy times a column's scale, which is a
+  // row's of dw: dy itself is dw's operand then, and the scale multiplies the sums, so
+  // that the rounding of x's values is the only one of an operand. (Where dy has the
+  // layout, and is not du's place.)
+  const bool of_dy = p.direct && p.x8 && !p.fold_x && act == 0 && row_scale == nullptr && col_scale != nullptr && dy != du &&
+                     p.ldn == N && reinterpret_cast<uintptr_t>(dy) % 16 == 0;
   if (M > 0 && N > 0) {
     const int64_t strips = (N + 7) / 8;
     int64_t tx = up(strips, 64);
@@ -573,28 +579,30 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     const dim3 block((unsigned)tx, (unsigned)(256 / tx));
     const dim3 grid((unsigned)((strips + tx - 1) / tx), (unsigned)p.rows);
     const SavedU u8{held.u.q, held.u.scale, scales_of(N, held.u.group), group_shift(held.u.group)};
-#define DORA_BWD_F(T, U8, FOLD)                                                                                      \
-  hipLaunchKernelGGL((matmul_bwd_kernel<T, U8, FOLD>), grid, block, 0, st, static_cast<const T*>(dy),                \
+#define DORA_BWD_F(T, U8, FOLD, KEEP)                                                                                \
+  hipLaunchKernelGGL((matmul_bwd_kernel<T, U8, FOLD, KEEP>), grid, block, 0, st, static_cast<const T*>(dy),                \
                      static_cast<const T*>(u), u8, row_scale, col_scale, bias, act, M, N, reinterpret_cast<T*>(d),   \
                      p.ldn, static_cast<T*>(du2),                                                                    \
                      (Folded<T>{held.w.scale, p.fold_w ? reinterpret_cast<T*>(ws + p.off_dun) : nullptr,             \
                                 held.x.scale, p.fold_x ? reinterpret_cast<T*>(ws + p.off_dum) : nullptr}),           \
                      sums)
-#define DORA_BWD_U(T, FOLD)          \
+#define DORA_BWD_U(T, FOLD, KEEP)    \
   if (u8.q != nullptr)               \
-    DORA_BWD_F(T, true, FOLD);       \
+    DORA_BWD_F(T, true, FOLD, KEEP); \
   else                               \
-    DORA_BWD_F(T, false, FOLD)
+    DORA_BWD_F(T, false, FOLD, KEEP)
 #define DORA_BWD(T)                  \
   if (p.fold_w || p.fold_x) {        \
-    DORA_BWD_U(T, true);             \
+    DORA_BWD_U(T, true, false);      \
+  } else if (of_dy) {                \
+    DORA_BWD_U(T, false, true);      \
   } else {                           \
-    DORA_BWD_U(T, false);            \
+    DORA_BWD_U(T, false, false);     \
   }
     switch (dtype) {
       case 0: DORA_BWD(bf16_t) break;
       case 2: DORA_BWD(f16_t) break;
-      default: DORA_BWD_U(float, false); break;
+      default: DORA_BWD_U(float, false, false); break;
     }
 #undef DORA_BWD
 #undef DORA_BWD_U
@@ -647,13 +655,7 @@ hipError_t launch_matmul_backward(const MatmulBackwardPlan& p, const void* dy, c
     }
     if (dw && N > 0 && K > 0) {
       g.a = p.fold_x ? ws + p.off_dum : d, g.lda = p.fold_x ? p.ldn : ldu;
-      // Without an activation or a row scale du is dy times a column's scale, which is a
-      // row's of dw: dy itself is the operand then, and the scale multiplies the sums,
-      // so that x's rounding is the only one of an operand. (Where dy has the layout,
-      // and is not du's place.)
-      if (p.x8 && !p.fold_x && act == 0 && row_scale == nullptr && col_scale != nullptr && dy != du && p.ldn == N &&
-          reinterpret_cast<uintptr_t>(dy) % 16 == 0)
-        g.a = dy, g.lda = N, g.ep.row_scale = col_scale;
+      if (of_dy) g.a = dy, g.lda = N, g.ep.row_scale = col_scale;
       g.b = x, g.ldb = ldx, g.K = M, g.M = N, g.N = K, g.splits = p.splits_dw;
       g.ep.y = dw;
       if (p.x8_tile)
