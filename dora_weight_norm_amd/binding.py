@@ -891,8 +891,6 @@ def _layer_norm(x, weight, bias, eps, residual, h, mean, rstd, want_stats, strea
     else:
         pm, prs = _maybe(mean, "mean", (T,), f32, dev), _maybe(rstd, "rstd", (T,), f32, dev)
     if q_dtype is not None:
-        if q_dtype not in _Q8_CODE:
-            raise TypeError(f"q_dtype must be int8 or float8_e4m3fn, got {q_dtype}")
         q, pq = _out(q, "q", shape, q_dtype, dev, stream)
         scale, ps = _out(scale, "scale", (T,), f32, dev, stream)
     if want_y or y is not None:
@@ -920,6 +918,8 @@ def dora_layer_norm_quant(x, weight, bias, eps: float, q_dtype=torch.int8, resid
     float8_e4m3fn) and scale float32 [T], the row's largest |value| / 127 or / 448.
     Returns (q, scale, h, mean, rstd). y, if a buffer for it is given, receives
     the output in x's dtype as well."""
+    if q_dtype not in _Q8_CODE:   # (None too, which would leave q as it was)
+        raise TypeError(f"q_dtype must be int8 or float8_e4m3fn, got {q_dtype}")
     _, q, scale, h, mean, rstd = _layer_norm(x, weight, bias, eps, residual, h, mean, rstd, want_stats, stream, y=y,
                                              q=q, scale=scale, q_dtype=q_dtype, want_y=False)
     return q, scale, h, mean, rstd

@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 from dora_weight_norm_amd import binding as bnd
 
@@ -100,3 +101,9 @@ def test_backward_workspaces(M, N, K, dtype):
     sz = ctypes.c_size_t()
     f = bnd.load().dora_matmul_backward_int8_scales_workspace_size
     assert f(M, N, K, 0, 31, 1, 1, None) == 1 and f(M, N, K, 0, 31, 1, -1, ctypes.byref(sz)) == 1
+
+
+@pytest.mark.parametrize("q_dtype", [None, torch.uint8, torch.bfloat16, "int8"])
+def test_the_norms_8_bit_type_is_one_of_two(q_dtype):
+    with pytest.raises(TypeError, match="q_dtype"):
+        bnd.dora_layer_norm_quant(torch.zeros(4, 8), None, None, 1e-5, q_dtype=q_dtype, y=torch.zeros(4, 8))
