@@ -7,7 +7,7 @@ namespace dora {
 
 namespace {
 
-// scale = fold_power * fold_factor. An integer of 8 bits times the power is exact in T
+// scale = power (FoldBits) * fold_factor. An integer of 8 bits times the power is exact in T
 // and finite: it is between 2^-24 and 2^8 for fp16 (128 2^8 is in its range), 2^-126 and
 // 2^120 for bf16. So one scale a row, which runs along a product's depth, costs its rows
 // no rounding when the other operand holds the factor, whose own rounding takes it in.
